@@ -293,7 +293,7 @@ def _own(st):
             resid=torch.empty(m, d, device="cuda"), q=torch.empty(m, d, dtype=torch.int8, device="cuda"),
             sx=torch.empty(m, device="cuda"), val=torch.empty(m, d, dtype=BF16, device="cuda")))
         kind = dfssm.DFSSM_F32 if delta is not None and delta.dtype == F32 else dfssm.DFSSM_BF16
-        dfssm.dfssm_add_rmsnorm_q8(ptr(st["w"]), d, EPS, ptr(st["resid"]), ptr(delta), kind, m, ptr(out["resid"]),
+        dfssm.dfssm_add_rmsnorm_quant(ptr(st["w"]), d, EPS, ptr(st["resid"]), ptr(delta), kind, m, ptr(out["resid"]),
                                    ptr(out["q"]), ptr(out["sx"]), ptr(out["val"]), stream)
         return dict(resid=out["resid"], sx=out["sx"], val=out["val"])
     if op == "norm_bwd":
