@@ -10,7 +10,8 @@ The entry points keep the C names: ``dfssm_linear_plan``, ``dfssm_plan_destroy``
 ``dfssm_plan_check``, ``dfssm_plan_workspace_bytes``, ``dfssm_status_string``,
 ``dfssm_linear_fwd_noalloc``, ``dfssm_plan_set_test_hooks``, ``dfssm_embed_fwd``,
 ``dfssm_lm_head_fwd``, ``dfssm_ssm_workspace_bytes``, ``dfssm_ssm_step``,
-``dfssm_ssm_read_error``, ``dfssm_add_rmsnorm``.
+``dfssm_ssm_read_error``, ``dfssm_add_rmsnorm``, ``dfssm_add_rmsnorm_quant``,
+``dfssm_add_rmsnorm_bwd_workspace_bytes``, ``dfssm_add_rmsnorm_bwd``.
 """
 from __future__ import annotations
 
@@ -44,6 +45,7 @@ EXPORTS = (
     "dfssm_linear_stack_fwd", "dfssm_plan_check", "dfssm_plan_workspace_bytes", "dfssm_status_string",
     "dfssm_linear_fwd_noalloc", "dfssm_plan_set_test_hooks", "dfssm_embed_fwd", "dfssm_lm_head_fwd",
     "dfssm_ssm_workspace_bytes", "dfssm_ssm_step", "dfssm_ssm_read_error", "dfssm_add_rmsnorm",
+    "dfssm_add_rmsnorm_quant", "dfssm_add_rmsnorm_bwd_workspace_bytes", "dfssm_add_rmsnorm_bwd",
 )
 DFSSM_DEVERR_TOKEN_ID = 0x10
 DFSSM_TEST_STALL = 0x1
@@ -119,6 +121,10 @@ def _load():
     lib.dfssm_ssm_step.argtypes = [ctypes.POINTER(SsmDims), vp, i32, i32, vp, ctypes.c_size_t, vp]
     lib.dfssm_ssm_read_error.argtypes = [vp, u32p, vp]
     lib.dfssm_add_rmsnorm.argtypes = [vp, i32, ctypes.c_float, vp, vp, i32, i32, vp, vp, i32, vp]
+    f32, sz = ctypes.c_float, ctypes.c_size_t
+    lib.dfssm_add_rmsnorm_quant.argtypes = [vp, i32, f32, vp, vp, i32, i32, vp, vp, vp, vp, vp]
+    lib.dfssm_add_rmsnorm_bwd_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(sz)]
+    lib.dfssm_add_rmsnorm_bwd.argtypes = [vp, i32, f32, vp, vp, i32, vp, i32, vp, vp, vp, sz, vp]
     lib.dfssm_status_string.restype = ctypes.c_char_p
     lib.dfssm_status_string.argtypes = [ctypes.c_int]
     for name in EXPORTS:
@@ -267,3 +273,26 @@ def dfssm_add_rmsnorm(norm_w_ptr: int, d: int, eps: float, resid_in_ptr: int, de
     """Residual add and RMS norm of the Mamba-2 block frame (see include/dfssm.h)."""
     _check(lib().dfssm_add_rmsnorm(norm_w_ptr, d, eps, resid_in_ptr, delta_ptr or None, delta_dtype, m,
                                    resid_out_ptr, out_ptr, out_dtype, stream), "dfssm_add_rmsnorm")
+
+
+def dfssm_add_rmsnorm_quant(norm_w_ptr: int, d: int, eps: float, resid_in_ptr: int, delta_ptr: int, delta_dtype: int,
+                         m: int, resid_out_ptr: int, q_ptr: int, sx_ptr: int, val_ptr: int = 0,
+                         stream: int = 0) -> None:
+    """Residual add and RMS norm with an int8 output and one scale per token (see include/dfssm.h)."""
+    _check(lib().dfssm_add_rmsnorm_quant(norm_w_ptr, d, eps, resid_in_ptr, delta_ptr or None, delta_dtype, m,
+                                      resid_out_ptr, q_ptr, sx_ptr, val_ptr or None, stream), "dfssm_add_rmsnorm_quant")
+
+
+def dfssm_add_rmsnorm_bwd_workspace_bytes(d: int, m: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().dfssm_add_rmsnorm_bwd_workspace_bytes(d, m, ctypes.byref(n)), "dfssm_add_rmsnorm_bwd_workspace_bytes")
+    return n.value
+
+
+def dfssm_add_rmsnorm_bwd(norm_w_ptr: int, d: int, eps: float, resid_ptr: int, dout_ptr: int, dout_dtype: int,
+                          dstream_ptr: int, m: int, dresid_ptr: int, dnorm_w_ptr: int, workspace_ptr: int = 0,
+                          workspace_bytes: int = 0, stream: int = 0) -> None:
+    """Gradient of the residual add and RMS norm (see include/dfssm.h)."""
+    _check(lib().dfssm_add_rmsnorm_bwd(norm_w_ptr, d, eps, resid_ptr, dout_ptr, dout_dtype, dstream_ptr or None, m,
+                                       dresid_ptr, dnorm_w_ptr or None, workspace_ptr or None, workspace_bytes,
+                                       stream), "dfssm_add_rmsnorm_bwd")

@@ -310,6 +310,38 @@ dfssm_status dfssm_add_rmsnorm(const float* norm_w, int32_t d, float eps, const 
                                const void* delta, int32_t delta_dtype, int32_t m, float* resid_out,
                                void* out, int32_t out_dtype, void* stream);
 
+/* ---- the block frame in 8 bits, and its gradient ---------------------------------------------
+ * dfssm_add_rmsnorm followed by the layer's quantiser (top of this file) in one pass: with
+ * r_new = resid_in + delta and o = r_new / sqrt(mean(r_new^2) + eps) * norm_w in fp32,
+ *   q, sx = the per-token absmax int8 quantisation of o (o is not rounded to bf16 first),
+ *   val   = bf16(sx q), if val is not NULL: the values that q stands for, as the operand of a
+ *           bf16 product (for instance the gradient of int8 weights).
+ * A token whose o holds an Inf or NaN gets a non-finite sx; its q and val are unspecified, the
+ * other tokens are not touched by it. Pointers, shapes, types and refusals as for
+ * dfssm_add_rmsnorm (resid_out may equal resid_in; delta may be NULL); q: m x d int8, sx: m
+ * fp32, val: m x d bf16 or NULL. One kernel on `stream`; allocates nothing. */
+dfssm_status dfssm_add_rmsnorm_quant(const float* norm_w, int32_t d, float eps, const float* resid_in,
+                                  const void* delta, int32_t delta_dtype, int32_t m, float* resid_out,
+                                  int8_t* q, float* sx, void* val, void* stream);
+
+/* The gradient of the block frame (dfssm_add_rmsnorm, and dfssm_add_rmsnorm_quant taken straight
+ * through its quantiser). resid: the forward call's resid_out (r, m x d fp32); dout: gradient
+ * with respect to the norm's output, m x d of dout_dtype (DFSSM_BF16 or DFSSM_F32); dstream:
+ * gradient that reaches resid_out from elsewhere (m x d fp32), or NULL:
+ *   f = 1/sqrt(mean(r^2) + eps);  g = dout norm_w;
+ *   dresid  = f g - f^3 (sum(g r)/d) r + dstream     (m x d fp32: the gradient of resid_in and
+ *                                                     of delta; may equal resid or dstream)
+ *   dnorm_w = sum over tokens of dout r f             (d fp32, or NULL: not computed)
+ * All in fp32, every sum in an order fixed by m and d. workspace: 16-byte aligned device
+ * memory of at least dfssm_add_rmsnorm_bwd_workspace_bytes (only read when dnorm_w is given; may
+ * be NULL otherwise); nothing in it is kept between calls, so calls that may overlap need one
+ * each. Shapes and refusals as for dfssm_add_rmsnorm. One kernel, and a second one for dnorm_w. */
+dfssm_status dfssm_add_rmsnorm_bwd_workspace_bytes(int32_t d, int32_t m, size_t* bytes);
+dfssm_status dfssm_add_rmsnorm_bwd(const float* norm_w, int32_t d, float eps, const float* resid,
+                                   const void* dout, int32_t dout_dtype, const float* dstream, int32_t m,
+                                   float* dresid, float* dnorm_w, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Test of the error path of the decode kernel (m <= 16 tokens), which must end with an
  * error status and never hang. With flags & DFSSM_TEST_STALL, the first CTA of that
  * kernel waits on a barrier that nothing arrives on: the wait gives up after
