@@ -11,7 +11,8 @@ The entry points keep the C names: ``dfssm_linear_plan``, ``dfssm_plan_destroy``
 ``dfssm_linear_fwd_noalloc``, ``dfssm_plan_set_test_hooks``, ``dfssm_embed_fwd``,
 ``dfssm_lm_head_fwd``, ``dfssm_ssm_workspace_bytes``, ``dfssm_ssm_step``,
 ``dfssm_ssm_read_error``, ``dfssm_add_rmsnorm``, ``dfssm_add_rmsnorm_quant``,
-``dfssm_add_rmsnorm_bwd_workspace_bytes``, ``dfssm_add_rmsnorm_bwd``.
+``dfssm_add_rmsnorm_bwd_workspace_bytes``, ``dfssm_add_rmsnorm_bwd``,
+``dfssm_xent_workspace_bytes``, ``dfssm_xent_fwd``, ``dfssm_xent_bwd``.
 """
 from __future__ import annotations
 
@@ -46,10 +47,12 @@ EXPORTS = (
     "dfssm_linear_fwd_noalloc", "dfssm_plan_set_test_hooks", "dfssm_embed_fwd", "dfssm_lm_head_fwd",
     "dfssm_ssm_workspace_bytes", "dfssm_ssm_step", "dfssm_ssm_read_error", "dfssm_add_rmsnorm",
     "dfssm_add_rmsnorm_quant", "dfssm_add_rmsnorm_bwd_workspace_bytes", "dfssm_add_rmsnorm_bwd",
+    "dfssm_xent_workspace_bytes", "dfssm_xent_fwd", "dfssm_xent_bwd",
 )
 DFSSM_DEVERR_TOKEN_ID = 0x10
 DFSSM_TEST_STALL = 0x1
 DFSSM_NOALLOC_MAX_M = 16
+DFSSM_IGNORE_TARGET = -100
 
 
 class DfssmError(RuntimeError):
@@ -125,6 +128,9 @@ def _load():
     lib.dfssm_add_rmsnorm_quant.argtypes = [vp, i32, f32, vp, vp, i32, i32, vp, vp, vp, vp, vp]
     lib.dfssm_add_rmsnorm_bwd_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(sz)]
     lib.dfssm_add_rmsnorm_bwd.argtypes = [vp, i32, f32, vp, vp, i32, vp, i32, vp, vp, vp, sz, vp]
+    lib.dfssm_xent_workspace_bytes.argtypes = [ctypes.POINTER(Int8Table), i32, i32, ctypes.POINTER(sz)]
+    lib.dfssm_xent_fwd.argtypes = [ctypes.POINTER(Int8Table), vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.dfssm_xent_bwd.argtypes = [ctypes.POINTER(Int8Table), vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]
     lib.dfssm_status_string.restype = ctypes.c_char_p
     lib.dfssm_status_string.argtypes = [ctypes.c_int]
     for name in EXPORTS:
@@ -296,3 +302,24 @@ def dfssm_add_rmsnorm_bwd(norm_w_ptr: int, d: int, eps: float, resid_ptr: int, d
     _check(lib().dfssm_add_rmsnorm_bwd(norm_w_ptr, d, eps, resid_ptr, dout_ptr, dout_dtype, dstream_ptr or None, m,
                                        dresid_ptr, dnorm_w_ptr or None, workspace_ptr or None, workspace_bytes,
                                        stream), "dfssm_add_rmsnorm_bwd")
+
+
+def dfssm_xent_workspace_bytes(table: Int8Table, m: int, backward: bool = False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().dfssm_xent_workspace_bytes(ctypes.byref(table), m, int(backward), ctypes.byref(n)),
+           "dfssm_xent_workspace_bytes")
+    return n.value
+
+
+def dfssm_xent_fwd(table: Int8Table, q_ptr: int, sx_ptr: int, targets_ptr: int, m: int, nll_ptr: int, lse_ptr: int,
+                   workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> None:
+    """Softmax cross entropy of m tokens over the int8 table (see include/dfssm.h)."""
+    _check(lib().dfssm_xent_fwd(ctypes.byref(table), q_ptr, sx_ptr, targets_ptr, m, nll_ptr, lse_ptr, workspace_ptr,
+                                workspace_bytes, stream), "dfssm_xent_fwd")
+
+
+def dfssm_xent_bwd(table: Int8Table, q_ptr: int, sx_ptr: int, targets_ptr: int, lse_ptr: int, grad_ptr: int, m: int,
+                   dh_ptr: int, workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> None:
+    """Gradient of the cross entropy with respect to the hidden state (see include/dfssm.h)."""
+    _check(lib().dfssm_xent_bwd(ctypes.byref(table), q_ptr, sx_ptr, targets_ptr, lse_ptr, grad_ptr, m, dh_ptr,
+                                workspace_ptr, workspace_bytes, stream), "dfssm_xent_bwd")

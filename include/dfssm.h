@@ -342,6 +342,41 @@ dfssm_status dfssm_add_rmsnorm_bwd(const float* norm_w, int32_t d, float eps, co
                                    float* dresid, float* dnorm_w, void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* ---- softmax cross entropy over the int8 table ----------------------------------------------------
+ * The loss of the next token over the whole vocabulary, and its gradient, for any number of tokens
+ * and without keeping the m x vocab logits. The hidden state comes in the layer's int8 form, as
+ * dfssm_add_rmsnorm_quant leaves it:
+ *   l[t, v] = sx[t] * scale[v] * sum_j table[v, j] q[t, j]      (the sum exact, in int32)
+ *   lse[t]  = log sum_v exp(l[t, v]);   nll[t] = lse[t] - l[t, targets[t]]
+ * q: m x d int8 (device, 16-byte aligned); sx, nll, lse: m fp32; targets: m int32 (4-byte aligned);
+ * table: HOST struct of device pointers as for dfssm_lm_head_fwd; 1 <= m <= 65536.
+ * A target of DFSSM_IGNORE_TARGET gives nll 0 (lse is written); any other target outside [0, vocab)
+ * is treated the same and sets DFSSM_DEVERR_TOKEN_ID in the workspace's error word. A non-finite sx
+ * or scale makes nll and lse of the tokens it reaches NaN and leaves the other tokens alone.
+ *
+ * workspace: 256-byte aligned device memory of at least dfssm_xent_workspace_bytes (backward: 0 for
+ * _fwd, 1 for _bwd), zeroed once before its first use. Its first 4 bytes are a device error word
+ * (DFSSM_DEVERR_TOKEN_ID, DFSSM_DEVERR_TIMEOUT), read and cleared by dfssm_ssm_read_error; nothing else
+ * is kept between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call
+ * on a device sets kernel attributes (make it before any stream capture). Results repeat bit for bit. */
+#define DFSSM_IGNORE_TARGET (-100)
+dfssm_status dfssm_xent_workspace_bytes(const dfssm_int8_table* table, int32_t m, int32_t backward,
+                                        size_t* bytes);
+dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8_t* q, const float* sx,
+                            const int32_t* targets, int32_t m, float* nll, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* The gradient of sum_t grad[t] nll[t] with respect to the hidden state that q and sx stand for
+ * (straight through the quantiser):
+ *   dh[t] = grad[t] * ( sum_v exp(l[t, v] - lse[t]) scale[v] table[v] - scale[target] table[target] )
+ * lse: the forward call's (m fp32); grad: m fp32; dh: m x d bf16 (device, 16-byte aligned). Tokens
+ * without a target (see above) get a row of zeros, whatever their sx, lse and grad hold. The
+ * probabilities are rounded to fp16 for the product with the table, the sums kept in fp32, the target's
+ * row taken off in fp32. */
+dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8_t* q, const float* sx,
+                            const int32_t* targets, const float* lse, const float* grad, int32_t m, void* dh,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* Test of the error path of the decode kernel (m <= 16 tokens), which must end with an
  * error status and never hang. With flags & DFSSM_TEST_STALL, the first CTA of that
  * kernel waits on a barrier that nothing arrives on: the wait gives up after

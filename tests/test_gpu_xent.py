@@ -1,0 +1,223 @@
+"""Cross entropy over the int8 table and its gradient on the GPU against 64 bits.
+
+Tolerances, with L the largest |logit| of the token:
+* A logit is an exact integer, converted (half a step, 2^-24) and multiplied three times (by the
+  scale, by s_x log2 e, itself rounded): 4 2^-24 relative, so any softmax average of logits is off
+  by at most 4 2^-24 L. exp2f is within 2 ulp (2^-22) and the arguments' subtraction within 2^-24 of
+  at most 2 L log2 e. The sum over a half tile adds at most 32 + 12 roundings, the joins at most
+  3 (2 ceil(V/256)/32 + 6), each 2^-24 relative; log2f 1 ulp, two more operations on lse. In all
+    |d lse| <= 2^-24 (8 L + 4 |lse| + 64 + 3 (V/4096 + 8)),
+  and nll adds the target's logit (4 2^-24 L) and one subtraction.
+* dh: the probabilities carry the errors above as relative errors, d_p = 2^-24 (16 L + 8 |lse| + 80),
+  are rounded to fp16 (2^-11; below its normal range by at most 2^-38 max|s|, 2^-25 over K), and the
+  fp32 accumulator takes V/16 steps of at most 2^-23 each of the sum of magnitudes S = sum p |s E|;
+  the splits add at most 148 2^-24 S. The target's row and the products with grad: 2^-22. The output's
+  bf16 rounding: 2^-8 |dh|.
+"""
+import pytest
+import torch
+
+import bit_gemv_gemm_dfssm_b200 as dfssm
+
+pytestmark = pytest.mark.gpu
+IGNORE = dfssm.DFSSM_IGNORE_TARGET
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def inputs(seed, m, v, d, ignored=0.2):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    table = torch.randint(-128, 128, (v, d), device="cuda", generator=g, dtype=torch.int8)
+    scale = torch.rand(v, device="cuda", generator=g) * 9e-4 + 1e-4
+    h = torch.randn(m, d, device="cuda", generator=g)
+    amax = h.abs().amax(1)
+    q = (h * (127 / amax)[:, None]).round().to(torch.int8)
+    # small widths get larger activations, so that the logits spread
+    sx = amax / 127 * (2048 / d) ** 0.5
+    tg = torch.randint(0, v, (m,), device="cuda", generator=g, dtype=torch.int32)
+    tg[torch.rand(m, device="cuda", generator=g) < ignored] = IGNORE
+    grad = torch.rand(m, device="cuda", generator=g) + 0.5
+    return dict(table=table, scale=scale, q=q, sx=sx, tg=tg, grad=grad)
+
+
+def ctable(a):
+    v, d = a["table"].shape
+    return dfssm.Int8Table(a["table"].data_ptr(), a["scale"].data_ptr(), v, d)
+
+
+def workspace(a, backward, fill=0):
+    n = dfssm.dfssm_xent_workspace_bytes(ctable(a), a["q"].shape[0], backward)
+    ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    return ws
+
+
+def fwd(a, ws=None):
+    m = a["q"].shape[0]
+    ws = workspace(a, False, 255) if ws is None else ws
+    nll = torch.full((m,), float("nan"), device="cuda")
+    lse = torch.full((m,), float("nan"), device="cuda")
+    dfssm.dfssm_xent_fwd(ctable(a), a["q"].data_ptr(), a["sx"].data_ptr(), a["tg"].data_ptr(), m, nll.data_ptr(),
+                         lse.data_ptr(), ws.data_ptr(), ws.numel(), stream())
+    return nll, lse, ws
+
+
+def bwd(a, lse, ws=None):
+    m, d = a["q"].shape
+    ws = workspace(a, True, 255) if ws is None else ws
+    dh = torch.full((m, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dfssm.dfssm_xent_bwd(ctable(a), a["q"].data_ptr(), a["sx"].data_ptr(), a["tg"].data_ptr(), lse.data_ptr(),
+                         a["grad"].data_ptr(), m, dh.data_ptr(), ws.data_ptr(), ws.numel(), stream())
+    return dh, ws
+
+
+def logits64(a):
+    return (a["q"].double() @ a["table"].double().T) * a["sx"].double()[:, None] * a["scale"].double()[None, :]
+
+
+def check(a, nll, lse, dh=None):
+    m, d = a["q"].shape
+    v = a["scale"].numel()
+    lg = logits64(a)
+    top = lg.abs().amax(1)
+    want = torch.logsumexp(lg, 1)
+    room = 2.0 ** -24 * (8 * top + 4 * want.abs() + 64 + 3 * (v / 4096 + 8))
+    assert ((lse.double() - want).abs() <= room).all()
+    on = a["tg"] >= 0
+    t0 = a["tg"].clamp(min=0).long()
+    hit = lg.gather(1, t0[:, None])[:, 0]
+    wn = torch.where(on, want - hit, torch.zeros_like(want))
+    assert ((nll.double() - wn).abs() <= room + 2.0 ** -24 * (4 * top + wn.abs())).all()
+    assert (nll[~on] == 0).all()
+    if dh is None:
+        return
+    p = torch.exp(lg - lse.double()[:, None])
+    e, s = a["table"].double(), a["scale"].double()
+    hot = e[t0] * s[t0][:, None]
+    gr = torch.where(on, a["grad"].double(), torch.zeros_like(want))[:, None]
+    wd = ((p * s) @ e - hot) * gr
+    mag = (p * s) @ e.abs()
+    dp = 2.0 ** -24 * (16 * top + 8 * want.abs() + 80)[:, None]
+    room = 2.0 ** -8 * wd.abs() + gr * (mag * (dp + 2.0 ** -11 + 2.0 ** -23 * (v / 16 + 148)) + 2.0 ** -22 * hot.abs()
+                                       + 2.0 ** -38 * s.max() * 128 * v)
+    assert ((dh.double() - wd).abs() <= room).all()
+    assert (dh[~on] == 0).all()
+
+
+@pytest.mark.parametrize("m,v,d", [(1, 1000, 256), (3, 1, 16), (2, 300, 16), (5, 128, 144), (128, 256, 128),
+                                   (130, 257, 272), (129, 513, 2048), (257, 5000, 400), (64, 2049, 8192),
+                                   (2300, 700, 64), (1, 50288, 2048), (16, 50288, 2048)])
+def test_parity(m, v, d):
+    a = inputs(m * 7 + v + d, m, v, d)
+    nll, lse, ws = fwd(a)
+    dh, ws2 = bwd(a, lse)
+    torch.cuda.synchronize()
+    check(a, nll, lse, dh)
+    for w in (ws, ws2):
+        assert dfssm.dfssm_ssm_read_error(w.data_ptr(), stream()) == (dfssm.DFSSM_OK, 0)
+
+
+def test_vocabulary_in_pieces_and_repeatable():
+    a = inputs(77, 2048, 50288, 256, 0.1)
+    nll, lse, ws = fwd(a)
+    dh, ws2 = bwd(a, lse)
+    torch.cuda.synchronize()
+    check(a, nll, lse, dh)
+    nll2, lse2, _ = fwd(a, ws)
+    dh2, _ = bwd(a, lse2, ws2)
+    torch.cuda.synchronize()
+    assert torch.equal(nll, nll2) and torch.equal(lse, lse2) and torch.equal(dh, dh2)
+
+
+def test_peaked_and_flat_rows():
+    """One logit far above the others (probability 1), a row of zeros (uniform), a negative scale."""
+    a = inputs(5, 6, 700, 512, 0.0)
+    a["scale"][3] = -a["scale"][3]
+    a["sx"][0] *= 300.0                       # logits in the hundreds: all probability on one row
+    a["q"][1] = 0                             # all logits 0
+    a["sx"][2] = 0.0
+    nll, lse, _ = fwd(a)
+    dh, _ = bwd(a, lse)
+    torch.cuda.synchronize()
+    check(a, nll, lse, dh)
+
+
+def test_targets_outside_the_vocabulary_are_ignored_and_reported():
+    a = inputs(9, 40, 900, 256, 0.0)
+    good = {k: v.clone() for k, v in a.items()}
+    for i, bad in ((3, 900), (7, -1), (20, 2 ** 31 - 1), (21, -2 ** 31)):
+        a["tg"][i] = bad
+        good["tg"][i] = IGNORE
+    nll, lse, ws = fwd(a)
+    dh, ws2 = bwd(a, lse)
+    torch.cuda.synchronize()
+    check(good, nll, lse, dh)
+    for w in (ws, ws2):
+        assert dfssm.dfssm_ssm_read_error(w.data_ptr(), stream()) == (dfssm.DFSSM_ERR_DEVICE_CHECK,
+                                                                     dfssm.DFSSM_DEVERR_TOKEN_ID)
+        assert dfssm.dfssm_ssm_read_error(w.data_ptr(), stream()) == (dfssm.DFSSM_OK, 0)
+
+
+def test_rows_that_are_not_finite_leave_the_others_alone():
+    a = inputs(10, 140, 900, 256, 0.0)
+    nll, lse, _ = fwd(a)
+    dh, _ = bwd(a, lse)
+    b = {k: v.clone() for k, v in a.items()}
+    b["sx"][5], b["sx"][130] = float("nan"), float("inf")
+    b["tg"][6], b["sx"][6], b["grad"][6] = IGNORE, float("nan"), float("nan")
+    nll2, lse2, _ = fwd(b)
+    dh2, _ = bwd(b, lse2)
+    torch.cuda.synchronize()
+    assert not torch.isfinite(nll2[5]) and not torch.isfinite(nll2[130])
+    assert nll2[6] == 0 and (dh2[6] == 0).all()
+    rest = torch.ones(140, dtype=torch.bool, device="cuda")
+    rest[[5, 6, 130]] = False
+    assert torch.equal(nll[rest], nll2[rest]) and torch.equal(lse[rest], lse2[rest]) and torch.equal(dh[rest], dh2[rest])
+
+
+def test_gradient_against_differences():
+    a = inputs(11, 6, 400, 96, 0.0)
+    nll, lse, _ = fwd(a)
+    dh, _ = bwd(a, lse)
+    torch.cuda.synchronize()
+    h = a["q"].double() * a["sx"].double()[:, None]
+    es = a["table"].double() * a["scale"].double()[:, None]
+    t0 = a["tg"].long()
+
+    def loss(x):
+        lg = x @ es.T
+        return ((torch.logsumexp(lg, 1) - lg.gather(1, t0[:, None])[:, 0]) * a["grad"].double()).sum()
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for _ in range(4):
+        u = torch.randn(h.shape, device="cuda", generator=g, dtype=torch.float64)
+        step = 1e-5
+        slope = (loss(h + step * u) - loss(h - step * u)) / (2 * step)
+        # dh's rounding (2^-8 of each entry, 2^-11 of the probabilities before it) and lse's in fp32
+        assert abs((dh.double() * u).sum() - slope) <= 2.0 ** -7 * (dh.double() * u).abs().sum()
+
+
+def test_on_another_stream_and_in_a_graph():
+    a = inputs(12, 200, 3000, 512)
+    nll, lse, ws = fwd(a)
+    dh, ws2 = bwd(a, lse)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        n2, l2, _ = fwd(a, ws)
+        d2, _ = bwd(a, l2, ws2)
+    s.synchronize()
+    assert torch.equal(nll, n2) and torch.equal(lse, l2) and torch.equal(dh, d2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        n3, l3, _ = fwd(a, ws)
+        d3, _ = bwd(a, l3, ws2)
+    other = inputs(13, 200, 3000, 512)
+    for k in ("q", "sx", "tg", "grad", "table", "scale"):
+        a[k].copy_(other[k])
+    graph.replay()
+    torch.cuda.synchronize()
+    check(a, n3, l3, d3)

@@ -40,3 +40,40 @@ def test_norm_bwd_refusals():
                 dict(eps=float("inf")), dict(kind=dfssm.DFSSM_I8)):
         assert call(**bad) == ARG, bad
     assert lib.dfssm_add_rmsnorm_bwd_workspace_bytes(2048, 9, None) == ARG
+
+
+def test_xent_refusals():
+    lib = dfssm.lib()
+
+    def table(**kw):
+        a = dict(table=A, scale=A, vocab=1000, d=256)
+        a.update(kw)
+        return dfssm.Int8Table(a["table"], a["scale"], a["vocab"], a["d"])
+
+    size = {b: dfssm.dfssm_xent_workspace_bytes(table(), 5, b) for b in (False, True)}
+
+    def fwd(t=None, **kw):
+        a = dict(q=A, sx=A, tg=A, m=5, nll=A, lse=A, ws=A, n=size[False])
+        a.update(kw)
+        return lib.dfssm_xent_fwd(t or table(), a["q"], a["sx"], a["tg"], a["m"], a["nll"], a["lse"], a["ws"], a["n"],
+                                  None)
+
+    def bwd(t=None, **kw):
+        a = dict(q=A, sx=A, tg=A, lse=A, grad=A, m=5, dh=A, ws=A, n=size[True])
+        a.update(kw)
+        return lib.dfssm_xent_bwd(t or table(), a["q"], a["sx"], a["tg"], a["lse"], a["grad"], a["m"], a["dh"], a["ws"],
+                                  a["n"], None)
+
+    for call in (fwd, bwd):
+        for bad in (dict(d=8), dict(d=264), dict(d=8208), dict(vocab=0), dict(vocab=(1 << 24) + 1)):
+            assert call(table(**bad)) == SHAPE, bad
+        for bad in (dict(table=None), dict(scale=None), dict(table=A + 8), dict(scale=A + 4)):
+            assert call(table(**bad)) == ARG, bad
+        for m in (0, -3, 65537):
+            assert call(m=m) == SHAPE
+        for bad in (dict(q=None), dict(q=A + 8), dict(sx=None), dict(sx=A + 2), dict(tg=None), dict(tg=A + 1),
+                    dict(lse=None), dict(ws=None), dict(ws=A + 16), dict(n=0)):
+            assert call(**bad) == ARG, bad
+    assert fwd(n=size[False] - 1) == ARG and fwd(nll=None) == ARG
+    assert bwd(n=size[True] - 1) == ARG and bwd(dh=None) == ARG and bwd(dh=A + 8) == ARG and bwd(grad=None) == ARG
+    assert lib.dfssm_xent_workspace_bytes(table(), 5, 0, None) == ARG
