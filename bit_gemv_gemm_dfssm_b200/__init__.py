@@ -12,7 +12,8 @@ The entry points keep the C names: ``dfssm_linear_plan``, ``dfssm_plan_destroy``
 ``dfssm_lm_head_fwd``, ``dfssm_ssm_workspace_bytes``, ``dfssm_ssm_step``,
 ``dfssm_ssm_read_error``, ``dfssm_add_rmsnorm``, ``dfssm_add_rmsnorm_quant``,
 ``dfssm_add_rmsnorm_bwd_workspace_bytes``, ``dfssm_add_rmsnorm_bwd``,
-``dfssm_xent_workspace_bytes``, ``dfssm_xent_fwd``, ``dfssm_xent_bwd``.
+``dfssm_xent_workspace_bytes``, ``dfssm_xent_fwd``, ``dfssm_xent_bwd``, ``dfssm_ssm_scan_workspace_bytes``,
+``dfssm_ssm_scan_fwd``, ``dfssm_ssm_scan_bwd``.
 """
 from __future__ import annotations
 
@@ -48,8 +49,10 @@ EXPORTS = (
     "dfssm_ssm_workspace_bytes", "dfssm_ssm_step", "dfssm_ssm_read_error", "dfssm_add_rmsnorm",
     "dfssm_add_rmsnorm_quant", "dfssm_add_rmsnorm_bwd_workspace_bytes", "dfssm_add_rmsnorm_bwd",
     "dfssm_xent_workspace_bytes", "dfssm_xent_fwd", "dfssm_xent_bwd",
+    "dfssm_ssm_scan_workspace_bytes", "dfssm_ssm_scan_fwd", "dfssm_ssm_scan_bwd",
 )
 DFSSM_DEVERR_TOKEN_ID = 0x10
+DFSSM_DEVERR_SEQLENS = 0x20
 DFSSM_TEST_STALL = 0x1
 DFSSM_NOALLOC_MAX_M = 16
 DFSSM_IGNORE_TARGET = -100
@@ -101,6 +104,26 @@ class SsmLayer(ctypes.Structure):
                 ("out", ctypes.c_void_p)]
 
 
+class ScanDims(ctypes.Structure):
+    _fields_ = [("nheads", ctypes.c_int32), ("ngroups", ctypes.c_int32), ("headdim", ctypes.c_int32),
+                ("d_state", ctypes.c_int32)]
+
+
+class ScanInputs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("b", ctypes.c_void_p),
+                ("b_stride", ctypes.c_int64), ("c", ctypes.c_void_p), ("c_stride", ctypes.c_int64),
+                ("dt", ctypes.c_void_p), ("dt_stride", ctypes.c_int64), ("dt_bias", ctypes.c_void_p),
+                ("a_log", ctypes.c_void_p), ("d_skip", ctypes.c_void_p), ("init_state", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p)]
+
+
+class ScanGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_int64), ("db", ctypes.c_void_p),
+                ("db_stride", ctypes.c_int64), ("dc", ctypes.c_void_p), ("dc_stride", ctypes.c_int64),
+                ("ddt", ctypes.c_void_p), ("ddt_stride", ctypes.c_int64), ("ddt_bias", ctypes.c_void_p),
+                ("da_log", ctypes.c_void_p), ("dd_skip", ctypes.c_void_p), ("dinit_state", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libdfssm.so is not built ({LIB_PATH}); run "
@@ -131,6 +154,10 @@ def _load():
     lib.dfssm_xent_workspace_bytes.argtypes = [ctypes.POINTER(Int8Table), i32, i32, ctypes.POINTER(sz)]
     lib.dfssm_xent_fwd.argtypes = [ctypes.POINTER(Int8Table), vp, vp, vp, i32, vp, vp, vp, sz, vp]
     lib.dfssm_xent_bwd.argtypes = [ctypes.POINTER(Int8Table), vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    i64, dims, ins = ctypes.c_int64, ctypes.POINTER(ScanDims), ctypes.POINTER(ScanInputs)
+    lib.dfssm_ssm_scan_workspace_bytes.argtypes = [dims, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.dfssm_ssm_scan_fwd.argtypes = [dims, ins, i32, i32, vp, i64, vp, vp, sz, vp]
+    lib.dfssm_ssm_scan_bwd.argtypes = [dims, ins, i32, i32, vp, i64, vp, ctypes.POINTER(ScanGrads), vp, sz, vp]
     lib.dfssm_status_string.restype = ctypes.c_char_p
     lib.dfssm_status_string.argtypes = [ctypes.c_int]
     for name in EXPORTS:
@@ -323,3 +350,27 @@ def dfssm_xent_bwd(table: Int8Table, q_ptr: int, sx_ptr: int, targets_ptr: int, 
     """Gradient of the cross entropy with respect to the hidden state (see include/dfssm.h)."""
     _check(lib().dfssm_xent_bwd(ctypes.byref(table), q_ptr, sx_ptr, targets_ptr, lse_ptr, grad_ptr, m, dh_ptr,
                                 workspace_ptr, workspace_bytes, stream), "dfssm_xent_bwd")
+
+
+def dfssm_ssm_scan_workspace_bytes(dims: ScanDims, total: int, nseq: int, backward: bool = False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().dfssm_ssm_scan_workspace_bytes(ctypes.byref(dims), total, nseq, int(backward), ctypes.byref(n)),
+           "dfssm_ssm_scan_workspace_bytes")
+    return n.value
+
+
+def dfssm_ssm_scan_fwd(dims: ScanDims, inputs: ScanInputs, total: int, nseq: int, y_ptr: int, y_stride: int,
+                       final_state_ptr: int, workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> None:
+    """The state recurrence over packed sequences (see include/dfssm.h)."""
+    _check(lib().dfssm_ssm_scan_fwd(ctypes.byref(dims), ctypes.byref(inputs), total, nseq, y_ptr, y_stride,
+                                    final_state_ptr or None, workspace_ptr, workspace_bytes, stream),
+           "dfssm_ssm_scan_fwd")
+
+
+def dfssm_ssm_scan_bwd(dims: ScanDims, inputs: ScanInputs, total: int, nseq: int, dy_ptr: int, dy_stride: int,
+                       dfinal_state_ptr: int, grads: ScanGrads, workspace_ptr: int, workspace_bytes: int,
+                       stream: int = 0) -> None:
+    """Gradient of the state recurrence over packed sequences (see include/dfssm.h)."""
+    _check(lib().dfssm_ssm_scan_bwd(ctypes.byref(dims), ctypes.byref(inputs), total, nseq, dy_ptr, dy_stride,
+                                    dfinal_state_ptr or None, ctypes.byref(grads), workspace_ptr, workspace_bytes,
+                                    stream), "dfssm_ssm_scan_bwd")

@@ -1,0 +1,611 @@
+// The state operations' recurrence over packed sequences of any length (dfssm_ssm_scan_fwd): what
+// ssm_step.cu does for one token, for the tokens of a prompt or a training batch.
+//
+// A CTA of 4 warps takes one head through one item (a sequence, or a segment of a long one), chunk by
+// chunk (ssm_scan.cuh has the formulas), with the head's 64 x 128 state in registers: warp w owns the
+// channels 16 w .. 16 w + 15, whose accumulator registers are at the same time the B fragments of the
+// state's readout. Per chunk, on bf16 warp MMAs with fp32 accumulation:
+//   G = C B^T (64 x 64, causal tiles only, warp w the rows 16 w ..), scaled to M = G exp(cum_t -
+//       cum_s) dt_s and stored as two bf16 parts (2^-17 of each value) for all warps;
+//   y = exp(cum_t) (C S^T) + M X + d_skip x, S as two bf16 parts: one rounding to bf16 at the end
+//       that counts;
+//   S = exp(cum_64) S + sum_s (w_s x_s) B_s^T, w_s x_s as three bf16 parts: the state, which
+//       goes on to the next tokens and is returned, keeps fp32's precision.
+// x, B and C are bf16 and enter exactly. The next chunk's tiles arrive by cp.async meanwhile.
+//
+// One CTA per (head, item) fills the GPU from about five sequences of 64 heads on; with fewer, sequences
+// longer than 1.25 times a CTA's fair share are cut into segments, whose start states come from two
+// small kernels before (each segment's own contribution, state MMAs only; then a carry over the
+// segments). Items are handed out longest first.
+#include <mutex>
+
+#include "ssm_scan.cuh"
+
+namespace dfssm {
+namespace scan {
+
+namespace {
+
+constexpr int kThreads = 128;
+
+// ------------------------------------------------------------------------------- the work table
+
+constexpr int kTableThreads = 1024;
+constexpr int kMaxSorted = 1024;
+
+// inclusive sum over the CTA; every thread gets its own and the total
+__device__ __forceinline__ int block_scan(int v, int* red, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = v;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int w = 0; w < kTableThreads / 32; ++w) {
+        if (w < warp) before += red[w];
+        total += red[w];
+    }
+    return v + before;
+}
+
+// One CTA: validates the offsets, cuts the sequences, numbers items and chunks. A sequence whose offsets
+// do not fit is left out (and reported).
+__global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a) {
+    __shared__ int red[kTableThreads / 32];
+    __shared__ int lens[kMaxSorted];
+    int n_items = 0, n_chunks = 0, n_slots = 0;
+    for (int s0 = 0; s0 < a.nseq; s0 += kTableThreads) {
+        const int s = s0 + threadIdx.x;
+        int t0 = 0, len = 0, nseg = 0, nch = 0;
+        if (s < a.nseq) {
+            t0 = a.cu[s];
+            const int t1 = a.cu[s + 1];
+            if (t0 < 0 || t1 < t0 || t1 > a.total) {
+                atomicOr(a.err, DFSSM_DEVERR_SEQLENS);
+            } else {
+                len = t1 - t0;
+                nseg = len <= a.seg_len ? 1 : (len + a.seg_len - 1) / a.seg_len;
+                nch = (len + kQ - 1) / kQ;
+            }
+        }
+        int ti = 0, tc = 0, ts = 0;
+        const int cut = nseg > 1 ? nseg : 0;
+        const int i1 = n_items + block_scan(nseg, red, ti);
+        const int c1 = n_chunks + block_scan(nch, red, tc);
+        const int s1 = n_slots + block_scan(cut, red, ts);
+        // overlapping offsets could ask for more than the workspace holds
+        const bool fits = i1 <= a.cap_items && c1 <= a.cap_chunks && s1 <= a.cap_slots;
+        if (s < a.nseq) {
+            const int i0 = i1 - nseg, c0 = c1 - nch;
+            a.seq_slots[s] = fits ? make_int2(s1 - cut, cut) : make_int2(0, 0);
+            if (!fits) {
+                atomicOr(a.err, DFSSM_DEVERR_SEQLENS);
+                for (int k = 0; k < nseg && i0 + k < a.cap_items; ++k) a.seq_items[i0 + k] = Item{s, 0, -1, 0, 0, 0};
+            } else {
+                for (int k = 0; k < nseg; ++k) {
+                    const int at = k * a.seg_len;
+                    a.seq_items[i0 + k] = Item{s, t0 + at, min(a.seg_len, len - at), c0 + at / kQ, s1 - cut + k,
+                                               (k == 0 ? kFirst : 0) | (k == nseg - 1 ? kLast : 0) | (nseg > 1 ? kCut : 0)};
+                }
+            }
+        }
+        n_items = min(n_items + ti, a.cap_items);
+        n_chunks = min(n_chunks + tc, a.cap_chunks);
+        n_slots = min(n_slots + ts, a.cap_slots);
+    }
+    __syncthreads();                    // the items of this CTA are visible to it
+    if (threadIdx.x == 0) {
+        a.count[0] = n_items;
+        a.count[1] = n_chunks;
+    }
+    const bool sorted = n_items <= kMaxSorted;
+    if (sorted)
+        for (int i = threadIdx.x; i < n_items; i += kTableThreads) lens[i] = a.seq_items[i].len;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_items; i += kTableThreads) {
+        int rank = i;
+        if (sorted) {
+            const int mine = lens[i];
+            rank = 0;
+            for (int j = 0; j < n_items; ++j) rank += lens[j] > mine || (lens[j] == mine && j < i);
+        }
+        a.items[rank] = a.seq_items[i];
+    }
+    for (int i = threadIdx.x >> 5; i < n_items; i += kTableThreads / 32) {
+        const Item it = a.seq_items[i];
+        for (int k = threadIdx.x & 31; kQ * k < it.len; k += 32)
+            a.chunks[it.chunk0 + k] = Chunk{it.t0 + kQ * k, min(kQ, it.len - kQ * k)};
+    }
+}
+
+// ------------------------------------------------------------------------------- forward
+
+struct FwdOut {
+    uint16_t* y;               // NULL in the backward pass's run
+    int64_t ldy;
+    float* final_state;        // or NULL
+    // backward pass: the state in front of every chunk, and dy_t . (y_t - d_skip x_t)
+    uint16_t* states;          // [chunks][H][2][64][128]
+    const uint16_t* dy;
+    int64_t lddy;
+    float* ydy;                // [total][H]
+};
+
+constexpr int kStage = 16384 + 16384 + 8192;          // C, B, X of one chunk
+constexpr int kFwdSmem = 2 * kStage + 2 * 8192 + 2 * (int)sizeof(Decay) + 4 * kQ * 4 + 128;
+
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const Args a, const FwdOut o) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
+    uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
+    const uint32_t s_m = base + 2 * kStage;           // M: high part, then low part
+    Decay* dec = reinterpret_cast<Decay*>(smem + 2 * kStage + 2 * 8192);
+    float* s_ydy = reinterpret_cast<float*>(dec + 2);  // [4][64]
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int h = blockIdx.x % a.nheads, g = h / a.per_group;
+    Item it;
+    if (!get_item(a, blockIdx.x / a.nheads, it) || it.len < 0) return;
+    const int n_ch = (it.len + kQ - 1) / kQ;
+
+    const uint16_t* x = a.x + (int64_t)h * kP;
+    const uint16_t* b = a.b + (int64_t)g * kN;
+    const uint16_t* c = a.c + (int64_t)g * kN;
+    auto fetch = [&](int k) {
+        if (k < n_ch) {
+            const int t0 = it.t0 + k * kQ, n = min(kQ, it.len - k * kQ);
+            const uint32_t st = base + (k & 1) * kStage;
+            load_tile<128, kThreads>(st, c, a.ldc, t0, n, tid);
+            load_tile<128, kThreads>(st + 16384, b, a.ldb, t0, n, tid);
+            load_tile<64, kThreads>(st + 32768, x, a.ldx, t0, n, tid);
+        }
+        ptx::cp_async_commit();
+    };
+    fetch(0);
+    const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e), skip = a.d_skip[h];
+    StateFrag S;
+    const int64_t sh = ((int64_t)it.seq * a.nheads + h) * kStateElems;
+    if (it.flags & kCut) state_load(S, a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems, w, lane);
+    else if (a.init) state_load(S, a.init + sh, w, lane);
+    else state_zero(S);
+    float raw0 = 0.0f, raw1 = 0.0f;
+    if (w == 0 && n_ch > 0) {
+        const int n = min(kQ, it.len);
+        raw0 = raw_dt(a, it.t0, n, h, 2 * lane);
+        raw1 = raw_dt(a, it.t0, n, h, 2 * lane + 1);
+        chunk_decay(dec[0], raw0, raw1, n, bias, a2, lane);
+    }
+    for (int k = 0; k < n_ch; ++k) {
+        const int t0 = it.t0 + k * kQ, n = min(kQ, it.len - k * kQ);
+        const uint32_t st = base + (k & 1) * kStage;
+        const uint32_t s_c = st, s_b = st + 16384, s_x = st + 32768;
+        const Decay& d = dec[k & 1];
+        // the next chunk's dt while this one is worked on
+        if (w == 0 && k + 1 < n_ch) {
+            const int n1 = min(kQ, it.len - (k + 1) * kQ);
+            raw0 = raw_dt(a, t0 + kQ, n1, h, 2 * lane);
+            raw1 = raw_dt(a, t0 + kQ, n1, h, 2 * lane + 1);
+        }
+        ptx::cp_async_wait<0>();
+        __syncthreads();                 // this chunk's tiles and decays are there; the last one's are free
+        fetch(k + 1);
+        if (BWD) state_store_split(S, o.states + ((int64_t)(it.chunk0 + k) * a.nheads + h) * 2 * kStateElems, w, lane);
+
+        // ---- M, rows 16 w + lane / 4 (+ 8)
+        {
+            float G[8][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) G[j][0] = G[j][1] = G[j][2] = G[j][3] = 0.0f;
+#pragma unroll 2
+            for (int kk = 0; kk < kN; kk += 16) {
+                uint32_t ca[4];
+                frag_a<256>(s_c, 16 * w, kk, lane, ca);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j > w) break;
+                    uint32_t bb[4];
+                    frag_b<256>(s_b, 16 * j, kk, lane, bb);
+                    mma(G[2 * j], ca, bb[0], bb[1]);
+                    mma(G[2 * j + 1], ca, bb[2], bb[3]);
+                }
+            }
+            const int r = 16 * w + (lane >> 2);
+            const float c0 = d.cum[r], c1 = d.cum[r + 8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j > 2 * w + 1) break;
+                const int s = 8 * j + 2 * (lane & 3);
+                const float2 cs = *reinterpret_cast<const float2*>(d.cum + s);
+                const float2 ds = *reinterpret_cast<const float2*>(d.dt + s);
+                float m[4];
+                m[0] = s <= r ? __fmul_rn(__fmul_rn(G[j][0], ds.x), exp2f(__fsub_rn(c0, cs.x))) : 0.0f;
+                m[1] = s + 1 <= r ? __fmul_rn(__fmul_rn(G[j][1], ds.y), exp2f(__fsub_rn(c0, cs.y))) : 0.0f;
+                m[2] = s <= r + 8 ? __fmul_rn(__fmul_rn(G[j][2], ds.x), exp2f(__fsub_rn(c1, cs.x))) : 0.0f;
+                m[3] = s + 1 <= r + 8 ? __fmul_rn(__fmul_rn(G[j][3], ds.y), exp2f(__fsub_rn(c1, cs.y))) : 0.0f;
+                uint32_t h0, l0, h1, l1;
+                split_bf16x2(m[0], m[1], h0, l0);
+                split_bf16x2(m[2], m[3], h1, l1);
+                const uint32_t p0 = tile128(s_m, r, j) + 4 * (lane & 3), p1 = tile128(s_m, r + 8, j) + 4 * (lane & 3);
+                ptx::sts32(p0, h0);
+                ptx::sts32(p1, h1);
+                ptx::sts32(p0 + 8192, l0);
+                ptx::sts32(p1 + 8192, l1);
+            }
+        }
+        __syncthreads();                 // M is there
+
+        // ---- y of the warp's 16 channels: readout of the state, then the chunk's own tokens
+        float y[4][2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) y[i][p][0] = y[i][p][1] = y[i][p][2] = y[i][p][3] = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            uint32_t hi[4], lo[4];       // [2 * channel tile + k half]
+            split_bf16x2(S.v[2 * kk][0], S.v[2 * kk][1], hi[0], lo[0]);
+            split_bf16x2(S.v[2 * kk + 1][0], S.v[2 * kk + 1][1], hi[1], lo[1]);
+            split_bf16x2(S.v[2 * kk][2], S.v[2 * kk][3], hi[2], lo[2]);
+            split_bf16x2(S.v[2 * kk + 1][2], S.v[2 * kk + 1][3], hi[3], lo[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t ca[4];
+                frag_a<256>(s_c, 16 * i, 16 * kk, lane, ca);
+                mma(y[i][0], ca, lo[0], lo[1]);
+                mma(y[i][1], ca, lo[2], lo[3]);
+                mma(y[i][0], ca, hi[0], hi[1]);
+                mma(y[i][1], ca, hi[2], hi[3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float e0 = d.done[16 * i + (lane >> 2)], e1 = d.done[16 * i + 8 + (lane >> 2)];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                y[i][p][0] = __fmul_rn(y[i][p][0], e0);
+                y[i][p][1] = __fmul_rn(y[i][p][1], e0);
+                y[i][p][2] = __fmul_rn(y[i][p][2], e1);
+                y[i][p][3] = __fmul_rn(y[i][p][3], e1);
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t xb[4];
+            frag_bt<128>(s_x, 16 * ks, 16 * w, lane, xb);
+#pragma unroll
+            for (int i = ks; i < 4; ++i) {
+                uint32_t mh[4], ml[4];
+                frag_a<128>(s_m, 16 * i, 16 * ks, lane, mh);
+                frag_a<128>(s_m + 8192, 16 * i, 16 * ks, lane, ml);
+                mma(y[i][0], ml, xb[0], xb[1]);
+                mma(y[i][1], ml, xb[2], xb[3]);
+                mma(y[i][0], mh, xb[0], xb[1]);
+                mma(y[i][1], mh, xb[2], xb[3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int t = 16 * i + 8 * hf + (lane >> 2);
+                float dot = 0.0f;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float y0 = y[i][p][2 * hf], y1 = y[i][p][2 * hf + 1];
+                    const int ch = 16 * w + 8 * p + 2 * (lane & 3);
+                    if (!BWD) {
+                        uint32_t xv;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv) : "r"(tile128(s_x, t, 2 * w + p) + 4 * (lane & 3)));
+                        if (t < n)
+                            *reinterpret_cast<uint32_t*>(o.y + (int64_t)(t0 + t) * o.ldy + h * kP + ch) =
+                                bf16x2_of(make_float2(__fmaf_rn(skip, bf16_lo(xv), y0), __fmaf_rn(skip, bf16_hi(xv), y1)));
+                    } else if (t < n) {
+                        const uint32_t dv =
+                            *reinterpret_cast<const uint32_t*>(o.dy + (int64_t)(t0 + t) * o.lddy + h * kP + ch);
+                        dot = __fmaf_rn(y0, bf16_lo(dv), dot);
+                        dot = __fmaf_rn(y1, bf16_hi(dv), dot);
+                    }
+                }
+                if (BWD) {
+                    dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, 1));
+                    dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, 2));
+                    if ((lane & 3) == 0) s_ydy[w * kQ + t] = dot;
+                }
+            }
+
+        // ---- the state at the chunk's end
+        state_update<true>(S, d.done[kQ - 1], s_x, s_b, d.left, d.dt, w, lane);
+        if (w == 0 && k + 1 < n_ch) chunk_decay(dec[(k + 1) & 1], raw0, raw1, min(kQ, it.len - (k + 1) * kQ), bias, a2, lane);
+        if (BWD) {
+            __syncthreads();
+            if (tid < n)
+                o.ydy[(int64_t)(t0 + tid) * a.nheads + h] = __fadd_rn(__fadd_rn(s_ydy[tid], s_ydy[kQ + tid]),
+                                                                     __fadd_rn(s_ydy[2 * kQ + tid], s_ydy[3 * kQ + tid]));
+        }
+    }
+    ptx::cp_async_wait<0>();
+    if (o.final_state && (it.flags & kLast)) state_store(S, o.final_state + sh, w, lane);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------------------- segments
+
+// Starts of the segments of cut sequences, from the segments' own contributions, in place.
+// CTA (sequence, head); reverse: from the last segment to the first.
+__global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const float* __restrict__ start, int reverse) {
+    const int h = blockIdx.x % a.nheads, s = blockIdx.x / a.nheads;
+    const int i0 = a.seq_slots[s].x, i1 = i0 + a.seq_slots[s].y;
+    if (i1 - i0 < 2) return;
+    float4 v[8];
+    const float4* src = reinterpret_cast<const float4*>(start + ((int64_t)s * a.nheads + h) * kStateElems);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = start ? src[threadIdx.x + 256 * k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = i0; i < i1; ++i) {
+        const int slot = reverse ? i0 + i1 - 1 - i : i;
+        float4* p = reinterpret_cast<float4*>(a.seg_state + ((int64_t)slot * a.nheads + h) * kStateElems);
+        const bool more = i + 1 < i1;
+        const float keep = more ? a.seg_decay[(int64_t)slot * a.nheads + h] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float4 own = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (more) own = p[threadIdx.x + 256 * k];
+            p[threadIdx.x + 256 * k] = v[k];
+            v[k] = make_float4(__fmaf_rn(keep, v[k].x, own.x), __fmaf_rn(keep, v[k].y, own.y),
+                               __fmaf_rn(keep, v[k].z, own.z), __fmaf_rn(keep, v[k].w, own.w));
+        }
+    }
+}
+
+// The state alone through an item: forward (u = x, v = B) or backward in time (u = dy, v = C: the state's
+// gradient). STORE: from its start, every chunk's end gradient to the workspace and the first one out;
+// otherwise from zero, the item's own contribution and decay.
+template <bool REV, bool STORE>
+__global__ void __launch_bounds__(kThreads, 3) scan_state_kernel(const Args a, const StateArgs o) {
+    constexpr int kSt = 16384 + 8192;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
+    uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
+    Decay* dec = reinterpret_cast<Decay*>(smem + 2 * kSt);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int h = blockIdx.x % a.nheads, g = h / a.per_group;
+    Item it;
+    if (!get_item(a, blockIdx.x / a.nheads, it) || it.len < 0) return;
+    if (!STORE && (!(it.flags & kCut) || (it.flags & (REV ? kFirst : kLast)))) return;     // nothing starts behind it
+    const int n_ch = (it.len + kQ - 1) / kQ;
+    const uint16_t* u = (REV ? o.u : a.x) + (int64_t)h * kP;
+    const uint16_t* v = (REV ? a.c : a.b) + (int64_t)g * kN;
+    const int64_t ldu = REV ? o.ldu : a.ldx, ldv = REV ? a.ldc : a.ldb;
+    auto chunk_of = [&](int k) { return REV ? n_ch - 1 - k : k; };
+    auto fetch = [&](int k) {
+        if (k < n_ch) {
+            const int q = chunk_of(k), t0 = it.t0 + q * kQ, n = min(kQ, it.len - q * kQ);
+            const uint32_t st = base + (k & 1) * kSt;
+            load_tile<128, kThreads>(st, v, ldv, t0, n, tid);
+            load_tile<64, kThreads>(st + 16384, u, ldu, t0, n, tid);
+        }
+        ptx::cp_async_commit();
+    };
+    fetch(0);
+    const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
+    StateFrag S;
+    const int64_t sh = ((int64_t)it.seq * a.nheads + h) * kStateElems;
+    if (STORE && (it.flags & kCut)) state_load(S, a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems, w, lane);
+    else if (STORE && o.start) state_load(S, o.start + sh, w, lane);
+    else state_zero(S);
+    float total = 0.0f;
+    auto decay = [&](int k) {
+        const int q = chunk_of(k), t0 = it.t0 + q * kQ, n = min(kQ, it.len - q * kQ);
+        chunk_decay(dec[k & 1], raw_dt(a, t0, n, h, 2 * lane), raw_dt(a, t0, n, h, 2 * lane + 1), n, bias, a2, lane);
+    };
+    if (w == 0 && n_ch > 0) decay(0);
+    for (int k = 0; k < n_ch; ++k) {
+        const uint32_t st = base + (k & 1) * kSt;
+        const Decay& d = dec[k & 1];
+        ptx::cp_async_wait<0>();
+        __syncthreads();
+        fetch(k + 1);
+        if (w == 0 && k + 1 < n_ch) decay(k + 1);
+        if (STORE)
+            state_store_split(S, o.states + ((int64_t)(it.chunk0 + chunk_of(k)) * a.nheads + h) * 2 * kStateElems, w, lane);
+        total = __fadd_rn(total, d.cum[kQ - 1]);
+        state_update<!REV>(S, d.done[kQ - 1], st + 16384, st, REV ? d.done : d.left, d.dt, w, lane);
+    }
+    ptx::cp_async_wait<0>();
+    if (!STORE) {
+        state_store(S, a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems, w, lane);
+        if (tid == 0) a.seg_decay[(int64_t)it.slot * a.nheads + h] = exp2f(total);
+    } else if (o.out && (it.flags & kFirst)) {
+        state_store(S, o.out + sh, w, lane);
+    }
+}
+constexpr int kStateSmem = 2 * (16384 + 8192) + 2 * (int)sizeof(Decay) + 128;
+
+// ------------------------------------------------------------------------------- host
+
+Plan make_plan(int nheads, int total, int nseq, bool backward) {
+    Plan p{};
+    // a CTA's fair share: two CTAs on each of 148 SMs; an item may be a quarter longer
+    int64_t share = ((int64_t)total * nheads + 295) / 296;
+    share += share / 4;
+    if (share < 512) share = 512;
+    p.seg_len = (int)((share + kQ - 1) / kQ * kQ);
+    if (p.seg_len > (total + kQ - 1) / kQ * kQ) p.seg_len = (total + kQ - 1) / kQ * kQ;
+    // small calls save the table's launch: every sequence is one item, in the order given
+    p.direct = !backward && total <= p.seg_len && total <= 4096;
+    p.cap_items = total / p.seg_len + nseq;
+    p.cap_chunks = total / kQ + nseq;
+    p.cap_slots = 2 * (total / p.seg_len) + 1;             // a cut sequence of n tokens has at most 2 n / seg_len segments
+    size_t o = 256;                                        // error word
+    p.count = o;       o += 256;
+    p.items = o;       o = up256(o + sizeof(Item) * (size_t)p.cap_items);
+    p.seq_items = o;   o = up256(o + sizeof(Item) * (size_t)p.cap_items);
+    p.seq_slots = o;   o = up256(o + sizeof(int2) * (size_t)nseq);
+    p.chunks = o;      o = up256(o + sizeof(Chunk) * (size_t)p.cap_chunks);
+    p.seg_decay = o;   o = up256(o + 4 * (size_t)p.cap_slots * nheads);
+    p.seg_state = o;
+    if (total > p.seg_len) o = up256(o + 4 * (size_t)p.cap_slots * nheads * kStateElems);
+    p.total = o;
+    return p;
+}
+
+Args make_args(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int total, int nseq, const Plan& p, uint8_t* ws) {
+    Args a{};
+    a.x = static_cast<const uint16_t*>(in->x);
+    a.b = static_cast<const uint16_t*>(in->b);
+    a.c = static_cast<const uint16_t*>(in->c);
+    a.dt = static_cast<const uint16_t*>(in->dt);
+    a.ldx = in->x_stride;
+    a.ldb = in->b_stride;
+    a.ldc = in->c_stride;
+    a.lddt = in->dt_stride;
+    a.dt_bias = in->dt_bias;
+    a.a_log = in->a_log;
+    a.d_skip = in->d_skip;
+    a.init = in->init_state;
+    a.cu = in->cu_seqlens;
+    a.nheads = dims->nheads;
+    a.per_group = dims->nheads / dims->ngroups;
+    a.total = total;
+    a.nseq = nseq;
+    a.seg_len = p.seg_len;
+    a.direct = p.direct;
+    a.cap_items = p.cap_items;
+    a.cap_chunks = p.cap_chunks;
+    a.cap_slots = p.cap_slots;
+    a.err = reinterpret_cast<uint32_t*>(ws);
+    a.count = reinterpret_cast<int32_t*>(ws + p.count);
+    a.items = reinterpret_cast<Item*>(ws + p.items);
+    a.seq_items = reinterpret_cast<Item*>(ws + p.seq_items);
+    a.seq_slots = reinterpret_cast<int2*>(ws + p.seq_slots);
+    a.chunks = reinterpret_cast<Chunk*>(ws + p.chunks);
+    a.seg_state = reinterpret_cast<float*>(ws + p.seg_state);
+    a.seg_decay = reinterpret_cast<float*>(ws + p.seg_decay);
+    return a;
+}
+
+dfssm_status check_dims(const dfssm_scan_dims* d, int total, int nseq) {
+    if (!d) return DFSSM_ERR_INVALID_ARG;
+    if (d->headdim != kP || d->d_state != kN) return DFSSM_ERR_UNSUPPORTED_SHAPE;
+    if (d->nheads < 1 || d->nheads > 1024 || d->ngroups < 1 || d->nheads % d->ngroups != 0)
+        return DFSSM_ERR_UNSUPPORTED_SHAPE;
+    if (total < 1 || total > (1 << 22) || nseq < 1 || nseq > 65536) return DFSSM_ERR_UNSUPPORTED_SHAPE;
+    return DFSSM_OK;
+}
+
+dfssm_status check_call(const dfssm_scan_dims* d, const dfssm_scan_inputs* in, int total, int nseq) {
+    const dfssm_status st = check_dims(d, total, nseq);
+    if (st != DFSSM_OK) return st;
+    if (!in) return DFSSM_ERR_INVALID_ARG;
+    const int64_t di = (int64_t)d->nheads * kP, gn = (int64_t)d->ngroups * kN, most = (int64_t)1 << 30;
+    const void* rows[3] = {in->x, in->b, in->c};
+    const int64_t ld[3] = {in->x_stride, in->b_stride, in->c_stride}, least[3] = {di, gn, gn};
+    for (int i = 0; i < 3; ++i)
+        if (!rows[i] || !al16(rows[i]) || ld[i] < least[i] || ld[i] % 8 != 0 || ld[i] > most) return DFSSM_ERR_INVALID_ARG;
+    if (!in->dt || (reinterpret_cast<uintptr_t>(in->dt) & 1u) || in->dt_stride < d->nheads || in->dt_stride > most)
+        return DFSSM_ERR_INVALID_ARG;
+    const void* words[4] = {in->dt_bias, in->a_log, in->d_skip, in->cu_seqlens};
+    for (const void* p : words)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return DFSSM_ERR_INVALID_ARG;
+    if (!al16(in->init_state)) return DFSSM_ERR_INVALID_ARG;
+    return DFSSM_OK;
+}
+
+namespace {
+bool g_ready[64];
+std::mutex g_mu;
+}  // namespace
+
+dfssm_status setup() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DFSSM_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_ready[dev]) {
+        const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        if (cudaFuncSetAttribute(scan_fwd_kernel<false>, at, kFwdSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(scan_fwd_kernel<true>, at, kFwdSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(scan_state_kernel<false, false>, at, kStateSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(scan_state_kernel<true, false>, at, kStateSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(scan_state_kernel<true, true>, at, kStateSmem) != cudaSuccess ||
+            setup_bwd() != cudaSuccess)
+            return DFSSM_ERR_CUDA;
+        g_ready[dev] = true;
+    }
+    return DFSSM_OK;
+}
+
+cudaError_t launch_table(const Args& a, cudaStream_t s) {
+    if (a.direct) return cudaSuccess;
+    scan_table_kernel<<<1, kTableThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_segment_starts(const Args& a, cudaStream_t s) {
+    if (a.total <= a.seg_len) return cudaSuccess;          // no sequence can be cut
+    scan_state_kernel<false, false><<<a.cap_items * a.nheads, kThreads, kStateSmem, s>>>(a, StateArgs{});
+    scan_carry_kernel<<<a.nseq * a.nheads, 256, 0, s>>>(a, a.init, 0);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_states_back(const Args& a, const StateArgs& o, cudaStream_t s) {
+    if (a.total > a.seg_len) {
+        scan_state_kernel<true, false><<<a.cap_items * a.nheads, kThreads, kStateSmem, s>>>(a, o);
+        scan_carry_kernel<<<a.nseq * a.nheads, 256, 0, s>>>(a, o.start, 1);
+    }
+    scan_state_kernel<true, true><<<a.cap_items * a.nheads, kThreads, kStateSmem, s>>>(a, o);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_states_forward(const Args& a, uint16_t* states, const uint16_t* dy, int64_t lddy, float* ydy,
+                                  cudaStream_t s) {
+    FwdOut o{};
+    o.states = states;
+    o.dy = dy;
+    o.lddy = lddy;
+    o.ydy = ydy;
+    scan_fwd_kernel<true><<<a.cap_items * a.nheads, kThreads, kFwdSmem, s>>>(a, o);
+    return cudaGetLastError();
+}
+
+}  // namespace scan
+}  // namespace dfssm
+
+using namespace dfssm;
+using namespace dfssm::scan;
+
+extern "C" dfssm_status dfssm_ssm_scan_workspace_bytes(const dfssm_scan_dims* dims, int32_t total, int32_t nseq,
+                                                       int32_t backward, size_t* bytes) {
+    const dfssm_status st = check_dims(dims, total, nseq);
+    if (st != DFSSM_OK) return st;
+    if (!bytes) return DFSSM_ERR_INVALID_ARG;
+    *bytes = backward ? bwd_workspace(dims, total, nseq) : make_plan(dims->nheads, total, nseq, false).total;
+    return DFSSM_OK;
+}
+
+extern "C" dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
+                                           int32_t nseq, void* y, int64_t y_stride, float* final_state, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+    dfssm_status st = check_call(dims, in, total, nseq);
+    if (st != DFSSM_OK) return st;
+    if (!y || !al16(y) || y_stride < (int64_t)dims->nheads * kP || y_stride % 8 != 0 || y_stride > ((int64_t)1 << 30) ||
+        !al16(final_state))
+        return DFSSM_ERR_INVALID_ARG;
+    const Plan p = make_plan(dims->nheads, total, nseq, false);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < p.total)
+        return DFSSM_ERR_INVALID_ARG;
+    if ((st = setup()) != DFSSM_OK) return st;
+    const Args a = make_args(dims, in, total, nseq, p, static_cast<uint8_t*>(workspace));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    FwdOut o{};
+    o.y = static_cast<uint16_t*>(y);
+    o.ldy = y_stride;
+    o.final_state = final_state;
+    if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, s) != cudaSuccess) return DFSSM_ERR_CUDA;
+    scan_fwd_kernel<false><<<(a.direct ? nseq : a.cap_items) * a.nheads, kThreads, kFwdSmem, s>>>(a, o);
+    return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
+}

@@ -1,0 +1,630 @@
+// Gradient of the state recurrence over packed sequences (dfssm_ssm_scan_bwd).
+//
+// With the state's gradient dS_t = dy_t C_t^T + exp(a_{t+1}) dS_{t+1} (dS_T + dfinal at the end):
+//   dx_t = dt_t dS_t B_t + d_skip dy_t;   dB_t = sum_h dt_t dS_t^T x_t;   dC_t = sum_h S_t^T dy_t
+//   d dt_t = x_t . dS_t B_t + A da_t,     da_t = <dS_t, exp(a_t) S_{t-1}>,  A = -exp(a_log)
+// For a chunk of 64 tokens with the state S in front of it and the gradient dS behind it (both from
+// sequential kernels, ssm_scan.cu, which leave one pair per chunk and head in the workspace as two
+// bf16 parts each), L[t, s] = exp(cum_t - cum_s) for s <= t:
+//   G = C B^T, Z = dy x^T;   M = G o L;   W = sum_h Z o L dt_s
+//   dx_s = dt_s (sum_t M[t, s] dy_t + exp(cum_64 - cum_s) dS B_s) + d_skip dy_s
+//   dB   = W^T C + sum_h dt_s exp(cum_64 - cum_s) x_s dS
+//   dC   = W B   + sum_h exp(cum_t) dy_t S
+// G is shared by the heads of a group and W, summed over them in registers, multiplies C and B once
+// per chunk, not once per head. da_t splits into what passes over token t:
+//   da_t = sum_{t' >= t} r_t' - sum_{s >= t} k_s + sum_s w_s + exp(cum_64) <dS, S>
+// with r_t = dy_t . (y_t - d_skip x_t) (from the forward kernel's run), k_s = dt_s x_s . dx'_s the
+// whole of token s's own contribution and w_s its part that leaves the chunk, both from the
+// accumulators of dx. Nothing is summed over more than a chunk before it is used.
+//
+// scan_grad_kernel: CTA (chunk, group, split of the group's heads), 8 warps, one head after another with the
+// next head's tiles on the way (cp.async), bf16 warp MMAs; fp32 operands (M, W, S, dS) as two bf16
+// parts (2^-17). Partial dB and dC of the splits and partial parameter sums per chunk are added in
+// order by two small kernels.
+#include "ssm_scan.cuh"
+
+namespace dfssm {
+namespace scan {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct GradArgs {
+    const uint16_t* dy;
+    int64_t lddy;
+    const uint16_t* s_in;      // [chunks][H][2][64][128] states in front of the chunks
+    const uint16_t* ds_out;    // the same: gradients behind them
+    const float* ydy;          // [total][H]
+    uint16_t* dx;
+    int64_t lddx;
+    uint16_t* ddt;
+    int64_t ldddt;
+    float* db_part;            // [splits][total][G 128]
+    float* dc_part;
+    float* sums;               // [chunks][H][4]: d dt_bias, d a_log, d d_skip
+    int splits, per_split;     // heads per CTA
+};
+
+// one head's tiles
+constexpr int kTx = 0, kTy = 8192, kTs = 16384, kTd = 16384 + 32768, kTile = 16384 + 2 * 32768;
+
+struct HeadVec {
+    Decay d;
+    float sig[kQ];             // d softplus
+    float r[kQ];
+    float k[4][kQ], wl[4][kQ]; // x . dx' of the four channel slices: whole, and the part that leaves the chunk
+    float skip[8];             // per warp: sum dy x
+    float dot[8];              // per warp: <dS, S>
+};
+constexpr int kGradSmem = 2 * 16384 + 2 * kTile + 2 * 8192 + 2 * (int)sizeof(HeadVec) + 128;
+
+// [64][128] bf16, contiguous in global memory, high then low part
+__device__ __forceinline__ void load_state_tiles(uint32_t dst, const uint16_t* src, int tid) {
+#pragma unroll
+    for (int i = tid; i < 2 * kP * 16; i += kThreads) {
+        const int part = i >> 10, row = (i >> 4) & 63, pc = i & 15;
+        ptx::cp_async16_s(tile256(dst + part * 16384, row, pc), src + part * kStateElems + row * kN + 8 * pc);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, const GradArgs o) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
+    uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
+    const uint32_t s_b = base, s_c = base + 16384, s_t = base + 32768, s_m = s_t + 2 * kTile;
+    HeadVec* vec = reinterpret_cast<HeadVec*>(smem + 32768 + 2 * kTile + 2 * 8192);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int ngroups = a.nheads / a.per_group;
+    const int sp = blockIdx.x % o.splits, g = blockIdx.x / o.splits % ngroups, ci = blockIdx.x / o.splits / ngroups;
+    if (ci >= a.count[1]) return;
+    const Chunk ch = a.chunks[ci];
+    const int t0 = ch.t0, n = ch.n;
+    const int h0 = g * a.per_group + sp * o.per_split;
+    const int h1 = min(h0 + o.per_split, (g + 1) * a.per_group);
+
+    auto fetch = [&](int h) {
+        if (h < h1) {
+            const uint32_t st = s_t + ((h - h0) & 1) * kTile;
+            load_tile<64, kThreads>(st + kTx, a.x + (int64_t)h * kP, a.ldx, t0, n, tid);
+            load_tile<64, kThreads>(st + kTy, o.dy + (int64_t)h * kP, o.lddy, t0, n, tid);
+            const int64_t at = ((int64_t)ci * a.nheads + h) * 2 * kStateElems;
+            load_state_tiles(st + kTs, o.s_in + at, tid);
+            load_state_tiles(st + kTd, o.ds_out + at, tid);
+        }
+        ptx::cp_async_commit();
+    };
+    auto vectors = [&](int h) {                   // one warp
+        HeadVec& v = vec[(h - h0) & 1];
+        const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
+        const float r0 = raw_dt(a, t0, n, h, 2 * lane), r1 = raw_dt(a, t0, n, h, 2 * lane + 1);
+        chunk_decay(v.d, r0, r1, n, bias, a2, lane);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const float x = __fadd_rn(i ? r1 : r0, bias);
+            v.sig[t] = x > 20.0f ? 1.0f : __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
+            v.r[t] = t < n ? o.ydy[(int64_t)(t0 + t) * a.nheads + h] : 0.0f;
+        }
+    };
+    load_tile<128, kThreads>(s_b, a.b + (int64_t)g * kN, a.ldb, t0, n, tid);
+    load_tile<128, kThreads>(s_c, a.c + (int64_t)g * kN, a.ldc, t0, n, tid);
+    fetch(h0);
+    if (w == 0) vectors(h0);
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+
+    // G^T: warp (ws, wt) has rows s = 16 ws .., columns t = 32 wt ..
+    const int ws = w & 3, wt = w >> 2;
+    float G[4][4], W[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) G[j][i] = W[j][i] = 0.0f;
+#pragma unroll 2
+    for (int kk = 0; kk < kN; kk += 16) {
+        uint32_t ba[4];
+        frag_a<256>(s_b, 16 * ws, kk, lane, ba);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (32 * wt + 16 * j < 16 * ws) continue;                 // t < s everywhere
+            uint32_t cb[4];
+            frag_b<256>(s_c, 32 * wt + 16 * j, kk, lane, cb);
+            mma(G[2 * j], ba, cb[0], cb[1]);
+            mma(G[2 * j + 1], ba, cb[2], cb[3]);
+        }
+    }
+    // dB rows s, dC rows t: 32 (w & 1) + 16 i .., columns 32 (w / 2) + 8 j ..
+    const int rw = 32 * (w & 1), cw = 32 * (w >> 1), pw = 16 * (w >> 1);
+    float dB[2][4][4], dC[2][4][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) dB[i][j][q] = dC[i][j][q] = 0.0f;
+
+    for (int h = h0; h < h1; ++h) {
+        const uint32_t st = s_t + ((h - h0) & 1) * kTile;
+        const uint32_t s_x = st + kTx, s_y = st + kTy, s_s = st + kTs, s_d = st + kTd;
+        HeadVec& v = vec[(h - h0) & 1];
+        const float skip = a.d_skip[h];
+        ptx::cp_async_wait<0>();
+        __syncthreads();                          // this head's tiles and vectors are there, the last one's are free
+        fetch(h + 1);
+
+        // ---- Z^T, then M^T to shared memory and W^T in registers
+        {
+            float Z[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) Z[j][0] = Z[j][1] = Z[j][2] = Z[j][3] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < kP; kk += 16) {
+                uint32_t xa[4];
+                frag_a<128>(s_x, 16 * ws, kk, lane, xa);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (32 * wt + 16 * j < 16 * ws) continue;
+                    uint32_t yb[4];
+                    frag_b<128>(s_y, 32 * wt + 16 * j, kk, lane, yb);
+                    mma(Z[2 * j], xa, yb[0], yb[1]);
+                    mma(Z[2 * j + 1], xa, yb[2], yb[3]);
+                }
+            }
+            const int s = 16 * ws + (lane >> 2);
+            const float cs0 = v.d.cum[s], cs1 = v.d.cum[s + 8], ds0 = v.d.dt[s], ds1 = v.d.dt[s + 8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 32 * wt + 8 * j + 2 * (lane & 3);
+                if (32 * wt + 16 * (j >> 1) < 16 * ws) continue;
+                const float2 ct = *reinterpret_cast<const float2*>(v.d.cum + t);
+                float l[4];
+                l[0] = t >= s ? exp2f(__fsub_rn(ct.x, cs0)) : 0.0f;
+                l[1] = t + 1 >= s ? exp2f(__fsub_rn(ct.y, cs0)) : 0.0f;
+                l[2] = t >= s + 8 ? exp2f(__fsub_rn(ct.x, cs1)) : 0.0f;
+                l[3] = t + 1 >= s + 8 ? exp2f(__fsub_rn(ct.y, cs1)) : 0.0f;
+                uint32_t m0, n0, m1, n1;
+                split_bf16x2(__fmul_rn(G[j][0], l[0]), __fmul_rn(G[j][1], l[1]), m0, n0);
+                split_bf16x2(__fmul_rn(G[j][2], l[2]), __fmul_rn(G[j][3], l[3]), m1, n1);
+                const uint32_t p0 = tile128(s_m, s, 4 * wt + j) + 4 * (lane & 3);
+                const uint32_t p1 = tile128(s_m, s + 8, 4 * wt + j) + 4 * (lane & 3);
+                ptx::sts32(p0, m0);
+                ptx::sts32(p1, m1);
+                ptx::sts32(p0 + 8192, n0);
+                ptx::sts32(p1 + 8192, n1);
+                W[j][0] = __fmaf_rn(Z[j][0], __fmul_rn(l[0], ds0), W[j][0]);
+                W[j][1] = __fmaf_rn(Z[j][1], __fmul_rn(l[1], ds0), W[j][1]);
+                W[j][2] = __fmaf_rn(Z[j][2], __fmul_rn(l[2], ds1), W[j][2]);
+                W[j][3] = __fmaf_rn(Z[j][3], __fmul_rn(l[3], ds1), W[j][3]);
+            }
+        }
+        __syncthreads();                          // M^T is there
+
+        // ---- dx, rows s = rw + 16 i .., channels pw + 8 p ..
+        {
+            float X[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) X[i][p][0] = X[i][p][1] = X[i][p][2] = X[i][p][3] = 0.0f;
+#pragma unroll 4
+            for (int kk = 0; kk < kN; kk += 16) {
+                uint32_t dh[4], dl[4];
+                frag_b<256>(s_d, pw, kk, lane, dh);
+                frag_b<256>(s_d + 16384, pw, kk, lane, dl);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t ba[4];
+                    frag_a<256>(s_b, rw + 16 * i, kk, lane, ba);
+                    mma(X[i][0], ba, dl[0], dl[1]);
+                    mma(X[i][1], ba, dl[2], dl[3]);
+                    mma(X[i][0], ba, dh[0], dh[1]);
+                    mma(X[i][1], ba, dh[2], dh[3]);
+                }
+            }
+            uint32_t xv[2][2][2], yv[2][2][2];    // x and dy where the accumulators are
+            float sk = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int s = rw + 16 * i + 8 * hf + (lane >> 2);
+                    const float e = v.d.left[s];
+                    float wl = 0.0f;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const uint32_t at = 4 * (lane & 3);
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv[i][hf][p]) : "r"(tile128(s_x, s, (pw >> 3) + p) + at));
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv[i][hf][p]) : "r"(tile128(s_y, s, (pw >> 3) + p) + at));
+                        float& x0 = X[i][p][2 * hf];
+                        float& x1 = X[i][p][2 * hf + 1];
+                        x0 = __fmul_rn(x0, e);
+                        x1 = __fmul_rn(x1, e);
+                        wl = __fmaf_rn(x0, bf16_lo(xv[i][hf][p]), wl);
+                        wl = __fmaf_rn(x1, bf16_hi(xv[i][hf][p]), wl);
+                        sk = __fmaf_rn(bf16_lo(yv[i][hf][p]), bf16_lo(xv[i][hf][p]), sk);
+                        sk = __fmaf_rn(bf16_hi(yv[i][hf][p]), bf16_hi(xv[i][hf][p]), sk);
+                    }
+                    wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 1));
+                    wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 2));
+                    if ((lane & 3) == 0) v.wl[w >> 1][s] = wl;
+                }
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                if (16 * kt < rw) continue;       // t < s everywhere
+                uint32_t yb[4];
+                frag_bt<128>(s_y, 16 * kt, pw, lane, yb);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (16 * kt < rw + 16 * i) continue;
+                    uint32_t mh[4], ml[4];
+                    frag_a<128>(s_m, rw + 16 * i, 16 * kt, lane, mh);
+                    frag_a<128>(s_m + 8192, rw + 16 * i, 16 * kt, lane, ml);
+                    mma(X[i][0], ml, yb[0], yb[1]);
+                    mma(X[i][1], ml, yb[2], yb[3]);
+                    mma(X[i][0], mh, yb[0], yb[1]);
+                    mma(X[i][1], mh, yb[2], yb[3]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int s = rw + 16 * i + 8 * hf + (lane >> 2);
+                    const float dts = v.d.dt[s];
+                    float k = 0.0f;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const float x0 = X[i][p][2 * hf], x1 = X[i][p][2 * hf + 1];
+                        k = __fmaf_rn(x0, bf16_lo(xv[i][hf][p]), k);
+                        k = __fmaf_rn(x1, bf16_hi(xv[i][hf][p]), k);
+                        if (s < n)
+                            *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
+                                bf16x2_of(make_float2(__fmaf_rn(dts, x0, __fmul_rn(skip, bf16_lo(yv[i][hf][p]))),
+                                                      __fmaf_rn(dts, x1, __fmul_rn(skip, bf16_hi(yv[i][hf][p])))));
+                    }
+                    k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 1));
+                    k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 2));
+                    if ((lane & 3) == 0) v.k[w >> 1][s] = k;
+                }
+#pragma unroll
+            for (int q = 16; q > 0; q >>= 1) sk = __fadd_rn(sk, __shfl_xor_sync(0xffffffffu, sk, q));
+            if (lane == 0) v.skip[w] = sk;
+        }
+
+        // ---- dC += exp(cum_t) dy S, dB += dt_s exp(cum_64 - cum_s) x dS
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const uint32_t s_u = side ? s_x : s_y, s_v = side ? s_d : s_s;
+            float T[2][4][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) T[i][j][0] = T[i][j][1] = T[i][j][2] = T[i][j][3] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < kP; kk += 16) {
+                uint32_t ua[2][4];
+                frag_a<128>(s_u, rw, kk, lane, ua[0]);
+                frag_a<128>(s_u, rw + 16, kk, lane, ua[1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t vh[4], vl[4];
+                    frag_bt<256>(s_v, kk, cw + 16 * j, lane, vh);
+                    frag_bt<256>(s_v + 16384, kk, cw + 16 * j, lane, vl);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        mma(T[i][2 * j], ua[i], vl[0], vl[1]);
+                        mma(T[i][2 * j + 1], ua[i], vl[2], vl[3]);
+                        mma(T[i][2 * j], ua[i], vh[0], vh[1]);
+                        mma(T[i][2 * j + 1], ua[i], vh[2], vh[3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = rw + 16 * i + (lane >> 2);
+                const float e0 = side ? __fmul_rn(v.d.dt[r], v.d.left[r]) : v.d.done[r];
+                const float e1 = side ? __fmul_rn(v.d.dt[r + 8], v.d.left[r + 8]) : v.d.done[r + 8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float(&acc)[4] = side ? dB[i][j] : dC[i][j];
+                    acc[0] = __fmaf_rn(e0, T[i][j][0], acc[0]);
+                    acc[1] = __fmaf_rn(e0, T[i][j][1], acc[1]);
+                    acc[2] = __fmaf_rn(e1, T[i][j][2], acc[2]);
+                    acc[3] = __fmaf_rn(e1, T[i][j][3], acc[3]);
+                }
+            }
+        }
+        // ---- <dS, S>
+        {
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int idx = tid + kThreads * i, row = idx >> 4, pc = idx & 15;
+                const uint4 sh = ptx::lds128(tile256(s_s, row, pc)), sl = ptx::lds128(tile256(s_s + 16384, row, pc));
+                const uint4 dh = ptx::lds128(tile256(s_d, row, pc)), dl = ptx::lds128(tile256(s_d + 16384, row, pc));
+                const uint32_t a4[4] = {sh.x, sh.y, sh.z, sh.w}, b4[4] = {sl.x, sl.y, sl.z, sl.w};
+                const uint32_t c4[4] = {dh.x, dh.y, dh.z, dh.w}, d4[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    dot = __fmaf_rn(__fadd_rn(bf16_lo(a4[q]), bf16_lo(b4[q])), __fadd_rn(bf16_lo(c4[q]), bf16_lo(d4[q])), dot);
+                    dot = __fmaf_rn(__fadd_rn(bf16_hi(a4[q]), bf16_hi(b4[q])), __fadd_rn(bf16_hi(c4[q]), bf16_hi(d4[q])), dot);
+                }
+            }
+#pragma unroll
+            for (int q = 16; q > 0; q >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, q));
+            if (lane == 0) v.dot[w] = dot;
+        }
+        if (w == 7 && h + 1 < h1) vectors(h + 1);
+        __syncthreads();                          // the head's sums are there
+        // ---- d dt: lane l has tokens 2 l, 2 l + 1
+        if (w == 0) {
+            const float A = -expf(a.a_log[h]);
+            float kp[2], q[2], wsum = 0.0f, dot = 0.0f, sk = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                const float dt = v.d.dt[t];
+                kp[i] = __fadd_rn(__fadd_rn(v.k[0][t], v.k[1][t]), __fadd_rn(v.k[2][t], v.k[3][t]));
+                const float wl = __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t]));
+                wsum = __fmaf_rn(dt, wl, wsum);
+                q[i] = __fmaf_rn(-dt, kp[i], v.r[t]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dot = __fadd_rn(dot, v.dot[i]);
+                sk = __fadd_rn(sk, v.skip[i]);
+            }
+            float suf = __fadd_rn(q[0], q[1]);      // inclusive sum from the right
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const float u = __shfl_down_sync(0xffffffffu, suf, s);
+                if (lane + s < 32) suf = __fadd_rn(suf, u);
+                wsum = __fadd_rn(wsum, __shfl_xor_sync(0xffffffffu, wsum, s));
+            }
+            float after = __shfl_down_sync(0xffffffffu, suf, 1);
+            if (lane == 31) after = 0.0f;
+            const float over = __fmaf_rn(v.d.done[kQ - 1], dot, wsum);
+            const float da[2] = {__fadd_rn(suf, over), __fadd_rn(__fadd_rn(q[1], after), over)};
+            float sb = 0.0f, sa = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                if (t >= n) continue;
+                const float dr = __fmul_rn(__fmaf_rn(A, da[i], kp[i]), v.sig[t]);
+                o.ddt[(int64_t)(t0 + t) * o.ldddt + h] = f32_to_bf16_bits(dr);
+                sb = __fadd_rn(sb, dr);
+                sa = __fmaf_rn(da[i], __fmul_rn(v.d.dt[t], A), sa);
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) {
+                sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, s));
+                sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, s));
+            }
+            if (lane == 0)
+                *reinterpret_cast<float4*>(o.sums + ((int64_t)ci * a.nheads + h) * 4) = make_float4(sb, sa, sk, 0.0f);
+        }
+    }
+    ptx::cp_async_wait<0>();
+
+    // ---- W^T as two bf16 parts, then dB += W^T C, dC += W B
+    {
+        const int s = 16 * ws + (lane >> 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t h0v, l0v, h1v, l1v;
+            split_bf16x2(W[j][0], W[j][1], h0v, l0v);
+            split_bf16x2(W[j][2], W[j][3], h1v, l1v);
+            const uint32_t p0 = tile128(s_m, s, 4 * wt + j) + 4 * (lane & 3);
+            const uint32_t p1 = tile128(s_m, s + 8, 4 * wt + j) + 4 * (lane & 3);
+            ptx::sts32(p0, h0v);
+            ptx::sts32(p1, h1v);
+            ptx::sts32(p0 + 8192, l0v);
+            ptx::sts32(p1 + 8192, l1v);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+#pragma unroll 1
+        for (int kk = 0; kk < kQ; kk += 16) {
+            if (side ? kk + 15 < rw : kk > rw + 31) continue;      // dB: t >= s; dC: s <= t
+            uint32_t vb[2][4];
+            frag_bt<256>(side ? s_c : s_b, kk, cw, lane, vb[0]);
+            frag_bt<256>(side ? s_c : s_b, kk, cw + 16, lane, vb[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int part = 1; part >= 0; --part) {
+                    uint32_t wa[4];
+                    if (side) frag_a<128>(s_m + part * 8192, rw + 16 * i, kk, lane, wa);
+                    else frag_at<128>(s_m + part * 8192, kk, rw + 16 * i, lane, wa);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        mma(side ? dB[i][2 * j] : dC[i][2 * j], wa, vb[j][0], vb[j][1]);
+                        mma(side ? dB[i][2 * j + 1] : dC[i][2 * j + 1], wa, vb[j][2], vb[j][3]);
+                    }
+                }
+            }
+        }
+    }
+    const int64_t ldp = (int64_t)ngroups * kN;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int r = rw + 16 * i + 8 * hf + (lane >> 2);
+            if (r >= n) continue;
+            const int64_t at = ((int64_t)sp * a.total + t0 + r) * ldp + g * kN + cw + 2 * (lane & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                *reinterpret_cast<float2*>(o.db_part + at + 8 * j) = make_float2(dB[i][j][2 * hf], dB[i][j][2 * hf + 1]);
+                *reinterpret_cast<float2*>(o.dc_part + at + 8 * j) = make_float2(dC[i][j][2 * hf], dC[i][j][2 * hf + 1]);
+            }
+        }
+}
+
+// dB and dC: the splits' parts added in order, 4 columns per thread; CTA per chunk (rows of no chunk stay)
+__global__ void __launch_bounds__(256) scan_sum_kernel(const Args a, const float* __restrict__ db_part,
+                                                       const float* __restrict__ dc_part, int splits, uint16_t* db,
+                                                       int64_t lddb, uint16_t* dc, int64_t lddc) {
+    if ((int)blockIdx.x >= a.count[1]) return;
+    const Chunk ch = a.chunks[blockIdx.x];
+    const int cols = a.nheads / a.per_group * kN, per = cols / 4;
+    const float* part = blockIdx.y ? dc_part : db_part;
+    uint16_t* out = blockIdx.y ? dc : db;
+    const int64_t ld = blockIdx.y ? lddc : lddb;
+    for (int i = threadIdx.x; i < ch.n * per; i += 256) {
+        const int r = i / per, c = 4 * (i - r * per);
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = 0; k < splits; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(part + ((int64_t)k * a.total + ch.t0 + r) * cols + c);
+            s = make_float4(__fadd_rn(s.x, v.x), __fadd_rn(s.y, v.y), __fadd_rn(s.z, v.z), __fadd_rn(s.w, v.w));
+        }
+        *reinterpret_cast<uint2*>(out + (int64_t)(ch.t0 + r) * ld + c) =
+            make_uint2(bf16x2_of(make_float2(s.x, s.y)), bf16x2_of(make_float2(s.z, s.w)));
+    }
+}
+
+// the parameters' gradients: CTA per head over all chunks
+__global__ void __launch_bounds__(256) scan_params_kernel(const Args a, const float* __restrict__ sums, float* ddt_bias,
+                                                          float* da_log, float* dd_skip) {
+    __shared__ float4 red[8];
+    const int h = blockIdx.x, n = a.count[1];
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = threadIdx.x; i < n; i += 256) {
+        const float4 v = *reinterpret_cast<const float4*>(sums + ((int64_t)i * a.nheads + h) * 4);
+        s = make_float4(__fadd_rn(s.x, v.x), __fadd_rn(s.y, v.y), __fadd_rn(s.z, v.z), 0.0f);
+    }
+#pragma unroll
+    for (int q = 16; q > 0; q >>= 1) {
+        s.x = __fadd_rn(s.x, __shfl_xor_sync(0xffffffffu, s.x, q));
+        s.y = __fadd_rn(s.y, __shfl_xor_sync(0xffffffffu, s.y, q));
+        s.z = __fadd_rn(s.z, __shfl_xor_sync(0xffffffffu, s.z, q));
+    }
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w)
+            s = make_float4(__fadd_rn(s.x, red[w].x), __fadd_rn(s.y, red[w].y), __fadd_rn(s.z, red[w].z), 0.0f);
+        ddt_bias[h] = s.x;
+        da_log[h] = s.y;
+        dd_skip[h] = s.z;
+    }
+}
+
+// Splits of a group's heads: the fewest waves of 148 CTAs, a CTA costing its heads and about one more
+struct Split {
+    int splits, per;
+};
+Split choose_split(int cap_chunks, int ngroups, int per_group) {
+    Split best{1, per_group};
+    double cost = 1e30;
+    for (int s = 1; s <= per_group && s <= 16; ++s) {
+        const int per = (per_group + s - 1) / s;
+        const int64_t ctas = (int64_t)cap_chunks * ngroups * s;
+        const double c = (double)((ctas + 147) / 148) * (per + 1);
+        if (c < cost) {
+            cost = c;
+            best = Split{(per_group + per - 1) / per, per};
+        }
+    }
+    return best;
+}
+
+struct BwdWs {
+    size_t s_in, ds, ydy, db, dc, sums, total;
+};
+BwdWs bwd_ws(const dfssm_scan_dims* d, int total, int nseq, const Plan& p) {
+    BwdWs w{};
+    const size_t states = (size_t)p.cap_chunks * d->nheads * 2 * kStateElems * 2;
+    const Split sp = choose_split(p.cap_chunks, d->ngroups, d->nheads / d->ngroups);
+    size_t o = p.total;
+    w.s_in = o;
+    o = up256(o + states);
+    w.ds = o;
+    o = up256(o + states);
+    w.ydy = o;
+    o = up256(o + (size_t)total * d->nheads * 4);
+    w.db = o;
+    o = up256(o + (size_t)sp.splits * total * d->ngroups * kN * 4);
+    w.dc = o;
+    o = up256(o + (size_t)sp.splits * total * d->ngroups * kN * 4);
+    w.sums = o;
+    o = up256(o + (size_t)p.cap_chunks * d->nheads * 16);
+    w.total = o;
+    return w;
+}
+
+}  // namespace
+
+cudaError_t setup_bwd() {
+    return cudaFuncSetAttribute(scan_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+}
+
+size_t bwd_workspace(const dfssm_scan_dims* d, int total, int nseq) {
+    return bwd_ws(d, total, nseq, make_plan(d->nheads, total, nseq, true)).total;
+}
+
+}  // namespace scan
+}  // namespace dfssm
+
+using namespace dfssm;
+using namespace dfssm::scan;
+
+extern "C" dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
+                                           int32_t nseq, const void* dy, int64_t dy_stride, const float* dfinal_state,
+                                           const dfssm_scan_grads* gr, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+    dfssm_status st = check_call(dims, in, total, nseq);
+    if (st != DFSSM_OK) return st;
+    if (!gr || !dy || !al16(dfinal_state) || !al16(gr->dinit_state)) return DFSSM_ERR_INVALID_ARG;
+    const int64_t di = (int64_t)dims->nheads * kP, gn = (int64_t)dims->ngroups * kN, most = (int64_t)1 << 30;
+    const void* rows[4] = {dy, gr->dx, gr->db, gr->dc};
+    const int64_t ld[4] = {dy_stride, gr->dx_stride, gr->db_stride, gr->dc_stride}, least[4] = {di, di, gn, gn};
+    for (int i = 0; i < 4; ++i)
+        if (!rows[i] || !al16(rows[i]) || ld[i] < least[i] || ld[i] % 8 != 0 || ld[i] > most) return DFSSM_ERR_INVALID_ARG;
+    if (!gr->ddt || (reinterpret_cast<uintptr_t>(gr->ddt) & 1u) || gr->ddt_stride < dims->nheads || gr->ddt_stride > most)
+        return DFSSM_ERR_INVALID_ARG;
+    const void* words[3] = {gr->ddt_bias, gr->da_log, gr->dd_skip};
+    for (const void* p : words)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return DFSSM_ERR_INVALID_ARG;
+    const Plan p = make_plan(dims->nheads, total, nseq, true);
+    const BwdWs w = bwd_ws(dims, total, nseq, p);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < w.total)
+        return DFSSM_ERR_INVALID_ARG;
+    if ((st = setup()) != DFSSM_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const Args a = make_args(dims, in, total, nseq, p, ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    GradArgs o{};
+    o.dy = static_cast<const uint16_t*>(dy);
+    o.lddy = dy_stride;
+    uint16_t* s_in = reinterpret_cast<uint16_t*>(ws + w.s_in);
+    uint16_t* ds = reinterpret_cast<uint16_t*>(ws + w.ds);
+    float* ydy = reinterpret_cast<float*>(ws + w.ydy);
+    o.s_in = s_in;
+    o.ds_out = ds;
+    o.ydy = ydy;
+    o.dx = static_cast<uint16_t*>(gr->dx);
+    o.lddx = gr->dx_stride;
+    o.ddt = static_cast<uint16_t*>(gr->ddt);
+    o.ldddt = gr->ddt_stride;
+    o.db_part = reinterpret_cast<float*>(ws + w.db);
+    o.dc_part = reinterpret_cast<float*>(ws + w.dc);
+    o.sums = reinterpret_cast<float*>(ws + w.sums);
+    const Split sp = choose_split(p.cap_chunks, dims->ngroups, dims->nheads / dims->ngroups);
+    o.splits = sp.splits;
+    o.per_split = sp.per;
+    StateArgs back{o.dy, dy_stride, dfinal_state, ds, gr->dinit_state};
+    if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, s) != cudaSuccess ||
+        launch_states_forward(a, s_in, o.dy, dy_stride, ydy, s) != cudaSuccess ||
+        launch_states_back(a, back, s) != cudaSuccess)
+        return DFSSM_ERR_CUDA;
+    scan_grad_kernel<<<p.cap_chunks * dims->ngroups * sp.splits, kThreads, kGradSmem, s>>>(a, o);
+    scan_sum_kernel<<<dim3(p.cap_chunks, 2), 256, 0, s>>>(a, o.db_part, o.dc_part, sp.splits,
+                                                          static_cast<uint16_t*>(gr->db), gr->db_stride,
+                                                          static_cast<uint16_t*>(gr->dc), gr->dc_stride);
+    scan_params_kernel<<<dims->nheads, 256, 0, s>>>(a, o.sums, gr->ddt_bias, gr->da_log, gr->dd_skip);
+    return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
+}

@@ -77,6 +77,7 @@ typedef enum { DFSSM_BF16 = 0, DFSSM_F32 = 1, DFSSM_I8 = 2 } dfssm_dtype;
 #define DFSSM_DEVERR_TIMEOUT    0x4u   /* a bounded in-kernel wait gave up (output undefined) */
 #define DFSSM_DEVERR_ENTRY_PTR  0x8u   /* a stack entry holds a NULL or misaligned pointer (entry skipped) */
 #define DFSSM_DEVERR_TOKEN_ID   0x10u  /* an embedding id outside [0, vocab) (its row is zeros) */
+#define DFSSM_DEVERR_SEQLENS    0x20u  /* sequence offsets out of order or range (the sequence is skipped) */
 
 /* Shape of one linear. d_in % 128 == 0, 128 <= d_in <= 8192; 1 <= d_out <= 2^20;
  * rank == 16; 1 <= max_m <= 65536; y_dtype DFSSM_BF16 or DFSSM_F32; flags = 0. */
@@ -376,6 +377,91 @@ dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8_t* q, cons
 dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8_t* q, const float* sx,
                             const int32_t* targets, const float* lse, const float* grad, int32_t m, void* dh,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the state recurrence over packed sequences -----------------------------------------------
+ * What dfssm_ssm_step does after its convolution for one token, for the tokens of prompts or of a
+ * training batch ("Density Field State Space Models", technical summary §2.C, state operations; the
+ * recurrence is Mamba-2's). Per head h, with the state S (headdim x d_state):
+ *   dt = softplus(dt_raw + dt_bias) (the argument itself above 20), a = -exp(a_log) dt
+ *   S_t = exp(a_t) S_{t-1} + dt_t x_t B_t^T;     y_t = S_t C_t + d_skip x_t
+ * Heads share B and C by groups: head h reads group h / (nheads / ngroups). Supported: headdim 64,
+ * d_state 128, nheads a multiple of ngroups, up to 1024. */
+typedef struct {
+    int32_t nheads;
+    int32_t ngroups;
+    int32_t headdim;   /* 64 */
+    int32_t d_state;   /* 128 */
+} dfssm_scan_dims;
+
+/* Inputs (HOST struct of device pointers, caller-owned). Token rows are bf16 with a row stride in
+ * elements, so that x, b and c can be column blocks of the convolution's output rows and dt one of the
+ * in_proj output's:
+ *   x   total x (nheads headdim), b, c  total x (ngroups d_state): 16-byte aligned, strides multiples of 8;
+ *   dt  total x nheads: 2-byte aligned, any stride >= nheads;
+ *   dt_bias, a_log, d_skip  nheads fp32;
+ *   init_state  nseq x nheads x headdim x d_state fp32 (the layout of dfssm_ssm_layer.ssm_state), or NULL: zeros;
+ *   cu_seqlens  nseq + 1 int32: sequence i has the token rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (any
+ *               length, 0 included); rows of no sequence are neither read nor written. */
+typedef struct {
+    const void* x;
+    int64_t x_stride;
+    const void* b;
+    int64_t b_stride;
+    const void* c;
+    int64_t c_stride;
+    const void* dt;
+    int64_t dt_stride;
+    const float* dt_bias;
+    const float* a_log;
+    const float* d_skip;
+    const float* init_state;
+    const int32_t* cu_seqlens;
+} dfssm_scan_inputs;
+
+/* Bytes of device workspace for a call on `total` token rows and nseq sequences (backward: 0 for
+ * dfssm_ssm_scan_fwd, 1 for dfssm_ssm_scan_bwd, which keeps the states around every 64 tokens there). */
+dfssm_status dfssm_ssm_scan_workspace_bytes(const dfssm_scan_dims* dims, int32_t total, int32_t nseq,
+                                            int32_t backward, size_t* bytes);
+
+/* y: total x (nheads headdim) bf16 (16-byte aligned, row stride y_stride a multiple of 8); final_state: as
+ * init_state (which it may equal), the state behind each sequence's last token, or NULL. 1 <= total <=
+ * 2^22, 1 <= nseq <= 65536. States are kept in fp32; a sequence is worked on in chunks of 64 tokens, inside
+ * which a non-finite input can reach earlier tokens too (never another sequence).
+ * workspace: 256-byte aligned, at least dfssm_ssm_scan_workspace_bytes, zeroed once before its first use.
+ * Its first 4 bytes are a device error word (DFSSM_DEVERR_SEQLENS: a sequence whose offsets are negative,
+ * descending or beyond total is skipped), read and cleared by dfssm_ssm_read_error; nothing else is kept
+ * between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call on a device
+ * sets kernel attributes (make it before any stream capture). Results repeat bit for bit. */
+dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
+                                int32_t nseq, void* y, int64_t y_stride, float* final_state, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Gradients (HOST struct of device pointers): dx, db, dc, ddt in the layout and type of x, b, c, dt
+ * (bf16; dx, db, dc 16-byte aligned with strides that are multiples of 8; ddt 2-byte aligned); db and dc
+ * are summed over the heads of a group; ddt is the gradient of dt_raw. ddt_bias, da_log, dd_skip: nheads fp32, summed
+ * over all tokens. dinit_state: as init_state, or NULL. */
+typedef struct {
+    void* dx;
+    int64_t dx_stride;
+    void* db;
+    int64_t db_stride;
+    void* dc;
+    int64_t dc_stride;
+    void* ddt;
+    int64_t ddt_stride;
+    float* ddt_bias;
+    float* da_log;
+    float* dd_skip;
+    float* dinit_state;
+} dfssm_scan_grads;
+
+/* The gradient of sum(dy y) + sum(dfinal_state final_state) with respect to every input. dy: bf16 as y;
+ * dfinal_state: as final_state, or NULL (zeros). Nothing of the forward call is needed; the states are
+ * computed again. Workspace, errors and limits as for dfssm_ssm_scan_fwd (with backward = 1). */
+dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
+                                int32_t nseq, const void* dy, int64_t dy_stride, const float* dfinal_state,
+                                const dfssm_scan_grads* grads, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /* Test of the error path of the decode kernel (m <= 16 tokens), which must end with an
  * error status and never hang. With flags & DFSSM_TEST_STALL, the first CTA of that
