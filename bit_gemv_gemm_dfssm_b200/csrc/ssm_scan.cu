@@ -126,27 +126,20 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
 // ------------------------------------------------------------------------------- forward
 
 struct FwdOut {
-    uint16_t* y;               // NULL in the backward pass's run
+    uint16_t* y;
     int64_t ldy;
     float* final_state;        // or NULL
-    // backward pass: the state in front of every chunk, and dy_t . (y_t - d_skip x_t)
-    uint16_t* states;          // [chunks][H][2][64][128]
-    const uint16_t* dy;
-    int64_t lddy;
-    float* ydy;                // [total][H]
 };
 
 constexpr int kStage = 16384 + 16384 + 8192;          // C, B, X of one chunk
-constexpr int kFwdSmem = 2 * kStage + 2 * 8192 + 2 * (int)sizeof(Decay) + 4 * kQ * 4 + 128;
+constexpr int kFwdSmem = 2 * kStage + 2 * 8192 + 2 * (int)sizeof(Decay) + 128;
 
-template <bool BWD>
 __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const Args a, const FwdOut o) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
     const uint32_t s_m = base + 2 * kStage;           // M: high part, then low part
     Decay* dec = reinterpret_cast<Decay*>(smem + 2 * kStage + 2 * 8192);
-    float* s_ydy = reinterpret_cast<float*>(dec + 2);  // [4][64]
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int h = blockIdx.x % a.nheads, g = h / a.per_group;
     Item it;
@@ -194,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const Args a, con
         ptx::cp_async_wait<0>();
         __syncthreads();                 // this chunk's tiles and decays are there; the last one's are free
         fetch(k + 1);
-        if (BWD) state_store_split(S, o.states + ((int64_t)(it.chunk0 + k) * a.nheads + h) * 2 * kStateElems, w, lane);
 
         // ---- M, rows 16 w + lane / 4 (+ 8)
         {
@@ -293,40 +285,20 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const Args a, con
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int t = 16 * i + 8 * hf + (lane >> 2);
-                float dot = 0.0f;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const float y0 = y[i][p][2 * hf], y1 = y[i][p][2 * hf + 1];
-                    const int ch = 16 * w + 8 * p + 2 * (lane & 3);
-                    if (!BWD) {
-                        uint32_t xv;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv) : "r"(tile128(s_x, t, 2 * w + p) + 4 * (lane & 3)));
-                        if (t < n)
-                            *reinterpret_cast<uint32_t*>(o.y + (int64_t)(t0 + t) * o.ldy + h * kP + ch) =
-                                bf16x2_of(make_float2(__fmaf_rn(skip, bf16_lo(xv), y0), __fmaf_rn(skip, bf16_hi(xv), y1)));
-                    } else if (t < n) {
-                        const uint32_t dv =
-                            *reinterpret_cast<const uint32_t*>(o.dy + (int64_t)(t0 + t) * o.lddy + h * kP + ch);
-                        dot = __fmaf_rn(y0, bf16_lo(dv), dot);
-                        dot = __fmaf_rn(y1, bf16_hi(dv), dot);
-                    }
-                }
-                if (BWD) {
-                    dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, 1));
-                    dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, 2));
-                    if ((lane & 3) == 0) s_ydy[w * kQ + t] = dot;
+                    uint32_t xv;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv) : "r"(tile128(s_x, t, 2 * w + p) + 4 * (lane & 3)));
+                    if (t < n)
+                        *reinterpret_cast<uint32_t*>(o.y + (int64_t)(t0 + t) * o.ldy + h * kP + 16 * w + 8 * p + 2 * (lane & 3)) =
+                            bf16x2_of(make_float2(__fmaf_rn(skip, bf16_lo(xv), y[i][p][2 * hf]),
+                                                  __fmaf_rn(skip, bf16_hi(xv), y[i][p][2 * hf + 1])));
                 }
             }
 
         // ---- the state at the chunk's end
-        state_update<true>(S, d.done[kQ - 1], s_x, s_b, d.left, d.dt, w, lane);
+        state_update(S, d.done[kQ - 1], s_x, s_b, d.left, d.dt, true, w, lane);
         if (w == 0 && k + 1 < n_ch) chunk_decay(dec[(k + 1) & 1], raw0, raw1, min(kQ, it.len - (k + 1) * kQ), bias, a2, lane);
-        if (BWD) {
-            __syncthreads();
-            if (tid < n)
-                o.ydy[(int64_t)(t0 + tid) * a.nheads + h] = __fadd_rn(__fadd_rn(s_ydy[tid], s_ydy[kQ + tid]),
-                                                                     __fadd_rn(s_ydy[2 * kQ + tid], s_ydy[3 * kQ + tid]));
-        }
     }
     ptx::cp_async_wait<0>();
     if (o.final_state && (it.flags & kLast)) state_store(S, o.final_state + sh, w, lane);
@@ -337,20 +309,22 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const Args a, con
 // ------------------------------------------------------------------------------- segments
 
 // Starts of the segments of cut sequences, from the segments' own contributions, in place.
-// CTA (sequence, head); reverse: from the last segment to the first.
-__global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const float* __restrict__ start, int reverse) {
-    const int h = blockIdx.x % a.nheads, s = blockIdx.x / a.nheads;
+// CTA (sequence, head), y: 0 forward in time, 1 backward (from the last segment to the first).
+__global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const float* __restrict__ init,
+                                                         const float* __restrict__ dfinal) {
+    const int h = blockIdx.x % a.nheads, s = blockIdx.x / a.nheads, rev = blockIdx.y;
     const int i0 = a.seq_slots[s].x, i1 = i0 + a.seq_slots[s].y;
     if (i1 - i0 < 2) return;
+    const float* start = rev ? dfinal : init;
     float4 v[8];
     const float4* src = reinterpret_cast<const float4*>(start + ((int64_t)s * a.nheads + h) * kStateElems);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = start ? src[threadIdx.x + 256 * k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i = i0; i < i1; ++i) {
-        const int slot = reverse ? i0 + i1 - 1 - i : i;
-        float4* p = reinterpret_cast<float4*>(a.seg_state + ((int64_t)slot * a.nheads + h) * kStateElems);
+        const int64_t at = ((int64_t)rev * a.cap_slots + (rev ? i0 + i1 - 1 - i : i)) * a.nheads + h;
+        float4* p = reinterpret_cast<float4*>(a.seg_state + at * kStateElems);
         const bool more = i + 1 < i1;
-        const float keep = more ? a.seg_decay[(int64_t)slot * a.nheads + h] : 0.0f;
+        const float keep = more ? a.seg_decay[at] : 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             float4 own = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -362,26 +336,28 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const flo
     }
 }
 
-// The state alone through an item: forward (u = x, v = B) or backward in time (u = dy, v = C: the state's
-// gradient). STORE: from its start, every chunk's end gradient to the workspace and the first one out;
-// otherwise from zero, the item's own contribution and decay.
-template <bool REV, bool STORE>
+// The state alone through an item: blockIdx.y 0 forward in time (u = x, v = B), 1 backward (u = dy, v = C: the
+// state's gradient). STORE: from its start, at every chunk to the workspace; otherwise from zero, the
+// item's own contribution and decay, for what starts behind it.
+template <bool STORE>
 __global__ void __launch_bounds__(kThreads, 3) scan_state_kernel(const Args a, const StateArgs o) {
     constexpr int kSt = 16384 + 8192;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
-    Decay* dec = reinterpret_cast<Decay*>(smem + 2 * kSt);
+    Decay* dec = reinterpret_cast<Decay*>(smem + 2 * kSt + 16384);
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const uint32_t stage = base + 2 * kSt + 4096 * w;
+    const bool rev = blockIdx.y != 0;
     const int h = blockIdx.x % a.nheads, g = h / a.per_group;
     Item it;
     if (!get_item(a, blockIdx.x / a.nheads, it) || it.len < 0) return;
-    if (!STORE && (!(it.flags & kCut) || (it.flags & (REV ? kFirst : kLast)))) return;     // nothing starts behind it
+    if (!STORE && (!(it.flags & kCut) || (it.flags & (rev ? kFirst : kLast)))) return;     // nothing starts behind it
     const int n_ch = (it.len + kQ - 1) / kQ;
-    const uint16_t* u = (REV ? o.u : a.x) + (int64_t)h * kP;
-    const uint16_t* v = (REV ? a.c : a.b) + (int64_t)g * kN;
-    const int64_t ldu = REV ? o.ldu : a.ldx, ldv = REV ? a.ldc : a.ldb;
-    auto chunk_of = [&](int k) { return REV ? n_ch - 1 - k : k; };
+    const uint16_t* u = (rev ? o.dy : a.x) + (int64_t)h * kP;
+    const uint16_t* v = (rev ? a.c : a.b) + (int64_t)g * kN;
+    const int64_t ldu = rev ? o.lddy : a.ldx, ldv = rev ? a.ldc : a.ldb;
+    auto chunk_of = [&](int k) { return rev ? n_ch - 1 - k : k; };
     auto fetch = [&](int k) {
         if (k < n_ch) {
             const int q = chunk_of(k), t0 = it.t0 + q * kQ, n = min(kQ, it.len - q * kQ);
@@ -395,36 +371,48 @@ __global__ void __launch_bounds__(kThreads, 3) scan_state_kernel(const Args a, c
     const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
     StateFrag S;
     const int64_t sh = ((int64_t)it.seq * a.nheads + h) * kStateElems;
-    if (STORE && (it.flags & kCut)) state_load(S, a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems, w, lane);
-    else if (STORE && o.start) state_load(S, o.start + sh, w, lane);
+    const int64_t slot = ((int64_t)(rev ? a.cap_slots : 0) + it.slot) * a.nheads + h;
+    const float* start = rev ? o.dfinal : a.init;
+    if (STORE && (it.flags & kCut)) state_load(S, a.seg_state + slot * kStateElems, w, lane);
+    else if (STORE && start) state_load(S, start + sh, w, lane);
     else state_zero(S);
-    float total = 0.0f;
-    auto decay = [&](int k) {
+    float total = 0.0f, raw0 = 0.0f, raw1 = 0.0f;
+    auto raws = [&](int k) {                    // the chunk's dt, one chunk before its decays are needed
+        if (w != 0 || k >= n_ch) return;
         const int q = chunk_of(k), t0 = it.t0 + q * kQ, n = min(kQ, it.len - q * kQ);
-        chunk_decay(dec[k & 1], raw_dt(a, t0, n, h, 2 * lane), raw_dt(a, t0, n, h, 2 * lane + 1), n, bias, a2, lane);
+        raw0 = raw_dt(a, t0, n, h, 2 * lane);
+        raw1 = raw_dt(a, t0, n, h, 2 * lane + 1);
     };
-    if (w == 0 && n_ch > 0) decay(0);
+    auto decay = [&](int k) {
+        if (w != 0 || k >= n_ch) return;
+        chunk_decay(dec[k & 1], raw0, raw1, min(kQ, it.len - chunk_of(k) * kQ), bias, a2, lane);
+    };
+    raws(0);
+    decay(0);
+    raws(1);
     for (int k = 0; k < n_ch; ++k) {
         const uint32_t st = base + (k & 1) * kSt;
         const Decay& d = dec[k & 1];
         ptx::cp_async_wait<0>();
         __syncthreads();
         fetch(k + 1);
-        if (w == 0 && k + 1 < n_ch) decay(k + 1);
+        decay(k + 1);
+        raws(k + 2);
         if (STORE)
-            state_store_split(S, o.states + ((int64_t)(it.chunk0 + chunk_of(k)) * a.nheads + h) * 2 * kStateElems, w, lane);
+            state_store_split(S, (rev ? o.dstates : o.states) + ((int64_t)(it.chunk0 + chunk_of(k)) * a.nheads + h) * 2 * kStateElems,
+                              stage, w, lane);
         total = __fadd_rn(total, d.cum[kQ - 1]);
-        state_update<!REV>(S, d.done[kQ - 1], st + 16384, st, REV ? d.done : d.left, d.dt, w, lane);
+        state_update(S, d.done[kQ - 1], st + 16384, st, rev ? d.done : d.left, d.dt, !rev, w, lane);
     }
     ptx::cp_async_wait<0>();
     if (!STORE) {
-        state_store(S, a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems, w, lane);
-        if (tid == 0) a.seg_decay[(int64_t)it.slot * a.nheads + h] = exp2f(total);
-    } else if (o.out && (it.flags & kFirst)) {
-        state_store(S, o.out + sh, w, lane);
+        state_store(S, a.seg_state + slot * kStateElems, w, lane);
+        if (tid == 0) a.seg_decay[slot] = exp2f(total);
+    } else if (rev && o.dinit && (it.flags & kFirst)) {
+        state_store(S, o.dinit + sh, w, lane);
     }
 }
-constexpr int kStateSmem = 2 * (16384 + 8192) + 2 * (int)sizeof(Decay) + 128;
+constexpr int kStateSmem = 2 * (16384 + 8192) + 16384 + 2 * (int)sizeof(Decay) + 128;
 
 // ------------------------------------------------------------------------------- host
 
@@ -447,9 +435,10 @@ Plan make_plan(int nheads, int total, int nseq, bool backward) {
     p.seq_items = o;   o = up256(o + sizeof(Item) * (size_t)p.cap_items);
     p.seq_slots = o;   o = up256(o + sizeof(int2) * (size_t)nseq);
     p.chunks = o;      o = up256(o + sizeof(Chunk) * (size_t)p.cap_chunks);
-    p.seg_decay = o;   o = up256(o + 4 * (size_t)p.cap_slots * nheads);
+    const size_t slots = (backward ? 2 : 1) * (size_t)p.cap_slots * nheads;
+    p.seg_decay = o;   o = up256(o + 4 * slots);
     p.seg_state = o;
-    if (total > p.seg_len) o = up256(o + 4 * (size_t)p.cap_slots * nheads * kStateElems);
+    if (total > p.seg_len) o = up256(o + 4 * slots * kStateElems);
     p.total = o;
     return p;
 }
@@ -527,11 +516,9 @@ dfssm_status setup() {
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_ready[dev]) {
         const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        if (cudaFuncSetAttribute(scan_fwd_kernel<false>, at, kFwdSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(scan_fwd_kernel<true>, at, kFwdSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(scan_state_kernel<false, false>, at, kStateSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(scan_state_kernel<true, false>, at, kStateSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(scan_state_kernel<true, true>, at, kStateSmem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(scan_fwd_kernel, at, kFwdSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(scan_state_kernel<false>, at, kStateSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(scan_state_kernel<true>, at, kStateSmem) != cudaSuccess ||
             setup_bwd() != cudaSuccess)
             return DFSSM_ERR_CUDA;
         g_ready[dev] = true;
@@ -545,30 +532,17 @@ cudaError_t launch_table(const Args& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_segment_starts(const Args& a, cudaStream_t s) {
+cudaError_t launch_segment_starts(const Args& a, const StateArgs& o, int directions, cudaStream_t s) {
     if (a.total <= a.seg_len) return cudaSuccess;          // no sequence can be cut
-    scan_state_kernel<false, false><<<a.cap_items * a.nheads, kThreads, kStateSmem, s>>>(a, StateArgs{});
-    scan_carry_kernel<<<a.nseq * a.nheads, 256, 0, s>>>(a, a.init, 0);
+    scan_state_kernel<false><<<dim3(a.cap_items * a.nheads, directions), kThreads, kStateSmem, s>>>(a, o);
+    scan_carry_kernel<<<dim3(a.nseq * a.nheads, directions), 256, 0, s>>>(a, a.init, o.dfinal);
     return cudaGetLastError();
 }
 
-cudaError_t launch_states_back(const Args& a, const StateArgs& o, cudaStream_t s) {
-    if (a.total > a.seg_len) {
-        scan_state_kernel<true, false><<<a.cap_items * a.nheads, kThreads, kStateSmem, s>>>(a, o);
-        scan_carry_kernel<<<a.nseq * a.nheads, 256, 0, s>>>(a, o.start, 1);
-    }
-    scan_state_kernel<true, true><<<a.cap_items * a.nheads, kThreads, kStateSmem, s>>>(a, o);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_states_forward(const Args& a, uint16_t* states, const uint16_t* dy, int64_t lddy, float* ydy,
-                                  cudaStream_t s) {
-    FwdOut o{};
-    o.states = states;
-    o.dy = dy;
-    o.lddy = lddy;
-    o.ydy = ydy;
-    scan_fwd_kernel<true><<<a.cap_items * a.nheads, kThreads, kFwdSmem, s>>>(a, o);
+cudaError_t launch_states(const Args& a, const StateArgs& o, cudaStream_t s) {
+    cudaError_t e = launch_segment_starts(a, o, 2, s);
+    if (e != cudaSuccess) return e;
+    scan_state_kernel<true><<<dim3(a.cap_items * a.nheads, 2), kThreads, kStateSmem, s>>>(a, o);
     return cudaGetLastError();
 }
 
@@ -605,7 +579,7 @@ extern "C" dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const df
     o.y = static_cast<uint16_t*>(y);
     o.ldy = y_stride;
     o.final_state = final_state;
-    if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, s) != cudaSuccess) return DFSSM_ERR_CUDA;
-    scan_fwd_kernel<false><<<(a.direct ? nseq : a.cap_items) * a.nheads, kThreads, kFwdSmem, s>>>(a, o);
+    if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, StateArgs{}, 1, s) != cudaSuccess) return DFSSM_ERR_CUDA;
+    scan_fwd_kernel<<<(a.direct ? nseq : a.cap_items) * a.nheads, kThreads, kFwdSmem, s>>>(a, o);
     return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
 }

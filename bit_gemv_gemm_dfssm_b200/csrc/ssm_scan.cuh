@@ -64,8 +64,8 @@ struct Args {
     Item* seq_items;                   // the same in sequence order
     int2* seq_slots;                   // [nseq] first slot and segments of a cut sequence (0 segments: not cut)
     Chunk* chunks;
-    float* seg_state;                  // [cap_slots][H][64][128]: what a cut sequence's segments start from
-    float* seg_decay;                  // [cap_slots][H]
+    float* seg_state;                  // [1 or 2][cap_slots][H][64][128]: what a cut sequence's segments start from
+    float* seg_decay;                  // [1 or 2][cap_slots][H] (1: the gradient's, backward in time)
 };
 
 __device__ __forceinline__ bool get_item(const Args& a, int i, Item& it) {
@@ -224,26 +224,41 @@ __device__ __forceinline__ void state_store(const StateFrag& s, float* dst, int 
         *reinterpret_cast<float2*>(p + 8 * kN + 8 * j) = make_float2(s.v[j][2], s.v[j][3]);
     }
 }
-// the state as bf16 high and low parts (2^-17 of each value), [64][128] each, high part first
-__device__ __forceinline__ void state_store_split(const StateFrag& s, uint16_t* dst, int w, int lane) {
-    uint16_t* p = dst + (16 * w + (lane >> 2)) * kN + 2 * (lane & 3);
+// The warp's 16 rows of the state as bf16 high and low parts (2^-17 of each value) to dst, [64][128] each, high
+// part first; staged in 4 KB of the warp's own shared memory, so that whole 256-byte rows go out.
+__device__ __forceinline__ void state_store_split(const StateFrag& s, uint16_t* dst, uint32_t stage, int w, int lane) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        uint32_t h0, l0, h1, l1;
-        split_bf16x2(s.v[j][0], s.v[j][1], h0, l0);
-        split_bf16x2(s.v[j][2], s.v[j][3], h1, l1);
-        *reinterpret_cast<uint32_t*>(p + 8 * j) = h0;
-        *reinterpret_cast<uint32_t*>(p + 8 * kN + 8 * j) = h1;
-        *reinterpret_cast<uint32_t*>(p + kStateElems + 8 * j) = l0;
-        *reinterpret_cast<uint32_t*>(p + kStateElems + 8 * kN + 8 * j) = l1;
+    for (int part = 0; part < 2; ++part) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            uint32_t q[4], lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                split_bf16x2(s.v[j + (i >> 1)][2 * (i & 1)], s.v[j + (i >> 1)][2 * (i & 1) + 1], q[i], lo);
+                if (part) q[i] = lo;
+            }
+            // matrices: rows 0..7 and 8..15 of tile j, then of tile j + 1
+            const int mi = lane >> 3;
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+                         ::"r"(tile256(stage, 8 * (mi & 1) + (lane & 7), j + (mi >> 1))), "r"(q[0]), "r"(q[1]), "r"(q[2]),
+                         "r"(q[3]) : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 2 * i + (lane >> 4), pc = lane & 15;
+            *reinterpret_cast<uint4*>(dst + part * kStateElems + (16 * w + row) * kN + 8 * pc) =
+                ptx::lds128(tile256(stage, row, pc));
+        }
     }
+    __syncwarp();
 }
 
 // s = keep s + sum_t wt[t] u_t v_t^T over the chunk: u tile [64][64], v tile [64][128]. The fp32 products
 // wt u enter the MMAs as three bf16 parts, so that the state keeps fp32's precision.
-template <bool USE_DT>
 __device__ __forceinline__ void state_update(StateFrag& s, float keep, uint32_t u, uint32_t v, const float* wt,
-                                             const float* dt, int w, int lane) {
+                                             const float* dt, bool use_dt, int w, int lane) {
 #pragma unroll
     for (int j = 0; j < 16; ++j)
 #pragma unroll
@@ -254,7 +269,7 @@ __device__ __forceinline__ void state_update(StateFrag& s, float keep, uint32_t 
         frag_at<128>(u, k, 16 * w, lane, r);
         float2 w0 = *reinterpret_cast<const float2*>(wt + k + 2 * (lane & 3));
         float2 w1 = *reinterpret_cast<const float2*>(wt + k + 8 + 2 * (lane & 3));
-        if (USE_DT) {
+        if (use_dt) {
             const float2 d0 = *reinterpret_cast<const float2*>(dt + k + 2 * (lane & 3));
             const float2 d1 = *reinterpret_cast<const float2*>(dt + k + 8 + 2 * (lane & 3));
             w0 = make_float2(__fmul_rn(w0.x, d0.x), __fmul_rn(w0.y, d0.y));
@@ -265,16 +280,18 @@ __device__ __forceinline__ void state_update(StateFrag& s, float keep, uint32_t 
             const float2 ww = i < 2 ? w0 : w1;
             split3(__fmul_rn(bf16_lo(r[i]), ww.x), __fmul_rn(bf16_hi(r[i]), ww.y), hi[i], mid[i], lo[i]);
         }
+        // eight accumulators at a time, so that one's three MMAs are far apart
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            uint32_t bb[4];
-            frag_bt<256>(v, k, 8 * j, lane, bb);
-            mma(s.v[j], lo, bb[0], bb[1]);
-            mma(s.v[j + 1], lo, bb[2], bb[3]);
-            mma(s.v[j], mid, bb[0], bb[1]);
-            mma(s.v[j + 1], mid, bb[2], bb[3]);
-            mma(s.v[j], hi, bb[0], bb[1]);
-            mma(s.v[j + 1], hi, bb[2], bb[3]);
+        for (int j = 0; j < 16; j += 8) {
+            uint32_t bb[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) frag_bt<256>(v, k, 8 * (j + 2 * q), lane, bb[q]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) mma(s.v[j + q], lo, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) mma(s.v[j + q], mid, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) mma(s.v[j + q], hi, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
         }
     }
 }
@@ -289,21 +306,19 @@ dfssm_status check_call(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in
 dfssm_status setup();
 Args make_args(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int total, int nseq, const Plan& p, uint8_t* ws);
 cudaError_t launch_table(const Args& a, cudaStream_t s);
-// the start states of the segments of cut sequences (nothing to do when none can be cut)
-cudaError_t launch_segment_starts(const Args& a, cudaStream_t s);
-
 struct StateArgs {
-    const uint16_t* u;         // dy
-    int64_t ldu;
-    const float* start;        // [nseq][H][64][128] gradient of the final states, or NULL
-    uint16_t* states;          // [chunks][H][2][64][128]: the gradient of every chunk's end state
-    float* out;                // [nseq][H][64][128] gradient of the initial states, or NULL
+    const uint16_t* dy;
+    int64_t lddy;
+    const float* dfinal;       // [nseq][H][64][128] gradient of the final states, or NULL
+    uint16_t* states;          // [chunks][H][2][64][128]: the state in front of every chunk
+    uint16_t* dstates;         // the same: the gradient of the state behind it
+    float* dinit;              // [nseq][H][64][128] gradient of the initial states, or NULL
 };
-// the state's gradient backward in time, every chunk's to o.states
-cudaError_t launch_states_back(const Args& a, const StateArgs& o, cudaStream_t s);
-// the states in front of every chunk, and dy_t . (y_t - d_skip x_t) per token and head
-cudaError_t launch_states_forward(const Args& a, uint16_t* states, const uint16_t* dy, int64_t lddy, float* ydy,
-                                  cudaStream_t s);
+// the start states of the segments of cut sequences (nothing to do when none can be cut); directions 2: of their
+// gradients too
+cudaError_t launch_segment_starts(const Args& a, const StateArgs& o, int directions, cudaStream_t s);
+// the states and, backward in time, their gradients at every chunk
+cudaError_t launch_states(const Args& a, const StateArgs& o, cudaStream_t s);
 cudaError_t setup_bwd();
 size_t bwd_workspace(const dfssm_scan_dims* dims, int total, int nseq);
 

@@ -11,11 +11,12 @@
 //   dB   = W^T C + sum_h dt_s exp(cum_64 - cum_s) x_s dS
 //   dC   = W B   + sum_h exp(cum_t) dy_t S
 // G is shared by the heads of a group and W, summed over them in registers, multiplies C and B once
-// per chunk, not once per head. da_t splits into what passes over token t:
-//   da_t = sum_{t' >= t} r_t' - sum_{s >= t} k_s + sum_s w_s + exp(cum_64) <dS, S>
-// with r_t = dy_t . (y_t - d_skip x_t) (from the forward kernel's run), k_s = dt_s x_s . dx'_s the
-// whole of token s's own contribution and w_s its part that leaves the chunk, both from the
-// accumulators of dx. Nothing is summed over more than a chunk before it is used.
+// per chunk, not once per head. da_t is what passes over token t:
+//   da_t = sum_{t' >= t, s < t} E[t', s] + sum_{t' >= t} z_t' + sum_{s < t} w_s + exp(cum_64) <dS, S>
+// with E = M o Z dt_s, z_t = exp(cum_t) dy_t . S C_t (from the accumulators of dC) and w_s = dt_s exp(cum_64 -
+// cum_s) x_s . dS B_s (from those of dx). The first sum is that of E's row sums from t on less that of its
+// column sums from t on; both come from the same fp32 values, so that what cancels cancels (taken from
+// dy . y and x . dx, which carry different roundings, d a_log was off by 3e-4).
 //
 // scan_grad_kernel: CTA (chunk, group, split of the group's heads), 8 warps, one head after another with the
 // next head's tiles on the way (cp.async), bf16 warp MMAs; fp32 operands (M, W, S, dS) as two bf16
@@ -35,7 +36,6 @@ struct GradArgs {
     int64_t lddy;
     const uint16_t* s_in;      // [chunks][H][2][64][128] states in front of the chunks
     const uint16_t* ds_out;    // the same: gradients behind them
-    const float* ydy;          // [total][H]
     uint16_t* dx;
     int64_t lddx;
     uint16_t* ddt;
@@ -52,8 +52,10 @@ constexpr int kTx = 0, kTy = 8192, kTs = 16384, kTd = 16384 + 32768, kTile = 163
 struct HeadVec {
     Decay d;
     float sig[kQ];             // d softplus
-    float r[kQ];
     float k[4][kQ], wl[4][kQ]; // x . dx' of the four channel slices: whole, and the part that leaves the chunk
+    float z[4][kQ];            // C . (dy S) of the four state slices
+    float row[4][kQ];          // sums of E over s, per block of 16 s
+    float col[2][kQ];          // sums of E over t, per block of 32 t
     float skip[8];             // per warp: sum dy x
     float dot[8];              // per warp: <dS, S>
 };
@@ -104,7 +106,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             const int t = 2 * lane + i;
             const float x = __fadd_rn(i ? r1 : r0, bias);
             v.sig[t] = x > 20.0f ? 1.0f : __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
-            v.r[t] = t < n ? o.ydy[(int64_t)(t0 + t) * a.nheads + h] : 0.0f;
         }
     };
     load_tile<128, kThreads>(s_b, a.b + (int64_t)g * kN, a.ldb, t0, n, tid);
@@ -173,19 +174,37 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             }
             const int s = 16 * ws + (lane >> 2);
             const float cs0 = v.d.cum[s], cs1 = v.d.cum[s + 8], ds0 = v.d.dt[s], ds1 = v.d.dt[s + 8];
+            float col0 = 0.0f, col1 = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = 32 * wt + 8 * j + 2 * (lane & 3);
-                if (32 * wt + 16 * (j >> 1) < 16 * ws) continue;
+                if (32 * wt + 16 * (j >> 1) < 16 * ws) {
+                    if (lane < 4) *reinterpret_cast<float2*>(v.row[ws] + t) = make_float2(0.0f, 0.0f);
+                    continue;
+                }
                 const float2 ct = *reinterpret_cast<const float2*>(v.d.cum + t);
                 float l[4];
                 l[0] = t >= s ? exp2f(__fsub_rn(ct.x, cs0)) : 0.0f;
                 l[1] = t + 1 >= s ? exp2f(__fsub_rn(ct.y, cs0)) : 0.0f;
                 l[2] = t >= s + 8 ? exp2f(__fsub_rn(ct.x, cs1)) : 0.0f;
                 l[3] = t + 1 >= s + 8 ? exp2f(__fsub_rn(ct.y, cs1)) : 0.0f;
+                const float m[4] = {__fmul_rn(G[j][0], l[0]), __fmul_rn(G[j][1], l[1]), __fmul_rn(G[j][2], l[2]),
+                                    __fmul_rn(G[j][3], l[3])};
                 uint32_t m0, n0, m1, n1;
-                split_bf16x2(__fmul_rn(G[j][0], l[0]), __fmul_rn(G[j][1], l[1]), m0, n0);
-                split_bf16x2(__fmul_rn(G[j][2], l[2]), __fmul_rn(G[j][3], l[3]), m1, n1);
+                split_bf16x2(m[0], m[1], m0, n0);
+                split_bf16x2(m[2], m[3], m1, n1);
+                // E, its sums over the warp's s for the thread's two t, and over the thread's t
+                const float e[4] = {__fmul_rn(__fmul_rn(m[0], ds0), Z[j][0]), __fmul_rn(__fmul_rn(m[1], ds0), Z[j][1]),
+                                    __fmul_rn(__fmul_rn(m[2], ds1), Z[j][2]), __fmul_rn(__fmul_rn(m[3], ds1), Z[j][3])};
+                col0 = __fadd_rn(col0, __fadd_rn(e[0], e[1]));
+                col1 = __fadd_rn(col1, __fadd_rn(e[2], e[3]));
+                float2 rs = make_float2(__fadd_rn(e[0], e[2]), __fadd_rn(e[1], e[3]));
+#pragma unroll
+                for (int q = 4; q < 32; q <<= 1) {
+                    rs.x = __fadd_rn(rs.x, __shfl_xor_sync(0xffffffffu, rs.x, q));
+                    rs.y = __fadd_rn(rs.y, __shfl_xor_sync(0xffffffffu, rs.y, q));
+                }
+                if (lane < 4) *reinterpret_cast<float2*>(v.row[ws] + t) = rs;
                 const uint32_t p0 = tile128(s_m, s, 4 * wt + j) + 4 * (lane & 3);
                 const uint32_t p1 = tile128(s_m, s + 8, 4 * wt + j) + 4 * (lane & 3);
                 ptx::sts32(p0, m0);
@@ -196,6 +215,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 W[j][1] = __fmaf_rn(Z[j][1], __fmul_rn(l[1], ds0), W[j][1]);
                 W[j][2] = __fmaf_rn(Z[j][2], __fmul_rn(l[2], ds1), W[j][2]);
                 W[j][3] = __fmaf_rn(Z[j][3], __fmul_rn(l[3], ds1), W[j][3]);
+            }
+#pragma unroll
+            for (int q = 1; q < 4; q <<= 1) {
+                col0 = __fadd_rn(col0, __shfl_xor_sync(0xffffffffu, col0, q));
+                col1 = __fadd_rn(col1, __shfl_xor_sync(0xffffffffu, col1, q));
+            }
+            if ((lane & 3) == 0) {
+                v.col[wt][s] = col0;
+                v.col[wt][s + 8] = col1;
             }
         }
         __syncthreads();                          // M^T is there
@@ -325,6 +353,27 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 const int r = rw + 16 * i + (lane >> 2);
                 const float e0 = side ? __fmul_rn(v.d.dt[r], v.d.left[r]) : v.d.done[r];
                 const float e1 = side ? __fmul_rn(v.d.dt[r + 8], v.d.left[r + 8]) : v.d.done[r + 8];
+                if (side == 0) {                  // C_t . (dy S)_t over the warp's states
+                    float z0 = 0.0f, z1 = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t c0, c1;
+                        const uint32_t at = 4 * (lane & 3);
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c0) : "r"(tile256(s_c, r, (cw >> 3) + j) + at));
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c1) : "r"(tile256(s_c, r + 8, (cw >> 3) + j) + at));
+                        z0 = __fmaf_rn(T[i][j][0], bf16_lo(c0), __fmaf_rn(T[i][j][1], bf16_hi(c0), z0));
+                        z1 = __fmaf_rn(T[i][j][2], bf16_lo(c1), __fmaf_rn(T[i][j][3], bf16_hi(c1), z1));
+                    }
+#pragma unroll
+                    for (int q = 1; q < 4; q <<= 1) {
+                        z0 = __fadd_rn(z0, __shfl_xor_sync(0xffffffffu, z0, q));
+                        z1 = __fadd_rn(z1, __shfl_xor_sync(0xffffffffu, z1, q));
+                    }
+                    if ((lane & 3) == 0) {
+                        v.z[w >> 1][r] = z0;
+                        v.z[w >> 1][r + 8] = z1;
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float(&acc)[4] = side ? dB[i][j] : dC[i][j];
@@ -360,32 +409,37 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         // ---- d dt: lane l has tokens 2 l, 2 l + 1
         if (w == 0) {
             const float A = -expf(a.a_log[h]);
-            float kp[2], q[2], wsum = 0.0f, dot = 0.0f, sk = 0.0f;
+            float kp[2], q[2], wl[2], dot = 0.0f, sk = 0.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                const float dt = v.d.dt[t];
                 kp[i] = __fadd_rn(__fadd_rn(v.k[0][t], v.k[1][t]), __fadd_rn(v.k[2][t], v.k[3][t]));
-                const float wl = __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t]));
-                wsum = __fmaf_rn(dt, wl, wsum);
-                q[i] = __fmaf_rn(-dt, kp[i], v.r[t]);
+                wl[i] = __fmul_rn(v.d.dt[t],
+                                  __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t])));
+                const float z = __fmul_rn(v.d.done[t],
+                                          __fadd_rn(__fadd_rn(v.z[0][t], v.z[1][t]), __fadd_rn(v.z[2][t], v.z[3][t])));
+                const float row = __fadd_rn(__fadd_rn(v.row[0][t], v.row[1][t]), __fadd_rn(v.row[2][t], v.row[3][t]));
+                q[i] = __fadd_rn(__fsub_rn(row, __fadd_rn(v.col[0][t], v.col[1][t])), z);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dot = __fadd_rn(dot, v.dot[i]);
                 sk = __fadd_rn(sk, v.skip[i]);
             }
-            float suf = __fadd_rn(q[0], q[1]);      // inclusive sum from the right
+            // what enters at or after t and leaves it (from the right), what enters before t (from the left)
+            float suf = __fadd_rn(q[0], q[1]), pre = __fadd_rn(wl[0], wl[1]);
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
-                const float u = __shfl_down_sync(0xffffffffu, suf, s);
+                const float u = __shfl_down_sync(0xffffffffu, suf, s), x = __shfl_up_sync(0xffffffffu, pre, s);
                 if (lane + s < 32) suf = __fadd_rn(suf, u);
-                wsum = __fadd_rn(wsum, __shfl_xor_sync(0xffffffffu, wsum, s));
+                if (lane >= s) pre = __fadd_rn(pre, x);
             }
-            float after = __shfl_down_sync(0xffffffffu, suf, 1);
+            float after = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
             if (lane == 31) after = 0.0f;
-            const float over = __fmaf_rn(v.d.done[kQ - 1], dot, wsum);
-            const float da[2] = {__fadd_rn(suf, over), __fadd_rn(__fadd_rn(q[1], after), over)};
+            if (lane == 0) before = 0.0f;
+            const float over = __fmul_rn(v.d.done[kQ - 1], dot);
+            const float da[2] = {__fadd_rn(__fadd_rn(suf, before), over),
+                                 __fadd_rn(__fadd_rn(__fadd_rn(q[1], after), __fadd_rn(before, wl[0])), over)};
             float sb = 0.0f, sa = 0.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -533,7 +587,7 @@ Split choose_split(int cap_chunks, int ngroups, int per_group) {
 }
 
 struct BwdWs {
-    size_t s_in, ds, ydy, db, dc, sums, total;
+    size_t s_in, ds, db, dc, sums, total;
 };
 BwdWs bwd_ws(const dfssm_scan_dims* d, int total, int nseq, const Plan& p) {
     BwdWs w{};
@@ -544,8 +598,6 @@ BwdWs bwd_ws(const dfssm_scan_dims* d, int total, int nseq, const Plan& p) {
     o = up256(o + states);
     w.ds = o;
     o = up256(o + states);
-    w.ydy = o;
-    o = up256(o + (size_t)total * d->nheads * 4);
     w.db = o;
     o = up256(o + (size_t)sp.splits * total * d->ngroups * kN * 4);
     w.dc = o;
@@ -602,10 +654,8 @@ extern "C" dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const df
     o.lddy = dy_stride;
     uint16_t* s_in = reinterpret_cast<uint16_t*>(ws + w.s_in);
     uint16_t* ds = reinterpret_cast<uint16_t*>(ws + w.ds);
-    float* ydy = reinterpret_cast<float*>(ws + w.ydy);
     o.s_in = s_in;
     o.ds_out = ds;
-    o.ydy = ydy;
     o.dx = static_cast<uint16_t*>(gr->dx);
     o.lddx = gr->dx_stride;
     o.ddt = static_cast<uint16_t*>(gr->ddt);
@@ -616,10 +666,8 @@ extern "C" dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const df
     const Split sp = choose_split(p.cap_chunks, dims->ngroups, dims->nheads / dims->ngroups);
     o.splits = sp.splits;
     o.per_split = sp.per;
-    StateArgs back{o.dy, dy_stride, dfinal_state, ds, gr->dinit_state};
-    if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, s) != cudaSuccess ||
-        launch_states_forward(a, s_in, o.dy, dy_stride, ydy, s) != cudaSuccess ||
-        launch_states_back(a, back, s) != cudaSuccess)
+    const StateArgs st_args{o.dy, dy_stride, dfinal_state, s_in, ds, gr->dinit_state};
+    if (launch_table(a, s) != cudaSuccess || launch_states(a, st_args, s) != cudaSuccess)
         return DFSSM_ERR_CUDA;
     scan_grad_kernel<<<p.cap_chunks * dims->ngroups * sp.splits, kThreads, kGradSmem, s>>>(a, o);
     scan_sum_kernel<<<dim3(p.cap_chunks, 2), 256, 0, s>>>(a, o.db_part, o.dc_part, sp.splits,
