@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 8192;
-constexpr int kBwdCtasPerSm = 4;
+constexpr int kBwdCtasPerSm = 3;                   // what the registers of the usual widths allow
 constexpr int kBwdMaxCtas = 148 * kBwdCtasPerSm;   // partial rows of dw in the workspace
 
 __device__ __forceinline__ void load8(const float* p, float v[8]) {
@@ -54,8 +54,8 @@ __device__ __forceinline__ void load8_bf16(const void* base, int64_t i, float v[
     }
 }
 
-// Sum (or max of non-negative bit patterns) over the TPR threads of a row; every thread gets it.
-// `red` holds one slot per warp; a second use needs another array (no barrier behind the read).
+// Sum, or max of bit patterns of |x|, over the TPR threads of a row; every thread gets it. `red` holds one
+// slot per warp; a second use needs another array (no barrier behind the read).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
@@ -193,43 +193,66 @@ struct BwdArgs {
     int dout_bf16;
 };
 
-template <int TPR, int NV>
+// One row group's loads in flight: the next rows' while the current ones are reduced and stored
+// (16,384 x 2048 with a bf16 gradient and a stream gradient: 94 -> 80 us).
+template <int NV, bool BF>
+struct BwdRow {
+    float r[NV][8];
+    uint32_t g[NV][BF ? 4 : 8];
+    float ds[NV][8];
+};
+
+template <int TPR, int NV, bool BF>
+__device__ __forceinline__ void bwd_load(const BwdArgs& a, int row, int sub, BwdRow<NV, BF>& v) {
+    const int64_t base = (int64_t)row * a.d;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c = 8 * (sub + TPR * n);
+        const bool in = row < a.m && c < a.d;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v.r[n][k] = v.ds[n][k] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < (BF ? 4 : 8); ++k) v.g[n][k] = 0u;
+        if (!in) continue;
+        load8(a.r + base + c, v.r[n]);
+        if (BF) {
+            const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + base + c);
+            v.g[n][0] = q.x; v.g[n][1] = q.y; v.g[n][2] = q.z; v.g[n][3] = q.w;
+        } else {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.dout) + base + c);
+            const uint4 x = p[0], y = p[1];
+            v.g[n][0] = x.x; v.g[n][1] = x.y; v.g[n][2] = x.z; v.g[n][3] = x.w;
+            v.g[n][BF ? 0 : 4] = y.x; v.g[n][BF ? 0 : 5] = y.y; v.g[n][BF ? 0 : 6] = y.z; v.g[n][BF ? 0 : 7] = y.w;
+        }
+        if (a.dstream) load8(a.dstream + base + c, v.ds[n]);
+    }
+}
+
+template <int NV, bool BF>
+__device__ __forceinline__ float bwd_g(const BwdRow<NV, BF>& v, int n, int k) {
+    if (BF) return (k & 1) ? bf16_hi(v.g[n][k >> 1]) : bf16_lo(v.g[n][k >> 1]);
+    return __uint_as_float(v.g[n][BF ? 0 : k]);
+}
+
+template <int TPR, int NV, bool BF>
 __global__ void __launch_bounds__(kThreads) add_rmsnorm_bwd_kernel(const BwdArgs a) {
     constexpr int kRows = kThreads / TPR;
-    __shared__ float red[2][2][kThreads / 32];   // [row parity][sum]: a slot is reused two barriers later
-    const int sub = threadIdx.x % TPR;
+    __shared__ float2 red[2][kThreads / 32];     // [row parity]: a slot is reused two barriers later
+    const int sub = threadIdx.x % TPR, in_row = threadIdx.x / TPR;
     float dw[NV][8];
 #pragma unroll
     for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int k = 0; k < 8; ++k) dw[n][k] = 0.0f;
     int par = 0;
+    BwdRow<NV, BF> cur, nxt;
+    bwd_load<TPR, NV, BF>(a, blockIdx.x * kRows + in_row, sub, cur);
     for (int row0 = blockIdx.x * kRows; row0 < a.m; row0 += gridDim.x * kRows, par ^= 1) {
-        const int row = row0 + threadIdx.x / TPR;
+        const int row = row0 + in_row;
         const bool live = row < a.m;
         const int64_t base = (int64_t)row * a.d;
-        float r[NV][8], g[NV][8];
+        bwd_load<TPR, NV, BF>(a, min(row + (int)gridDim.x * kRows, a.m), sub, nxt);
         float ss = 0.0f, gr = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int c = 8 * (sub + TPR * n);
-            if (live && c < a.d) {
-                load8(a.r + base + c, r[n]);
-                if (a.dout_bf16) load8_bf16(a.dout, base + c, g[n]);
-                else load8(static_cast<const float*>(a.dout) + base + c, g[n]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[n][k] = g[n][k] = 0.0f;
-            }
-        }
-        float dso[NV][8];
-        if (a.dstream) {
-#pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const int c = 8 * (sub + TPR * n);
-                if (live && c < a.d) load8(a.dstream + base + c, dso[n]);
-            }
-        }
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int c = 8 * (sub + TPR * n);
@@ -240,12 +263,26 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_bwd_kernel(const BwdArgs
                 for (int k = 0; k < 8; ++k) w[k] = 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                ss = __fmaf_rn(r[n][k], r[n][k], ss);
-                gr = __fmaf_rn(__fmul_rn(g[n][k], w[k]), r[n][k], gr);
+                ss = __fmaf_rn(cur.r[n][k], cur.r[n][k], ss);
+                gr = __fmaf_rn(__fmul_rn(bwd_g(cur, n, k), w[k]), cur.r[n][k], gr);
             }
         }
-        ss = row_sum<TPR>(ss, red[par][0]);
-        gr = row_sum<TPR>(gr, red[par][1]);
+#pragma unroll
+        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+            ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+            gr = __fadd_rn(gr, __shfl_xor_sync(0xffffffffu, gr, o));
+        }
+        if (TPR > 32) {
+            if ((threadIdx.x & 31) == 0) red[par][threadIdx.x >> 5] = make_float2(ss, gr);
+            __syncthreads();
+            ss = red[par][0].x;
+            gr = red[par][0].y;
+#pragma unroll
+            for (int w = 1; w < kThreads / 32; ++w) {
+                ss = __fadd_rn(ss, red[par][w].x);
+                gr = __fadd_rn(gr, red[par][w].y);
+            }
+        }
         const float f = norm_factor(ss, a.d, a.eps);
         const float c3 = __fmul_rn(__fmul_rn(__fmul_rn(f, f), f), __fdiv_rn(gr, (float)a.d));
 #pragma unroll
@@ -256,12 +293,14 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_bwd_kernel(const BwdArgs
             load8(a.w + c, w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                o[k] = __fmaf_rn(-c3, r[n][k], __fmul_rn(f, __fmul_rn(g[n][k], w[k])));
-                if (a.dstream) o[k] = __fadd_rn(o[k], dso[n][k]);
-                dw[n][k] = __fmaf_rn(g[n][k], __fmul_rn(r[n][k], f), dw[n][k]);
+                const float g = bwd_g(cur, n, k);
+                o[k] = __fmaf_rn(-c3, cur.r[n][k], __fmul_rn(f, __fmul_rn(g, w[k])));
+                if (a.dstream) o[k] = __fadd_rn(o[k], cur.ds[n][k]);
+                dw[n][k] = __fmaf_rn(g, __fmul_rn(cur.r[n][k], f), dw[n][k]);
             }
             store8(a.dr + base + c, o);
         }
+        cur = nxt;
     }
     if (!a.part) return;
     // the CTA's partial dw: its row groups added in order
@@ -285,20 +324,20 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_bwd_kernel(const BwdArgs
     }
 }
 
-// dw[c] = sum over the partial rows: 32 columns per CTA, 8 row groups added in order
-__global__ void __launch_bounds__(kThreads) dw_reduce_kernel(const float* __restrict__ part, int n, int d, float* dw) {
-    __shared__ float s[8][33];
+// dw[c] = sum over the partial rows: 32 columns per CTA, 32 row groups added in order
+__global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* __restrict__ part, int n, int d, float* dw) {
+    __shared__ float s[32][33];
     const int cl = threadIdx.x & 31, g = threadIdx.x >> 5, c = blockIdx.x * 32 + cl;
     float acc = 0.0f;
     if (c < d) {
 #pragma unroll 8
-        for (int i = g; i < n; i += 8) acc = __fadd_rn(acc, part[(int64_t)i * d + c]);
+        for (int i = g; i < n; i += 32) acc = __fadd_rn(acc, part[(int64_t)i * d + c]);
     }
     s[g][cl] = acc;
     __syncthreads();
     if (g == 0 && c < d) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) acc = __fadd_rn(acc, s[k][cl]);
+        for (int k = 1; k < 32; ++k) acc = __fadd_rn(acc, s[k][cl]);
         dw[c] = acc;
     }
 }
@@ -321,7 +360,8 @@ template <int TPR, int NV>
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t s) {
     constexpr int rows = kThreads / TPR;
     const size_t smem = TPR == kThreads ? 0 : sizeof(float) * rows * TPR * NV * 8;   // at most 32 KB
-    add_rmsnorm_bwd_kernel<TPR, NV><<<bwd_ctas(a.d, a.m), kThreads, smem, s>>>(a);
+    if (a.dout_bf16) add_rmsnorm_bwd_kernel<TPR, NV, true><<<bwd_ctas(a.d, a.m), kThreads, smem, s>>>(a);
+    else add_rmsnorm_bwd_kernel<TPR, NV, false><<<bwd_ctas(a.d, a.m), kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -386,7 +426,7 @@ extern "C" dfssm_status dfssm_add_rmsnorm_bwd(const float* norm_w, int32_t d, fl
     else if (d <= 4096) e = launch_bwd<256, 2>(a, s);
     else e = launch_bwd<256, 4>(a, s);
     if (e == cudaSuccess && dnorm_w) {
-        dw_reduce_kernel<<<(d + 31) / 32, kThreads, 0, s>>>(a.part, bwd_ctas(d, m), d, dnorm_w);
+        dw_reduce_kernel<<<(d + 31) / 32, 1024, 0, s>>>(a.part, bwd_ctas(d, m), d, dnorm_w);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;

@@ -39,6 +39,9 @@ namespace {
 
 constexpr int kBM = 128;                 // tokens per tile (TMEM lanes)
 constexpr int kBN = 256;                 // table rows (logits) or channels (gradient) per tile
+// With one token tile the table is streamed once and a call has few tiles: 192 rows give 262 tiles for 50,288 rows,
+// two for nearly each of 148 CTAs, where 256 rows give 197, two for a third of them (1 token: 27 -> 21 us).
+constexpr int kBNFew = 192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -47,14 +50,15 @@ constexpr int kLgStages = 4;
 constexpr int kLgA = kBM * 128, kLgB = kBN * 128, kLgStage = kLgA + kLgB;     // 128 K bytes per stage
 constexpr int kLgThreads = 12 * 32;      // TMA, MMA, 2 idle warps; 8 epilogue warps
 constexpr int kLgEpi = 256;
-constexpr int kLgSmem = kLgStages * kLgStage + 2 * kBN * 4 + 256 + 1024;
+constexpr int kLgOut = 8 * 2048;         // kGrad: an epilogue warp's 32 tokens x 32 columns
+constexpr int kLgSmem = kLgStages * kLgStage + kLgOut + 2 * kBN * 4 + 256 + 1024;
 
 // -- gradient kernel
-constexpr int kDhStages = 4;
-constexpr int kDhA = kBM * 128, kDhB = kBN * 128, kDhStage = kDhA + kDhB;     // 64 K values per stage
+constexpr int kDhA = kBM * 128, kDhB = kBN * 128;      // 64 K values per stage and accumulator
 constexpr int kDhConv = 256;             // converter threads (8 warps), the epilogue afterwards
 constexpr int kDhThreads = 4 * 32 + kDhConv;
-constexpr int kDhSmem = kDhStages * kDhStage + 256 + 1024;
+// 4 stages of one A tile and B, or 3 of two and B; barriers; the accumulators' staging rows
+constexpr int kDhSmem = 192 * 1024 + 256 + 8 * 4096 + 1024;
 
 constexpr int kTokBlock = 2048;          // tokens whose gradient is worked on at a time
 constexpr size_t kGradBytes = 80u << 20; // about the fp16 piece that stays in the 126 MB L2
@@ -63,7 +67,8 @@ struct LogitsArgs {
     const float* scale;
     const float* sx;
     int vocab, d, m;
-    int v0, v_end;                       // table rows of this call (a multiple of kBN at v0)
+    int bn;                              // table rows per tile: kBN or kBNFew
+    int v0, v_end;                       // table rows of this call
     float2* part;                        // kLse: [2 * v tiles][m]
     const float* lse;                    // kGrad
     const int32_t* targets;              // kGrad
@@ -72,6 +77,13 @@ struct LogitsArgs {
     int ldg;
     uint32_t* err;
 };
+
+// 2^x to 2 ulp, 0 below 2^-126
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 __device__ __forceinline__ bool is_token(int target, int vocab) { return target >= 0 && target < vocab; }
 
@@ -95,19 +107,23 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                    const LogitsArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    float* s_scale = reinterpret_cast<float*>(smem + kLgStages * kLgStage);          // [2][kBN]
+    const uint32_t s_out = ptx::smem_u32(smem) + kLgStages * kLgStage;
+    float* s_scale = reinterpret_cast<float*>(smem + kLgStages * kLgStage + kLgOut); // [2][kBN]
     uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 2 * kBN);                 // TMA bytes
     uint64_t* empty = full + kLgStages;                                              // MMA commit
     uint64_t* acc_full = empty + kLgStages;                                          // [2] MMA commit
-    uint64_t* acc_empty = acc_full + 2;                                              // [2] epilogue threads
+    uint64_t* acc_empty = acc_full + 2;                                              // [2] one arrival per epilogue warp
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_tt = (a.m + kBM - 1) / kBM;
-    const int n_tiles = n_tt * ((a.v_end - a.v0 + kBN - 1) / kBN);
+    const int n_tiles = n_tt * ((a.v_end - a.v0 + a.bn - 1) / a.bn);
+    const int hw = a.bn / 2;                          // columns of an epilogue warp's half: a multiple of 32
     const int n_k = (a.d + 127) / 128;
 
+    // what follows in the stream may come in as CTAs end here; it waits for the whole grid before it reads
+    ptx::pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kLgStages; ++s) {
             ptx::mbar_init(&full[s], 1);
@@ -115,7 +131,7 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&acc_full[b], 1);
-            ptx::mbar_init(&acc_empty[b], kLgEpi);
+            ptx::mbar_init(&acc_empty[b], kLgEpi / 32);
         }
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -141,9 +157,9 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         break;
                     }
                     uint8_t* st = smem + s * kLgStage;
-                    ptx::mbar_arrive_expect_tx(&full[s], kLgStage);
+                    ptx::mbar_arrive_expect_tx(&full[s], kLgA + a.bn * 128);
                     ptx::tma_load_2d(st, &map_q, k * 128, tt * kBM, &full[s]);
-                    ptx::tma_load_2d(st + kLgA, &map_e, k * 128, a.v0 + vt * kBN, &full[s]);
+                    ptx::tma_load_2d(st + kLgA, &map_e, k * 128, a.v0 + vt * a.bn, &full[s]);
                 }
             }
             // after a wait that gave up: the copies still in flight land before the CTA ends
@@ -154,8 +170,8 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     } else if (warp == 1) {
         if (lane == 0) {
             // kind::i8: D s32, A and B s8, both K-major
-            constexpr uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kBN >> 3) << 17) |
-                                       ((uint32_t)(kBM >> 4) << 24);
+            const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(a.bn >> 3) << 17) |
+                                   ((uint32_t)(kBM >> 4) << 24);
             int it = 0, tc = 0;
             bool ok = true;
             for (int tile = blockIdx.x; tile < n_tiles && ok && !*abort_flag; tile += gridDim.x, ++tc) {
@@ -188,6 +204,7 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
     } else if (warp >= 4) {
         const int e = threadIdx.x - 4 * 32, q4 = warp & 3, half = (warp - 4) >> 2;
+        if (MODE == kGrad) ptx::pdl_wait();        // max |scale|, and the piece's readers before it
         float gk = 0.0f;
         if (MODE == kGrad) gk = grad_scale(*a.smax);
         int tc = 0;
@@ -195,9 +212,9 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++tc) {
             const int vt = tile / n_tt, tt = tile - vt * n_tt;
             const int buf = tc & 1;
-            const int vbase = a.v0 + vt * kBN;
+            const int vbase = a.v0 + vt * a.bn;
             float* sc = s_scale + buf * kBN;
-            sc[e] = vbase + e < a.v_end ? a.scale[vbase + e] : 0.0f;
+            sc[e] = e < a.bn && vbase + e < a.v_end ? a.scale[vbase + e] : 0.0f;
             const int t = tt * kBM + 32 * q4 + lane;
             const bool live = t < a.m;
             const float k2 = live ? __fmul_rn(a.sx[t], kLog2e) : 0.0f;      // logits in units of log 2
@@ -217,16 +234,17 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
             ptx::tc_fence_after();
             float mx = -INFINITY, sum = 0.0f;
-            const int c_end = min(kBN / 2, a.v_end - vbase - half * (kBN / 2));     // live columns of this half
+            const int c_end = min(hw, a.v_end - vbase - half * hw);      // live columns of this half
 #pragma unroll 1
-            for (int c = 0; c < kBN / 2; c += 32) {
-                const int col = half * (kBN / 2) + c;
+            for (int c = 0; c < hw; c += 32) {
+                const int col = half * hw + c;
                 uint32_t r[32];
                 ptx::tmem_ld_32x32b_x32(tmem + (uint32_t)(buf * kBN + col) + ((uint32_t)(32 * q4) << 16), r);
                 ptx::tmem_ld_wait();
-                if (c + 32 == kBN / 2) {           // the last read of this accumulator
+                if (c + 32 == hw) {           // the last read of this accumulator
                     ptx::tc_fence_before();
-                    ptx::mbar_arrive(&acc_empty[buf]);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
                 }
                 float z[32];
 #pragma unroll
@@ -247,30 +265,45 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 32; ++i) cm = fmaxf(cm, z[i]);
                     const float ref = cm == -INFINITY ? 0.0f : cm;       // no live column yet: 2^(-inf - 0) = 0
-                    float s0 = __fmul_rn(sum, exp2f(__fsub_rn(mx, ref))), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+                    float s0 = __fmul_rn(sum, ex2(__fsub_rn(mx, ref))), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        s0 = __fadd_rn(s0, exp2f(__fsub_rn(z[i], ref)));
-                        s1 = __fadd_rn(s1, exp2f(__fsub_rn(z[i + 1], ref)));
-                        s2 = __fadd_rn(s2, exp2f(__fsub_rn(z[i + 2], ref)));
-                        s3 = __fadd_rn(s3, exp2f(__fsub_rn(z[i + 3], ref)));
+                        s0 = __fadd_rn(s0, ex2(__fsub_rn(z[i], ref)));
+                        s1 = __fadd_rn(s1, ex2(__fsub_rn(z[i + 1], ref)));
+                        s2 = __fadd_rn(s2, ex2(__fsub_rn(z[i + 2], ref)));
+                        s3 = __fadd_rn(s3, ex2(__fsub_rn(z[i + 3], ref)));
                     }
                     sum = __fadd_rn(__fadd_rn(s0, s1), __fadd_rn(s2, s3));
                     mx = cm;
-                } else if (live) {
+                } else {
                     uint32_t o[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        const float f0 = __fmul_rn(sc[col + i], gk), f1 = __fmul_rn(sc[col + i + 1], gk);
-                        const float g0 = counted && c + i < c_end ? __fmul_rn(exp2f(__fsub_rn(z[i], lse2)), f0) : 0.0f;
-                        const float g1 =
-                            counted && c + i + 1 < c_end ? __fmul_rn(exp2f(__fsub_rn(z[i + 1], lse2)), f1) : 0.0f;
+                        const float2 f = *reinterpret_cast<const float2*>(sc + col + i);
+                        const float g0 = counted && c + i < c_end
+                                             ? __fmul_rn(ex2(__fsub_rn(z[i], lse2)), __fmul_rn(f.x, gk)) : 0.0f;
+                        const float g1 = counted && c + i + 1 < c_end
+                                             ? __fmul_rn(ex2(__fsub_rn(z[i + 1], lse2)), __fmul_rn(f.y, gk)) : 0.0f;
                         const __half2 h = __floats2half2_rn(g0, g1);
                         o[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-                    uint4* dst = reinterpret_cast<uint4*>(a.g + (int64_t)t * a.ldg + vt * kBN + col);
+                    // through the warp's staging rows (a token's 32 columns, 64 bytes, pieces swizzled by the row),
+                    // so that a store covers 64 bytes of 8 rows: straight from the accumulator's layout, 16 bytes
+                    // of 32 rows at a time, the stores bounded the kernel
+                    const uint32_t so = s_out + (uint32_t)((warp - 4) * 2048);
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i)
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                                     ::"r"(so + (uint32_t)(lane * 64 + 16 * (i ^ ((lane >> 1) & 3)))), "r"(o[4 * i]),
+                                     "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3]) : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r0 = 8 * i + (lane >> 2), pc = lane & 3, tr = tt * kBM + 32 * q4 + r0;
+                        const uint4 v = ptx::lds128(so + (uint32_t)(r0 * 64 + 16 * (pc ^ ((r0 >> 1) & 3))));
+                        if (tr < a.m) *reinterpret_cast<uint4*>(a.g + (int64_t)tr * a.ldg + vt * a.bn + col + 8 * pc) = v;
+                    }
                 }
             }
             if (MODE == kLse && live) a.part[(int64_t)(2 * vt + half) * a.m + t] = make_float2(mx, sum);
@@ -285,60 +318,78 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     }
 }
 
-// One warp per token: joins the token's (max, sum) pairs, lane i taking pairs i, i + 32, ... in
-// order, then a shuffle tree; the target's logit from an int32 dot product.
+// WARPS warps per token (one for many tokens, eight for few: the pairs of one token are a chain of
+// loads) join the token's (max, sum) pairs: lane i of warp w takes pairs i + 32 w, + 32 WARPS, ... in order, then a
+// shuffle tree, then the warps in order. The target's logit comes from an int32 dot product.
+template <int WARPS>
 __global__ void __launch_bounds__(256) xent_lse_kernel(const float2* __restrict__ part, int n_part,
                                                        const int8_t* __restrict__ table,
                                                        const float* __restrict__ scale, int vocab, int d,
                                                        const int8_t* __restrict__ q, const float* __restrict__ sx,
                                                        const int32_t* __restrict__ targets, int m, float* nll,
                                                        float* lse_out, uint32_t* err) {
-    const int t = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    if (t >= m) return;
-    float mx = -INFINITY, sum = 0.0f;
-    auto join = [&](float m2, float s2) {
-        const float nm = fmaxf(mx, m2);
-        const float ref = nm == -INFINITY ? 0.0f : nm;
-        sum = __fadd_rn(__fmul_rn(sum, exp2f(__fsub_rn(mx, ref))), __fmul_rn(s2, exp2f(__fsub_rn(m2, ref))));
-        mx = nm;
-    };
-    for (int i = lane; i < n_part; i += 32) {
-        const float2 p = part[(int64_t)i * m + t];
-        join(p.x, p.y);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
-        join(m2, s2);
-    }
-    const float lse = __fmul_rn(__fadd_rn(mx, log2f(sum)), kLn2);
-    const int tg = targets[t];
-    float loss = 0.0f;
+    __shared__ float2 s_ms[8];
+    __shared__ int s_acc[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = WARPS == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x, w = WARPS == 1 ? 0 : warp;
+    const bool live = t < m;
+    const int tg = live ? targets[t] : DFSSM_IGNORE_TARGET;
+    int acc = 0;
     if (is_token(tg, vocab)) {
         const uint4* ep = reinterpret_cast<const uint4*>(table + (int64_t)tg * d);
         const uint4* qp = reinterpret_cast<const uint4*>(q + (int64_t)t * d);
-        int acc = 0;
-        for (int i = lane; i < (d >> 4); i += 32) {
+        for (int i = lane + 32 * w; i < (d >> 4); i += 32 * WARPS) {
             const uint4 x = ep[i], y = qp[i];
             acc = __dp4a((int)x.x, (int)y.x, acc);
             acc = __dp4a((int)x.y, (int)y.y, acc);
             acc = __dp4a((int)x.z, (int)y.z, acc);
             acc = __dp4a((int)x.w, (int)y.w, acc);
         }
-        acc = __reduce_add_sync(0xffffffffu, acc);
-        loss = __fsub_rn(lse, __fmul_rn(sx[t], __fmul_rn(scale[tg], (float)acc)));
-    } else if (tg != DFSSM_IGNORE_TARGET && lane == 0) {
-        atomicOr(err, DFSSM_DEVERR_TOKEN_ID);
     }
-    if (lane == 0) {
-        nll[t] = loss;
-        lse_out[t] = lse;
+    acc = __reduce_add_sync(0xffffffffu, acc);
+    ptx::pdl_wait();                               // the pairs
+    float mx = -INFINITY, sum = 0.0f;
+    auto join = [&](float m2, float s2) {
+        const float nm = fmaxf(mx, m2);
+        const float ref = nm == -INFINITY ? 0.0f : nm;
+        sum = __fadd_rn(__fmul_rn(sum, ex2(__fsub_rn(mx, ref))), __fmul_rn(s2, ex2(__fsub_rn(m2, ref))));
+        mx = nm;
+    };
+    if (live)
+        for (int i = lane + 32 * w; i < n_part; i += 32 * WARPS) {
+            const float2 p = part[(int64_t)i * m + t];
+            join(p.x, p.y);
+        }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+        join(m2, s2);
     }
+    if (WARPS > 1) {
+        if (lane == 0) {
+            s_ms[warp] = make_float2(mx, sum);
+            s_acc[warp] = acc;
+        }
+        __syncthreads();
+        if (threadIdx.x != 0) return;
+        for (int k = 1; k < WARPS; ++k) {
+            join(s_ms[k].x, s_ms[k].y);
+            acc += s_acc[k];
+        }
+    }
+    if (lane != 0 || !live) return;
+    const float lse = __fmul_rn(__fadd_rn(mx, log2f(sum)), kLn2);
+    float loss = 0.0f;
+    if (is_token(tg, vocab)) loss = __fsub_rn(lse, __fmul_rn(sx[t], __fmul_rn(scale[tg], (float)acc)));
+    else if (tg != DFSSM_IGNORE_TARGET) atomicOr(err, DFSSM_DEVERR_TOKEN_ID);
+    nll[t] = loss;
+    lse_out[t] = lse;
 }
 
 // max |scale| as bits (one CTA)
 __global__ void __launch_bounds__(1024) xent_smax_kernel(const float* __restrict__ scale, int vocab, uint32_t* out) {
     __shared__ uint32_t red[32];
+    ptx::pdl_launch_dependents();
     uint32_t v = 0u;
     const int n4 = vocab >> 2;
     for (int i = threadIdx.x; i < n4; i += 1024) {
@@ -357,47 +408,75 @@ __global__ void __launch_bounds__(1024) xent_smax_kernel(const float* __restrict
 
 // ------------------------------------------------------------------------------- gradient
 
+// The product's work is cut evenly over the CTAs in units of 64 table rows of one output tile; a CTA's range may
+// begin inside one tile and end inside another. What a CTA adds up for a tile is one partial sum, in the
+// tile's slot (CTA - first CTA of the tile).
+struct DhSplit {
+    int n_ct, ns;           // channel tiles; units per tile (of a full piece)
+    int ctas;
+    uint32_t share, more;   // units per CTA; the first `more` CTAs have one more
+};
+__host__ __device__ inline uint32_t first_unit(const DhSplit& p, uint32_t cta) {
+    return cta * p.share + (cta < p.more ? cta : p.more);
+}
+__host__ __device__ inline int cta_of(const DhSplit& p, uint32_t unit) {
+    const uint32_t big = p.more * (p.share + 1);
+    return unit < big ? (int)(unit / (p.share + 1)) : (int)(p.more + (unit - big) / p.share);
+}
+
 struct DhArgs {
     const int8_t* table;
     int d, m;
     int v0, k_total;        // table row of the piece's column 0; its live columns
-    int k_split;            // columns per split (a multiple of 64)
-    float* part;            // [splits][m][d]
-    int add;                // 1: add to part (a later piece), 0: write it
+    DhSplit sp;
+    float* part;            // [slots][m][d] of this piece
     uint32_t* err;
 };
 
-// CTA (split, channel tile, token tile). Warp 0 loads the fp16 gradients by TMA, warps 4..11 turn the
-// table's bytes into the B operand and write the accumulator out afterwards, warp 1 issues the MMAs.
+// Warp 0 loads the fp16 gradients by TMA, warps 4..11 turn the table's bytes into the B operand and write the
+// accumulators out, warp 1 issues the MMAs. A tile is 128 NM tokens x 256 channels: with NM = 2 (more than
+// 128 tokens) the expanded bytes serve two accumulators, which takes a quarter off the shared-memory traffic per
+// MMA that bounds NM = 1.
+template <int NM>
 __global__ void __launch_bounds__(kDhThreads, 1)
 xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
+    constexpr int kStages = NM == 1 ? 4 : 3, kA = NM * kDhA, kStage = kA + kDhB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + kDhStages * kDhStage);     // TMA bytes
-    uint64_t* full_b = full_a + kDhStages;                                           // kDhConv arrivals
-    uint64_t* empty = full_b + kDhStages;                                            // MMA commit
-    uint64_t* acc_full = empty + kDhStages;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + kStages * kStage);         // TMA bytes
+    uint64_t* full_b = full_a + kStages;                                             // one arrival per warp of a converter group
+    uint64_t* empty = full_b + kStages;                                              // MMA commit
+    uint64_t* acc_full = empty + kStages;                                            // MMA commit
+    uint64_t* acc_empty = acc_full + 1;                                              // one arrival per converter warp
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tok0 = blockIdx.x * kBM, c0 = blockIdx.y * kBN, sp = blockIdx.z;
-    const int k0 = sp * a.k_split;
-    const int k_end = min(a.k_total, k0 + a.k_split);
-    const int n_k = k_end > k0 ? (k_end - k0 + 63) / 64 : 0;
+    const uint32_t u0 = first_unit(a.sp, blockIdx.x), u1 = first_unit(a.sp, blockIdx.x + 1);
+    const int ns_live = (a.k_total + 63) / 64;
+    // the CTA's range tile by tile: f(tile, first unit, units); units may be none in the last, shorter piece
+    auto for_tiles = [&](auto f) {
+        for (uint32_t u = u0; u < u1;) {
+            const int tile = (int)(u / (uint32_t)a.sp.ns), lo = (int)(u - (uint32_t)tile * a.sp.ns);
+            const int hi = min(a.sp.ns, lo + (int)(u1 - u));
+            if (!f(tile, lo, max(0, min(hi, ns_live) - lo))) return;
+            u += hi - lo;
+        }
+    };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kDhStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&full_a[s], 1);
-            ptx::mbar_init(&full_b[s], kDhConv);
+            ptx::mbar_init(&full_b[s], kDhConv / 64);
             ptx::mbar_init(&empty[s], 1);
         }
         ptx::mbar_init(acc_full, 1);
+        ptx::mbar_init(acc_empty, kDhConv / 32);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(tmem_slot, 256);
+        ptx::tmem_alloc(tmem_slot, NM * 256);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -407,199 +486,260 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
 
     if (warp == 0) {
         if (lane == 0) {
-            int k = 0;
-            for (; k < n_k && !*abort_flag; ++k) {
-                const int s = k % kDhStages;
-                if (!ptx::mbar_wait(&empty[s], ((uint32_t)(k / kDhStages) & 1u) ^ 1u)) {
-                    give_up(a.err, abort_flag);
-                    break;
+            ptx::pdl_wait();                       // the gradients of this piece
+            int it = 0;
+            for_tiles([&](int tile, int lo, int n) {
+                for (int k = 0; k < n; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (*abort_flag || !ptx::mbar_wait(&empty[s], ((uint32_t)(it / kStages) & 1u) ^ 1u)) {
+                        give_up(a.err, abort_flag);
+                        return false;
+                    }
+                    ptx::mbar_arrive_expect_tx(&full_a[s], kA);
+#pragma unroll
+                    for (int i = 0; i < NM; ++i)
+                        ptx::tma_load_2d(smem + s * kStage + i * kDhA, &map_g, 64 * (lo + k),
+                                         (tile / a.sp.n_ct * NM + i) * kBM, &full_a[s]);
                 }
-                ptx::mbar_arrive_expect_tx(&full_a[s], kDhA);
-                ptx::tma_load_2d(smem + s * kDhStage, &map_g, k0 + 64 * k, tok0, &full_a[s]);
-            }
+                return true;
+            });
             if (*abort_flag)
-                for (int i = max(0, k - kDhStages); i < k; ++i)
-                    ptx::mbar_wait(&full_a[i % kDhStages], (uint32_t)(i / kDhStages) & 1u);
+                for (int i = max(0, it - kStages); i < it; ++i)
+                    ptx::mbar_wait(&full_a[i % kStages], (uint32_t)(i / kStages) & 1u);
         }
     } else if (warp == 1) {
         if (lane == 0) {
             // kind::f16: D fp32, A and B fp16, both K-major
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            int k = 0;
-            for (; k < n_k && !*abort_flag; ++k) {
-                const int s = k % kDhStages;
-                const uint32_t ph = (uint32_t)(k / kDhStages) & 1u;
-                if (!ptx::mbar_wait(&full_a[s], ph) || !ptx::mbar_wait(&full_b[s], ph)) {
+            int it = 0, seg = 0;
+            for_tiles([&](int, int, int n) {
+                if (n == 0) return true;
+                if (!ptx::mbar_wait(acc_empty, ((uint32_t)seg & 1u) ^ 1u)) {
                     give_up(a.err, abort_flag);
-                    break;
+                    return false;
                 }
                 ptx::tc_fence_after();
-                const uint64_t ad = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * kDhStage));
-                const uint64_t bd = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * kDhStage + kDhA));
+                for (int k = 0; k < n; ++k, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+                    if (*abort_flag || !ptx::mbar_wait(&full_a[s], ph) || !ptx::mbar_wait(&full_b[s], ph)) {
+                        give_up(a.err, abort_flag);
+                        return false;
+                    }
+                    ptx::tc_fence_after();
+                    const uint64_t bd = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * kStage + kA));
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) ptx::mma_f16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
-                ptx::mma_commit(&empty[s]);
-            }
-            if (!*abort_flag) ptx::mma_commit(acc_full);
-            else
-                for (int i = max(0, k - kDhStages); i < k; ++i)
-                    ptx::mbar_wait(&empty[i % kDhStages], (uint32_t)(i / kDhStages) & 1u);
+                    for (int i = 0; i < NM; ++i) {
+                        const uint64_t ad = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * kStage + i * kDhA));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_f16(tmem + (uint32_t)(256 * i), ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+                    }
+                    ptx::mma_commit(&empty[s]);
+                }
+                ptx::mma_commit(acc_full);
+                ++seg;
+                return true;
+            });
+            if (*abort_flag)
+                for (int i = max(0, it - kStages); i < it; ++i)
+                    ptx::mbar_wait(&empty[i % kStages], (uint32_t)(i / kStages) & 1u);
         }
     } else if (warp >= 4) {
-        // Converter: a warp's unit is 8 table rows (K) x 128 channels, lane l the channels 4 l .. 4 l + 3;
-        // warp w takes K rows 8 w .. 8 w + 7 of the stage, both channel halves. A 16-byte piece holds
-        // one channel's 8 K values: row n, piece w ^ (n & 7) of the 128-byte swizzle. Lane l stores its
-        // channels in the order i = (j + l/2) % 4, so that the 8 lanes of a store phase hit 8 pieces.
-        const int w = warp - 4;
-        uint32_t sel[4], row[4];
+        // Converters, two groups of four warps that take turns at the stages (what a stage costs a warp in
+        // latency, from the wait for its release to the fence behind its stores, is then paid side by side). A
+        // unit is 8 table rows (K) x 128 channels, lane l the channels 4 l .. 4 l + 3; warp w of a group takes the
+        // K octets w and w + 4 of the stage, both channel halves. A 16-byte piece holds one channel's 8 K
+        // values: row n, piece octet ^ (n & 7) of the 128-byte swizzle. Lane l stores its channels in the
+        // order i = (j + l/2) % 4, so that the 8 lanes of a store phase hit 8 pieces. Two of the group's stages
+        // are in flight. Whole stages take a path without bounds.
+        const int w = (warp - 4) & 3, group = (warp - 4) >> 2;
+        uint32_t sel[4], off[4];         // off: the thread's pieces of octet 0, first half, in a stage's B tile
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t i = (uint32_t)(j + (lane >> 1)) & 3u;
+            const uint32_t i = (uint32_t)(j + (lane >> 1)) & 3u, nr = 4 * lane + i;
             sel[j] = i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12);
-            row[j] = 4 * lane + i;
+            off[j] = nr * 128 + 16 * (nr & 7u);
         }
-        const bool in0 = c0 + 4 * lane < a.d, in1 = c0 + 128 + 4 * lane < a.d;
-        uint32_t x[2][16];           // two stages in flight: [half][8 rows]
-        auto load = [&](int k, uint32_t* r) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int kr = k0 + 64 * k + 8 * w + i;
-                const bool in = k < n_k && kr < k_end;
-                const uint32_t* p =
-                    reinterpret_cast<const uint32_t*>(a.table + (int64_t)(a.v0 + (in ? kr : 0)) * a.d + c0) + lane;
-                r[i] = in && in0 ? __ldg(p) : 0u;
-                r[8 + i] = in && in1 ? __ldg(p + 32) : 0u;
-            }
-        };
-        auto convert = [&](int k, const uint32_t* r) -> bool {
-            const int s = k % kDhStages;
-            bool got = true;
-            if (lane == 0) got = ptx::mbar_wait(&empty[s], ((uint32_t)(k / kDhStages) & 1u) ^ 1u) && !*abort_flag;
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got) {
-                if (lane == 0) give_up(a.err, abort_flag);
-                return false;
-            }
-            uint8_t* bs = smem + s * kDhStage + kDhA;
-            const __half2 off = __floats2half2_rn(1152.0f, 1152.0f);          // 1024 + 128
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        // bytes b0, b1 of two K rows -> fp16 (1024 + (b ^ 128)) pairs -> minus 1152: exact
-                        const uint32_t t2 = __byte_perm(r[8 * h + 2 * p], r[8 * h + 2 * p + 1], sel[j]);
-                        const uint32_t u2 = (t2 & 0x00FF00FFu) ^ 0x64806480u;
-                        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u2), off);
-                        o[p] = *reinterpret_cast<const uint32_t*>(&v);
-                    }
-                    const uint32_t n = 128 * h + row[j];
-                    *reinterpret_cast<uint4*>(bs + n * 128 + 16 * ((uint32_t)w ^ (n & 7u))) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&full_b[s]);
-            return true;
-        };
-        load(0, x[0]);
-        load(1, x[1]);
-        bool ok = true;
-        for (int k = 0; k < n_k && ok; k += 2) {
-            ok = convert(k, x[0]);
-            load(k + 2, x[0]);
-            if (ok && k + 1 < n_k) ok = convert(k + 1, x[1]);
-            load(k + 3, x[1]);
-        }
-        // ---- the accumulator: lane quarter warp & 3, channel half (warp - 4) / 4
+        const uint32_t smem_b = ptx::smem_u32(smem) + kA, s_out = ptx::smem_u32(smem) + kStages * kStage + 256 + (warp - 4) * 4096;
         const int q4 = warp & 3, half = (warp - 4) >> 2;
-        const int t = tok0 + 32 * q4 + lane;
-        float* dst = a.part + ((int64_t)sp * a.m + t) * a.d + c0 + half * (kBN / 2);
-        const int c_end = min(kBN / 2, a.d - c0 - half * (kBN / 2));
-        bool got = ok;
-        if (n_k > 0) {
-            if (got && lane == 0) got = ptx::mbar_wait(acc_full, 0u);
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got && lane == 0) give_up(a.err, abort_flag);
-        }
-        ptx::tc_fence_after();
-        if (got && !(n_k == 0 && a.add)) {
+        const uint32_t d32 = (uint32_t)a.d;
+        int seg = 0, it0 = 0;            // segments done; stages of all segments before
+        bool waited = false;
+        for_tiles([&](int tile, int lo, int n) {
+            const int tok0 = tile / a.sp.n_ct * NM * kBM, c0 = tile % a.sp.n_ct * kBN;
+            const bool in0 = c0 + 4 * lane < a.d, in1 = c0 + 128 + 4 * lane < a.d;
+            const bool all_c = c0 + kBN <= a.d;
+            const int8_t* src = a.table + (int64_t)(a.v0 + 64 * lo + 8 * w) * a.d + c0 + 4 * lane;
+            const int left = a.k_total - 64 * lo - 8 * w;        // live rows from the thread's first one on
+            uint32_t x[2][32];           // [stage in flight][octet, half, 8 rows]
+            auto load = [&](int k, uint32_t* r) {
+                const int8_t* p = src + (int64_t)k * 64 * d32;
+                if (k < n && all_c && 64 * k + 40 <= left) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t* q = reinterpret_cast<const uint32_t*>(p + (uint32_t)(i < 8 ? i : 24 + i) * d32);
+                        r[(i >> 3) * 16 + (i & 7)] = __ldg(q);
+                        r[(i >> 3) * 16 + 8 + (i & 7)] = __ldg(q + 32);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int row = i < 8 ? i : 24 + i;
+                        const bool in = k < n && 64 * k + row < left;
+                        const uint32_t* q = reinterpret_cast<const uint32_t*>(p + (uint32_t)row * d32);
+                        r[(i >> 3) * 16 + (i & 7)] = in && in0 ? __ldg(q) : 0u;
+                        r[(i >> 3) * 16 + 8 + (i & 7)] = in && in1 ? __ldg(q + 32) : 0u;
+                    }
+                }
+            };
+            auto convert = [&](int k, const uint32_t* r) -> bool {
+                const int it = it0 + k, st = it % kStages;
+                bool got = true;
+                if (lane == 0) got = ptx::mbar_wait(&empty[st], ((uint32_t)(it / kStages) & 1u) ^ 1u) && !*abort_flag;
+                got = __shfl_sync(0xffffffffu, got, 0);
+                if (!got) {
+                    if (lane == 0) give_up(a.err, abort_flag);
+                    return false;
+                }
+                const uint32_t bs = smem_b + st * kStage;
+                const __half2 bias = __floats2half2_rn(1152.0f, 1152.0f);         // 1024 + 128
+#pragma unroll
+                for (int oc = 0; oc < 2; ++oc)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                // bytes b0, b1 of two K rows -> fp16 (1024 + (b ^ 128)) pairs -> minus 1152: exact
+                                const uint32_t t2 = __byte_perm(r[16 * oc + 8 * h + 2 * p], r[16 * oc + 8 * h + 2 * p + 1], sel[j]);
+                                const uint32_t u2 = (t2 & 0x00FF00FFu) ^ 0x64806480u;
+                                const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u2), bias);
+                                o[p] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                            const uint32_t at = bs + 128 * 128 * h + (off[j] ^ (uint32_t)(16 * (w + 4 * oc)));
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                                         ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                        }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();                      // one arrival per warp: 256 on one barrier serialise
+                if (lane == 0) ptx::mbar_arrive(&full_b[st]);
+                return true;
+            };
+            const int k0 = (it0 + group) & 1;      // this group's first stage of the segment
+            load(k0, x[0]);
+            load(k0 + 2, x[1]);
+            for (int k = k0; k < n; k += 4) {
+                if (!convert(k, x[0])) return false;
+                load(k + 4, x[0]);
+                if (k + 2 < n && !convert(k + 2, x[1])) return false;
+                load(k + 6, x[1]);
+            }
+            it0 += n;
+            // ---- the accumulators: lane quarter warp & 3, channel half (warp - 4) / 4
+            if (!waited) {
+                ptx::pdl_wait();                   // earlier readers of the partial sums
+                waited = true;
+            }
+            if (n > 0) {
+                bool got = true;
+                if (lane == 0) got = ptx::mbar_wait(acc_full, (uint32_t)seg & 1u);
+                got = __shfl_sync(0xffffffffu, got, 0);
+                if (!got) {
+                    if (lane == 0) give_up(a.err, abort_flag);
+                    return false;
+                }
+                ptx::tc_fence_after();
+            }
+            const int slot = blockIdx.x - cta_of(a.sp, (uint32_t)tile * a.sp.ns);
 #pragma unroll 1
-            for (int c = 0; c < kBN / 2; c += 32) {
+            for (int c = 0; c < NM * kBN / 2; c += 32) {
+                const int i = c / (kBN / 2), col = half * (kBN / 2) + c % (kBN / 2);
                 uint32_t r[32];
-                if (n_k > 0) {
-                    ptx::tmem_ld_32x32b_x32(tmem + (uint32_t)(half * (kBN / 2) + c) + ((uint32_t)(32 * q4) << 16), r);
+                if (n > 0) {
+                    ptx::tmem_ld_32x32b_x32(tmem + (uint32_t)(256 * i + col) + ((uint32_t)(32 * q4) << 16), r);
                     ptx::tmem_ld_wait();
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0u;
+                    for (int e = 0; e < 32; ++e) r[e] = 0u;
                 }
-                if (t >= a.m) continue;
+                // through the warp's 4 KB, so that a store covers four whole 128-byte rows
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    if (c + i >= c_end) continue;              // d is a multiple of 16
-                    float4 v = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), __uint_as_float(r[i + 2]),
-                                           __uint_as_float(r[i + 3]));
-                    float4* p = reinterpret_cast<float4*>(dst + c + i);
-                    if (a.add) {
-                        const float4 o = *p;
-                        v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
-                    }
-                    *p = v;
+                for (int e = 0; e < 8; ++e)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                                 ::"r"(s_out + (uint32_t)(lane * 128 + 16 * (e ^ (lane & 7)))), "r"(r[4 * e]), "r"(r[4 * e + 1]),
+                                 "r"(r[4 * e + 2]), "r"(r[4 * e + 3]) : "memory");
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int rr = 4 * e + (lane >> 3), pc = lane & 7, t = tok0 + i * kBM + 32 * q4 + rr;
+                    const uint4 v = ptx::lds128(s_out + (uint32_t)(rr * 128 + 16 * (pc ^ (rr & 7))));
+                    if (t < a.m && c0 + col + 4 * pc < a.d)
+                        *reinterpret_cast<uint4*>(a.part + ((int64_t)slot * a.m + t) * a.d + c0 + col + 4 * pc) = v;
                 }
             }
-        }
+            if (n > 0) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(acc_empty);
+                ++seg;
+            }
+            return true;
+        });
     }
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 256);
+        ptx::tmem_dealloc(tmem, NM * 256);
     }
 }
 
-// dh = bf16(grad (sum of the splits / K - s[target] E[target])): 8 channels per thread
-__global__ void __launch_bounds__(256) xent_dh_out_kernel(const float* __restrict__ part, int splits,
+// dh = bf16(grad (sum of the slots / K - s[target] E[target])): 4 channels per thread
+__global__ void __launch_bounds__(256) xent_dh_out_kernel(const float* __restrict__ part, const DhSplit sp, int pieces,
+                                                          int max_slots, int tile_tokens,
                                                           const int8_t* __restrict__ table,
                                                           const float* __restrict__ scale, int vocab, int d,
                                                           const int32_t* __restrict__ targets,
                                                           const float* __restrict__ grad, int m,
                                                           const uint32_t* __restrict__ smax, uint16_t* dh,
                                                           uint32_t* err) {
-    const int per = d >> 3;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)m * per) return;
-    const int t = (int)(i / per), c = 8 * (int)(i - (int64_t)t * per);
+    const int per = d >> 2;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;      // m is at most a token block here
+    if (i >= (uint32_t)(m * per)) return;
+    const int t = (int)(i / (uint32_t)per), c = 4 * (int)(i - (uint32_t)(t * per));
     const int tg = targets[t];
-    uint4 out = make_uint4(0u, 0u, 0u, 0u);
-    if (is_token(tg, vocab)) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-        for (int s = 0; s < splits; ++s) {
-            const float4* p = reinterpret_cast<const float4*>(part + ((int64_t)s * m + t) * d + c);
-            const float4 x = p[0], y = p[1];
-            v[0] = __fadd_rn(v[0], x.x); v[1] = __fadd_rn(v[1], x.y); v[2] = __fadd_rn(v[2], x.z);
-            v[3] = __fadd_rn(v[3], x.w); v[4] = __fadd_rn(v[4], y.x); v[5] = __fadd_rn(v[5], y.y);
-            v[6] = __fadd_rn(v[6], y.z); v[7] = __fadd_rn(v[7], y.w);
+    const bool on = is_token(tg, vocab);
+    const uint32_t u = (uint32_t)(t / tile_tokens * sp.n_ct + c / kBN) * sp.ns;
+    const int slots = cta_of(sp, u + sp.ns - 1) - cta_of(sp, u) + 1;
+    ptx::pdl_wait();                                   // the partial sums
+    uint2 out = make_uint2(0u, 0u);
+    if (on) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int p = 0; p < pieces; ++p) {
+#pragma unroll 8
+            for (int s = 0; s < slots; ++s) {
+                const float4 x =
+                    *reinterpret_cast<const float4*>(part + ((int64_t)(p * max_slots + s) * m + t) * d + c);
+                v = make_float4(__fadd_rn(v.x, x.x), __fadd_rn(v.y, x.y), __fadd_rn(v.z, x.z), __fadd_rn(v.w, x.w));
+            }
         }
         const float back = __fdiv_rn(1.0f, grad_scale(*smax)), g = grad[t], s = scale[tg];
-        const uint2 e = *reinterpret_cast<const uint2*>(table + (int64_t)tg * d + c);
-        uint32_t b[4];
+        const uint32_t e = *reinterpret_cast<const uint32_t*>(table + (int64_t)tg * d + c);
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        float o[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float w = small_int_to_float((int)(int8_t)((k < 4 ? e.x : e.y) >> (8 * (k & 3))));
-            v[k] = __fmul_rn(g, __fmaf_rn(-s, w, __fmul_rn(v[k], back)));
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) b[k] = bf16x2_of(make_float2(v[2 * k], v[2 * k + 1]));
-        out = make_uint4(b[0], b[1], b[2], b[3]);
+        for (int k = 0; k < 4; ++k)
+            o[k] = __fmul_rn(g, __fmaf_rn(-s, small_int_to_float((int)(int8_t)(e >> (8 * k))), __fmul_rn(f[k], back)));
+        out = make_uint2(bf16x2_of(make_float2(o[0], o[1])), bf16x2_of(make_float2(o[2], o[3])));
     } else if (tg != DFSSM_IGNORE_TARGET && c == 0) {
         atomicOr(err, DFSSM_DEVERR_TOKEN_ID);
     }
-    *reinterpret_cast<uint4*>(dh + (int64_t)t * d + c) = out;
+    *reinterpret_cast<uint2*>(dh + (int64_t)t * d + c) = out;
 }
 
 // ------------------------------------------------------------------------------- host
@@ -607,27 +747,36 @@ __global__ void __launch_bounds__(256) xent_dh_out_kernel(const float* __restric
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// How a gradient call is cut: token blocks, vocabulary pieces, splits of a piece over the CTAs.
+constexpr int kSms = 148;
+
+int tile_rows(int m) { return m <= kBM ? kBNFew : kBN; }
+
+// How a gradient call is cut: token blocks, vocabulary pieces, the product's units over the CTAs.
 struct DhPlan {
     int tok_block;      // tokens per block
-    int piece;          // table rows per piece (a multiple of kBN)
-    int splits;         // K splits of a piece
-    int k_split;        // columns per split (a multiple of 64)
+    int pieces;
+    int piece;          // table rows per piece (a multiple of the logits' tile and of 64)
+    int nm;             // 128-token accumulators per CTA
+    DhSplit sp;
+    int slots;          // partial sums a tile can have
 };
 
 DhPlan dh_plan(int m, int vocab, int d) {
     DhPlan p;
     p.tok_block = m < kTokBlock ? m : kTokBlock;
-    const size_t bytes = (size_t)p.tok_block * vocab * 2;
-    const int pieces = (int)((bytes + kGradBytes - 1) / kGradBytes);
-    p.piece = ((vocab + pieces - 1) / pieces + kBN - 1) / kBN * kBN;
-    // as many splits as fill 148 SMs with one CTA each, at least 1024 columns (16 stages) per split
-    const int tiles = ((p.tok_block + kBM - 1) / kBM) * ((d + kBN - 1) / kBN);
-    int s = 148 / tiles;
-    const int most = (p.piece + 1023) / 1024;
-    p.splits = s < 1 ? 1 : s > most ? most : s;
-    p.k_split = ((p.piece + p.splits - 1) / p.splits + 63) / 64 * 64;
-    p.splits = (p.piece + p.k_split - 1) / p.k_split;
+    const int bn = tile_rows(p.tok_block), all = (vocab + bn - 1) / bn;
+    const int most = (int)(kGradBytes / ((size_t)p.tok_block * 2 * bn));       // tiles of the largest piece
+    p.pieces = (all + most - 1) / most;
+    p.piece = (all + p.pieces - 1) / p.pieces * bn;
+    p.nm = p.tok_block > kBM ? 2 : 1;
+    p.sp.n_ct = (d + kBN - 1) / kBN;
+    p.sp.ns = p.piece / 64;
+    // at most 8 x 32 tiles of at most 2^18 units
+    const uint32_t units = (uint32_t)((p.tok_block + p.nm * kBM - 1) / (p.nm * kBM)) * p.sp.n_ct * p.sp.ns;
+    p.sp.ctas = units / 8 < 1 ? 1 : units / 8 < (uint32_t)kSms ? (int)(units / 8) : kSms;        // 8 units at least
+    p.sp.share = units / p.sp.ctas;
+    p.sp.more = units % p.sp.ctas;
+    p.slots = (int)((p.sp.ns + p.sp.share - 1) / p.sp.share) + 1;
     return p;
 }
 
@@ -639,7 +788,7 @@ XentWs xent_ws(int m, int vocab, int d, bool backward) {
     size_t o = 256;                                       // error word
     if (!backward) {
         w.part = o;
-        o = up256(o + (size_t)2 * ((vocab + kBN - 1) / kBN) * m * sizeof(float2));
+        o = up256(o + (size_t)2 * ((vocab + tile_rows(m) - 1) / tile_rows(m)) * m * sizeof(float2));
     } else {
         const DhPlan p = dh_plan(m, vocab, d);
         w.smax = o;
@@ -647,7 +796,7 @@ XentWs xent_ws(int m, int vocab, int d, bool backward) {
         w.g = o;
         o = up256(o + (size_t)p.tok_block * p.piece * sizeof(__half));
         w.dh = o;
-        o = up256(o + (size_t)p.splits * p.tok_block * d * sizeof(float));
+        o = up256(o + (size_t)p.pieces * p.slots * p.tok_block * d * sizeof(float));
     }
     w.total = o;
     return w;
@@ -684,12 +833,30 @@ dfssm_status xent_setup(int* sm_count) {
                 cudaSuccess ||
             cudaFuncSetAttribute(xent_logits_kernel<kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLgSmem) !=
                 cudaSuccess ||
-            cudaFuncSetAttribute(xent_dh_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDhSmem) != cudaSuccess)
+            cudaFuncSetAttribute(xent_dh_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDhSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(xent_dh_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDhSmem) != cudaSuccess)
             return DFSSM_ERR_CUDA;
         t.ready = true;
     }
     *sm_count = t.sm_count;
     return DFSSM_OK;
+}
+
+// Launch that may begin while the launch before it in the stream still runs; the kernel waits (pdl_wait) before it
+// touches what that one reads or writes.
+template <typename... K, typename... A>
+cudaError_t launch_after(void (*kernel)(K...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
 }
 
 dfssm_status check_xent(const dfssm_int8_table* t, int32_t m) {
@@ -733,8 +900,9 @@ extern "C" dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8
     uint32_t* err = reinterpret_cast<uint32_t*>(ws);
     float2* part = reinterpret_cast<float2*>(ws + w.part);
     CUtensorMap mq, me;
+    const int bn = tile_rows(m);
     if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q, d, m, d, kBM) ||
-        !encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, kBN))
+        !encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, bn))
         return DFSSM_ERR_CUDA;
     LogitsArgs a{};
     a.scale = table->scale;
@@ -742,19 +910,23 @@ extern "C" dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8
     a.vocab = vocab;
     a.d = d;
     a.m = m;
+    a.bn = bn;
     a.v0 = 0;
     a.v_end = vocab;
     a.part = part;
     a.err = err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int n_vt = (vocab + kBN - 1) / kBN;
+    const int n_vt = (vocab + bn - 1) / bn;
     const int64_t tiles = (int64_t)n_vt * ((m + kBM - 1) / kBM);
     if (tiles > (1 << 30)) return DFSSM_ERR_UNSUPPORTED_SHAPE;
     xent_logits_kernel<kLse><<<(int)(tiles < sms ? tiles : sms), kLgThreads, kLgSmem, s>>>(mq, me, a);
     if (cudaGetLastError() != cudaSuccess) return DFSSM_ERR_CUDA;
-    xent_lse_kernel<<<(m + 7) / 8, 256, 0, s>>>(part, 2 * n_vt, table->table, table->scale, vocab, d, q, sx, targets, m,
-                                                nll, lse, err);
-    return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
+    const cudaError_t e =
+        m < 1024 ? launch_after(xent_lse_kernel<8>, m, 256, 0, s, part, 2 * n_vt, table->table, table->scale, vocab, d, q,
+                                sx, targets, m, nll, lse, err)
+                 : launch_after(xent_lse_kernel<1>, (m + 7) / 8, 256, 0, s, part, 2 * n_vt, table->table, table->scale, vocab,
+                                d, q, sx, targets, m, nll, lse, err);
+    return e == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
 }
 
 extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8_t* q, const float* sx,
@@ -778,22 +950,25 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
     const DhPlan p = dh_plan(m, vocab, d);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap me;
-    if (!encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, kBN)) return DFSSM_ERR_CUDA;
+    const int bn = tile_rows(p.tok_block);
+    if (!encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, bn)) return DFSSM_ERR_CUDA;
     xent_smax_kernel<<<1, 1024, 0, s>>>(table->scale, vocab, smax);
-    for (int t0 = 0; t0 < m; t0 += p.tok_block) {
+    cudaError_t e = cudaGetLastError();
+    for (int t0 = 0; t0 < m && e == cudaSuccess; t0 += p.tok_block) {
         const int mb = m - t0 < p.tok_block ? m - t0 : p.tok_block;
         CUtensorMap mq, mg;
         if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q + (int64_t)t0 * d, d, mb, d, kBM) ||
             !encode_rows(&mg, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, g, p.piece, mb, p.piece, kBM))
             return DFSSM_ERR_CUDA;
         const int n_tt = (mb + kBM - 1) / kBM;
-        for (int v0 = 0; v0 < vocab; v0 += p.piece) {
+        for (int v0 = 0; v0 < vocab && e == cudaSuccess; v0 += p.piece) {
             LogitsArgs a{};
             a.scale = table->scale;
             a.sx = sx + t0;
             a.vocab = vocab;
             a.d = d;
             a.m = mb;
+            a.bn = bn;
             a.v0 = v0;
             a.v_end = vocab - v0 < p.piece ? vocab : v0 + p.piece;
             a.lse = lse + t0;
@@ -802,17 +977,17 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
             a.g = g;
             a.ldg = p.piece;
             a.err = err;
-            const int tiles = n_tt * ((a.v_end - v0 + kBN - 1) / kBN);
-            xent_logits_kernel<kGrad><<<tiles < sms ? tiles : sms, kLgThreads, kLgSmem, s>>>(mq, me, a);
-            DhArgs b{table->table, d, mb, v0, a.v_end - v0, p.k_split, part, v0 > 0 ? 1 : 0, err};
-            xent_dh_kernel<<<dim3(n_tt, (d + kBN - 1) / kBN, p.splits), kDhThreads, kDhSmem, s>>>(mg, b);
-            if (cudaGetLastError() != cudaSuccess) return DFSSM_ERR_CUDA;
+            const int tiles = n_tt * ((a.v_end - v0 + bn - 1) / bn);
+            e = launch_after(xent_logits_kernel<kGrad>, tiles < sms ? tiles : sms, kLgThreads, kLgSmem, s, mq, me, a);
+            const DhArgs b{table->table, d, mb, v0, a.v_end - v0, p.sp, part + (size_t)(v0 / p.piece) * p.slots * mb * d, err};
+            if (e == cudaSuccess)
+                e = launch_after(p.nm == 1 ? xent_dh_kernel<1> : xent_dh_kernel<2>, p.sp.ctas, kDhThreads, kDhSmem, s, mg, b);
         }
-        const int64_t n = (int64_t)mb * (d >> 3);
-        xent_dh_out_kernel<<<(int)((n + 255) / 256), 256, 0, s>>>(part, p.splits, table->table, table->scale, vocab, d,
-                                                                   targets + t0, grad + t0, mb, smax,
-                                                                   static_cast<uint16_t*>(dh) + (int64_t)t0 * d, err);
-        if (cudaGetLastError() != cudaSuccess) return DFSSM_ERR_CUDA;
+        const int64_t n = (int64_t)mb * (d >> 2);
+        if (e == cudaSuccess)
+            e = launch_after(xent_dh_out_kernel, (int)((n + 255) / 256), 256, 0, s, part, p.sp, p.pieces, p.slots, p.nm * kBM, table->table,
+                             table->scale, vocab, d, targets + t0, grad + t0, mb, smax,
+                             static_cast<uint16_t*>(dh) + (int64_t)t0 * d, err);
     }
-    return DFSSM_OK;
+    return e == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
 }
