@@ -131,16 +131,95 @@ struct FwdOut {
     float* final_state;        // or NULL
 };
 
-constexpr int kStage = 16384 + 16384 + 8192;          // C, B, X of one chunk
-constexpr int kFwdSmem = 2 * kStage + 2 * 8192 + 2 * (int)sizeof(Decay) + 128;
+// ---- B and C in fp16
+// fp16 holds a bf16 value exactly over 2^-24 .. 2^15; a tile of 64 tokens is scaled by a power of two that brings its
+// largest magnitude to [2^3, 2^4), so that only values below 2^-17 of that lose bits, and G = C B^T stays below 2^15.
 
-__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const Args a, const FwdOut o) {
+constexpr int kTileTop = 3;
+
+__device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t m, uint32_t v) {
+    return max(m, max((v << 16) & 0x7FFF0000u, v & 0x7FFF0000u));
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
+    return f16x2_of(__fmul_rn(bf16_lo(v), scale), __fmul_rn(bf16_hi(v), scale));
+}
+
+// CTA (chunk, group, C or B): the tile, rows behind the chunk's tokens as zeros
+__global__ void __launch_bounds__(256) scan_tiles_kernel(const Args a) {
+    __shared__ uint32_t red[8];
+    const int ngroups = a.nheads / a.per_group;
+    const int side = blockIdx.x & 1, g = (blockIdx.x >> 1) % ngroups, ci = (blockIdx.x >> 1) / ngroups;
+    if (ci >= a.count[1]) return;
+    const Chunk ch = a.chunks[ci];
+    const uint16_t* src = (side ? a.b : a.c) + (int64_t)g * kN;
+    const int64_t ld = side ? a.ldb : a.ldc;
+    uint4 v[4];
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (threadIdx.x >> 4) + 16 * i, pc = threadIdx.x & 15;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < ch.n) v[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(ch.t0 + row) * ld + 8 * pc);
+        m = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(m, v[i].x), v[i].y), v[i].z), v[i].w);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = max(m, red[w]);
+    const float2 sc = pow2_scale(m, kTileTop);
+    uint16_t* dst = a.tiles + (((int64_t)ci * ngroups + g) * 2 + side) * (kQ * kN);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(dst + 8 * (threadIdx.x + 256 * i)) =
+            make_uint4(bf16x2_to_f16x2(v[i].x, sc.x), bf16x2_to_f16x2(v[i].y, sc.x), bf16x2_to_f16x2(v[i].z, sc.x),
+                       bf16x2_to_f16x2(v[i].w, sc.x));
+    if (threadIdx.x == 0) (side ? &a.tile_scale[(int64_t)ci * ngroups + g].y : &a.tile_scale[(int64_t)ci * ngroups + g].x)[0] = sc.y;
+}
+
+// ---- the forward kernel
+constexpr int kFwdThreads = 256;
+constexpr int kStage = 16384 + 16384 + 8192;          // C, B, X of one chunk
+struct FwdDecay {
+    float cum[kQ];       // log 2 units
+    float dts[kQ];       // dt 2^kd, the largest in [1/2, 1)
+    float wl[kQ];        // dts exp(cum_64 - cum_t)
+    float done[kQ];      // exp(cum_t)
+    float kd;            // 2^-kd
+    float pad[3];
+};
+constexpr int kFwdX = 16384;                          // y's parts that a warp hands to its partner
+constexpr int kFwdSmem = 2 * kStage + 8192 + kFwdX + 2 * (int)sizeof(FwdDecay) + 128 + 128;
+
+__device__ __forceinline__ void fwd_decay(FwdDecay& f, Decay& d, float raw0, float raw1, int n, float bias, float a2,
+                                          int lane) {
+    chunk_decay(d, raw0, raw1, n, bias, a2, lane);
+    __syncwarp();
+    const float2 cum = reinterpret_cast<const float2*>(d.cum)[lane], dt = reinterpret_cast<const float2*>(d.dt)[lane];
+    const float2 left = reinterpret_cast<const float2*>(d.left)[lane];
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(dt.x), __float_as_uint(dt.y)));
+    const float2 sc = pow2_scale(m, -1);
+    const float2 ds = make_float2(__fmul_rn(dt.x, sc.x), __fmul_rn(dt.y, sc.x));
+    reinterpret_cast<float2*>(f.cum)[lane] = cum;
+    reinterpret_cast<float2*>(f.dts)[lane] = ds;
+    reinterpret_cast<float2*>(f.wl)[lane] = make_float2(__fmul_rn(ds.x, left.x), __fmul_rn(ds.y, left.y));
+    reinterpret_cast<float2*>(f.done)[lane] = reinterpret_cast<const float2*>(d.done)[lane];
+    if (lane == 0) f.kd = sc.y;
+}
+
+// TILES: C and B from scan_tiles_kernel; otherwise this kernel converts each chunk's tiles itself.
+template <bool TILES>
+__global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, const FwdOut o) {
     extern __shared__ uint8_t smem_raw[];
+    __shared__ Decay scratch;                         // of warp 0
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
-    const uint32_t s_m = base + 2 * kStage;           // M: high part, then low part
-    Decay* dec = reinterpret_cast<Decay*>(smem + 2 * kStage + 2 * 8192);
+    const uint32_t s_m = base + 2 * kStage, s_ex = s_m + 8192;
+    FwdDecay* dec = reinterpret_cast<FwdDecay*>(smem + 2 * kStage + 8192 + kFwdX);
+    uint32_t* s_max = reinterpret_cast<uint32_t*>(dec + 2);                // [2][8]
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int pw = w & 3, hv = w >> 2;                // channels 16 pw ..; states 64 hv ..; tokens 32 hv .. of y
+    const int ngroups = a.nheads / a.per_group;
     const int h = blockIdx.x % a.nheads, g = h / a.per_group;
     Item it;
     if (!get_item(a, blockIdx.x / a.nheads, it) || it.len < 0) return;
@@ -153,155 +232,307 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const Args a, con
         if (k < n_ch) {
             const int t0 = it.t0 + k * kQ, n = min(kQ, it.len - k * kQ);
             const uint32_t st = base + (k & 1) * kStage;
-            load_tile<128, kThreads>(st, c, a.ldc, t0, n, tid);
-            load_tile<128, kThreads>(st + 16384, b, a.ldb, t0, n, tid);
-            load_tile<64, kThreads>(st + 32768, x, a.ldx, t0, n, tid);
+            if (TILES) {
+                const uint16_t* tl = a.tiles + ((int64_t)(it.chunk0 + k) * ngroups + g) * 2 * (kQ * kN);
+                load_tile<128, kFwdThreads>(st, tl, kN, 0, kQ, tid);
+                load_tile<128, kFwdThreads>(st + 16384, tl + kQ * kN, kN, 0, kQ, tid);
+            } else {
+                load_tile<128, kFwdThreads>(st, c, a.ldc, t0, n, tid);
+                load_tile<128, kFwdThreads>(st + 16384, b, a.ldb, t0, n, tid);
+            }
+            load_tile<64, kFwdThreads>(st + 32768, x, a.ldx, t0, n, tid);
         }
         ptx::cp_async_commit();
     };
     fetch(0);
     const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e), skip = a.d_skip[h];
-    StateFrag S;
+    // the warp's part of the state: 16 channels x 64 states, 8 accumulator tiles
+    float S[8][4];
     const int64_t sh = ((int64_t)it.seq * a.nheads + h) * kStateElems;
-    if (it.flags & kCut) state_load(S, a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems, w, lane);
-    else if (a.init) state_load(S, a.init + sh, w, lane);
-    else state_zero(S);
-    float raw0 = 0.0f, raw1 = 0.0f;
-    if (w == 0 && n_ch > 0) {
-        const int n = min(kQ, it.len);
-        raw0 = raw_dt(a, it.t0, n, h, 2 * lane);
-        raw1 = raw_dt(a, it.t0, n, h, 2 * lane + 1);
-        chunk_decay(dec[0], raw0, raw1, n, bias, a2, lane);
+    const int s_at = (16 * pw + (lane >> 2)) * kN + 64 * hv + 2 * (lane & 3);
+    {
+        const float* src = it.flags & kCut ? a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems
+                                           : a.init ? a.init + sh : nullptr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float2 lo = make_float2(0.0f, 0.0f), hi = lo;
+            if (src) {
+                lo = *reinterpret_cast<const float2*>(src + s_at + 8 * j);
+                hi = *reinterpret_cast<const float2*>(src + s_at + 8 * kN + 8 * j);
+            }
+            S[j][0] = lo.x; S[j][1] = lo.y; S[j][2] = hi.x; S[j][3] = hi.y;
+        }
     }
+    float raw0 = 0.0f, raw1 = 0.0f;
+    auto raws = [&](int k) {
+        if (w != 0 || k >= n_ch) return;
+        const int t0 = it.t0 + k * kQ, n = min(kQ, it.len - k * kQ);
+        raw0 = raw_dt(a, t0, n, h, 2 * lane);
+        raw1 = raw_dt(a, t0, n, h, 2 * lane + 1);
+    };
+    auto decay = [&](int k) {
+        if (w != 0 || k >= n_ch) return;
+        fwd_decay(dec[k & 1], scratch, raw0, raw1, min(kQ, it.len - k * kQ), bias, a2, lane);
+    };
+    raws(0);
+    decay(0);
+    raws(1);
     for (int k = 0; k < n_ch; ++k) {
         const int t0 = it.t0 + k * kQ, n = min(kQ, it.len - k * kQ);
         const uint32_t st = base + (k & 1) * kStage;
         const uint32_t s_c = st, s_b = st + 16384, s_x = st + 32768;
-        const Decay& d = dec[k & 1];
-        // the next chunk's dt while this one is worked on
-        if (w == 0 && k + 1 < n_ch) {
-            const int n1 = min(kQ, it.len - (k + 1) * kQ);
-            raw0 = raw_dt(a, t0 + kQ, n1, h, 2 * lane);
-            raw1 = raw_dt(a, t0 + kQ, n1, h, 2 * lane + 1);
-        }
+        const FwdDecay& d = dec[k & 1];
         ptx::cp_async_wait<0>();
         __syncthreads();                 // this chunk's tiles and decays are there; the last one's are free
         fetch(k + 1);
+        float2 tsc;                      // 2^-k of C and of B
+        if (TILES) {
+            tsc = a.tile_scale[(int64_t)(it.chunk0 + k) * ngroups + g];
+        } else {
+            uint4 v[2][4];
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                uint32_t m = 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[side][i] = ptx::lds128(st + 16384 * side + 16 * (tid + kFwdThreads * i));
+                    m = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(m, v[side][i].x), v[side][i].y),
+                                                      v[side][i].z), v[side][i].w);
+                }
+                m = __reduce_max_sync(0xffffffffu, m);
+                if (lane == 0) s_max[8 * side + w] = m;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                uint32_t m = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max(m, s_max[8 * side + i]);
+                const float2 sc = pow2_scale(m, kTileTop);
+                (side ? tsc.y : tsc.x) = sc.y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                                 ::"r"(st + 16384 * side + 16 * (tid + kFwdThreads * i)),
+                                 "r"(bf16x2_to_f16x2(v[side][i].x, sc.x)), "r"(bf16x2_to_f16x2(v[side][i].y, sc.x)),
+                                 "r"(bf16x2_to_f16x2(v[side][i].z, sc.x)), "r"(bf16x2_to_f16x2(v[side][i].w, sc.x)) : "memory");
+            }
+            __syncthreads();
+        }
 
-        // ---- M, rows 16 w + lane / 4 (+ 8)
+        // ---- M in fp16, rows 16 pw + lane / 4 (+ 8), columns in blocks hv and hv + 2 of 16 up to the diagonal
         {
-            float G[8][4];
+            float G[2][2][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) G[j][0] = G[j][1] = G[j][2] = G[j][3] = 0.0f;
-#pragma unroll 2
-            for (int kk = 0; kk < kN; kk += 16) {
-                uint32_t ca[4];
-                frag_a<256>(s_c, 16 * w, kk, lane, ca);
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j > w) break;
-                    uint32_t bb[4];
-                    frag_b<256>(s_b, 16 * j, kk, lane, bb);
-                    mma(G[2 * j], ca, bb[0], bb[1]);
-                    mma(G[2 * j + 1], ca, bb[2], bb[3]);
+                for (int j = 0; j < 2; ++j) G[q][j][0] = G[q][j][1] = G[q][j][2] = G[q][j][3] = 0.0f;
+            if (hv <= pw) {
+#pragma unroll
+                for (int kk = 0; kk < kN; kk += 16) {
+                    uint32_t ca[4];
+                    frag_a<256>(s_c, 16 * pw, kk, lane, ca);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (hv + 2 * q > pw) break;
+                        uint32_t bb[4];
+                        frag_b<256>(s_b, 16 * (hv + 2 * q), kk, lane, bb);
+                        mma_h(G[q][0], ca, bb[0], bb[1]);
+                        mma_h(G[q][1], ca, bb[2], bb[3]);
+                    }
                 }
             }
-            const int r = 16 * w + (lane >> 2);
+            const int r = 16 * pw + (lane >> 2);
             const float c0 = d.cum[r], c1 = d.cum[r + 8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j > 2 * w + 1) break;
-                const int s = 8 * j + 2 * (lane & 3);
-                const float2 cs = *reinterpret_cast<const float2*>(d.cum + s);
-                const float2 ds = *reinterpret_cast<const float2*>(d.dt + s);
-                float m[4];
-                m[0] = s <= r ? __fmul_rn(__fmul_rn(G[j][0], ds.x), exp2f(__fsub_rn(c0, cs.x))) : 0.0f;
-                m[1] = s + 1 <= r ? __fmul_rn(__fmul_rn(G[j][1], ds.y), exp2f(__fsub_rn(c0, cs.y))) : 0.0f;
-                m[2] = s <= r + 8 ? __fmul_rn(__fmul_rn(G[j][2], ds.x), exp2f(__fsub_rn(c1, cs.x))) : 0.0f;
-                m[3] = s + 1 <= r + 8 ? __fmul_rn(__fmul_rn(G[j][3], ds.y), exp2f(__fsub_rn(c1, cs.y))) : 0.0f;
-                uint32_t h0, l0, h1, l1;
-                split_bf16x2(m[0], m[1], h0, l0);
-                split_bf16x2(m[2], m[3], h1, l1);
-                const uint32_t p0 = tile128(s_m, r, j) + 4 * (lane & 3), p1 = tile128(s_m, r + 8, j) + 4 * (lane & 3);
-                ptx::sts32(p0, h0);
-                ptx::sts32(p1, h1);
-                ptx::sts32(p0 + 8192, l0);
-                ptx::sts32(p1 + 8192, l1);
+            for (int q = 0; q < 2; ++q) {
+                const int blk = hv + 2 * q;
+                if (blk > pw) break;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int s = 16 * blk + 8 * j + 2 * (lane & 3);
+                    const float2 cs = *reinterpret_cast<const float2*>(d.cum + s);
+                    const float2 ds = *reinterpret_cast<const float2*>(d.dts + s);
+                    float m[4];
+                    m[0] = __fmul_rn(__fmul_rn(G[q][j][0], ds.x), ex2(__fsub_rn(c0, cs.x)));
+                    m[1] = __fmul_rn(__fmul_rn(G[q][j][1], ds.y), ex2(__fsub_rn(c0, cs.y)));
+                    m[2] = __fmul_rn(__fmul_rn(G[q][j][2], ds.x), ex2(__fsub_rn(c1, cs.x)));
+                    m[3] = __fmul_rn(__fmul_rn(G[q][j][3], ds.y), ex2(__fsub_rn(c1, cs.y)));
+                    if (blk == pw) {             // the diagonal
+                        if (s > r) m[0] = 0.0f;
+                        if (s + 1 > r) m[1] = 0.0f;
+                        if (s > r + 8) m[2] = 0.0f;
+                        if (s + 1 > r + 8) m[3] = 0.0f;
+                    }
+                    ptx::sts32(tile128(s_m, r, 2 * blk + j) + 4 * (lane & 3), f16x2_of(m[0], m[1]));
+                    ptx::sts32(tile128(s_m, r + 8, 2 * blk + j) + 4 * (lane & 3), f16x2_of(m[2], m[3]));
+                }
             }
         }
-        __syncthreads();                 // M is there
-
-        // ---- y of the warp's 16 channels: readout of the state, then the chunk's own tokens
+        decay(k + 1);                    // warp 0, which has the fewest blocks of M
+        raws(k + 2);
+        // ---- the state's readout over the warp's 64 states, for all 64 tokens
         float y[4][2][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int p = 0; p < 2; ++p) y[i][p][0] = y[i][p][1] = y[i][p][2] = y[i][p][3] = 0.0f;
+        {
+            uint32_t m = 0u;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-            uint32_t hi[4], lo[4];       // [2 * channel tile + k half]
-            split_bf16x2(S.v[2 * kk][0], S.v[2 * kk][1], hi[0], lo[0]);
-            split_bf16x2(S.v[2 * kk + 1][0], S.v[2 * kk + 1][1], hi[1], lo[1]);
-            split_bf16x2(S.v[2 * kk][2], S.v[2 * kk][3], hi[2], lo[2]);
-            split_bf16x2(S.v[2 * kk + 1][2], S.v[2 * kk + 1][3], hi[3], lo[3]);
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t ca[4];
-                frag_a<256>(s_c, 16 * i, 16 * kk, lane, ca);
-                mma(y[i][0], ca, lo[0], lo[1]);
-                mma(y[i][1], ca, lo[2], lo[3]);
-                mma(y[i][0], ca, hi[0], hi[1]);
-                mma(y[i][1], ca, hi[2], hi[3]);
-            }
-        }
+                for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(S[j][q]) & 0x7FFFFFFFu);
+            m = __reduce_max_sync(0xffffffffu, m);
+            const float2 ss = pow2_scale(m, 13);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float e0 = d.done[16 * i + (lane >> 2)], e1 = d.done[16 * i + 8 + (lane >> 2)];
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t sb[4];          // [2 * channel tile + k half]
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                y[i][p][0] = __fmul_rn(y[i][p][0], e0);
-                y[i][p][1] = __fmul_rn(y[i][p][1], e0);
-                y[i][p][2] = __fmul_rn(y[i][p][2], e1);
-                y[i][p][3] = __fmul_rn(y[i][p][3], e1);
-            }
-        }
+                for (int q = 0; q < 4; ++q)
+                    sb[q] = f16x2_of(__fmul_rn(S[2 * kk + (q & 1)][q & 2], ss.x), __fmul_rn(S[2 * kk + (q & 1)][(q & 2) + 1], ss.x));
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t xb[4];
-            frag_bt<128>(s_x, 16 * ks, 16 * w, lane, xb);
-#pragma unroll
-            for (int i = ks; i < 4; ++i) {
-                uint32_t mh[4], ml[4];
-                frag_a<128>(s_m, 16 * i, 16 * ks, lane, mh);
-                frag_a<128>(s_m + 8192, 16 * i, 16 * ks, lane, ml);
-                mma(y[i][0], ml, xb[0], xb[1]);
-                mma(y[i][1], ml, xb[2], xb[3]);
-                mma(y[i][0], mh, xb[0], xb[1]);
-                mma(y[i][1], mh, xb[2], xb[3]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int t = 16 * i + 8 * hf + (lane >> 2);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    uint32_t xv;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv) : "r"(tile128(s_x, t, 2 * w + p) + 4 * (lane & 3)));
-                    if (t < n)
-                        *reinterpret_cast<uint32_t*>(o.y + (int64_t)(t0 + t) * o.ldy + h * kP + 16 * w + 8 * p + 2 * (lane & 3)) =
-                            bf16x2_of(make_float2(__fmaf_rn(skip, bf16_lo(xv), y[i][p][2 * hf]),
-                                                  __fmaf_rn(skip, bf16_hi(xv), y[i][p][2 * hf + 1])));
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t ca[4];
+                    frag_a<256>(s_c, 16 * i, 64 * hv + 16 * kk, lane, ca);
+                    mma_h(y[i][0], ca, sb[0], sb[1]);
+                    mma_h(y[i][1], ca, sb[2], sb[3]);
                 }
             }
+            // the other half's tokens go to the warp that has the other 64 states of these channels
+            const float back = __fmul_rn(ss.y, tsc.x);
+            const uint32_t ex = s_ex + (uint32_t)((pw * 2 + (hv ^ 1)) * 2048 + lane * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e0 = __fmul_rn(d.done[16 * i + (lane >> 2)], back), e1 = __fmul_rn(d.done[16 * i + 8 + (lane >> 2)], back);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    y[i][p][0] = __fmul_rn(y[i][p][0], e0);
+                    y[i][p][1] = __fmul_rn(y[i][p][1], e0);
+                    y[i][p][2] = __fmul_rn(y[i][p][2], e1);
+                    y[i][p][3] = __fmul_rn(y[i][p][3], e1);
+                    if ((i >> 1) != hv)
+                        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};"
+                                     ::"r"(ex + (uint32_t)(((i & 1) * 2 + p) * 512)), "f"(y[i][p][0]), "f"(y[i][p][1]),
+                                     "f"(y[i][p][2]), "f"(y[i][p][3]) : "memory");
+                }
+            }
+        }
+        // ---- the scale of x over the warp's channels
+        uint32_t xm = 0u;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t xa[4];
+            frag_at<128>(s_x, 16 * ks, 16 * pw, lane, xa);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) xm = abs_max_bf16x2(xm, xa[q]);
+        }
+        const float2 xs = pow2_scale(__reduce_max_sync(0xffffffffu, xm), 13);
+        __syncthreads();                 // M and the exchanged parts are there
 
-        // ---- the state at the chunk's end
-        state_update(S, d.done[kQ - 1], s_x, s_b, d.left, d.dt, true, w, lane);
-        if (w == 0 && k + 1 < n_ch) chunk_decay(dec[(k + 1) & 1], raw0, raw1, min(kQ, it.len - (k + 1) * kQ), bias, a2, lane);
+        // ---- y of the warp's 32 tokens and 16 channels
+        {
+            float u[2][2][4];            // the chunk's own tokens
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) u[i][p][0] = u[i][p][1] = u[i][p][2] = u[i][p][3] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                if (ks > 2 * hv + 1) break;
+                uint32_t xb[4];
+                frag_bt<128>(s_x, 16 * ks, 16 * pw, lane, xb);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) xb[q] = bf16x2_to_f16x2(xb[q], xs.x);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (ks > 2 * hv + i) continue;
+                    uint32_t ma[4];
+                    frag_a<128>(s_m, 32 * hv + 16 * i, 16 * ks, lane, ma);
+                    mma_h(u[i][0], ma, xb[0], xb[1]);
+                    mma_h(u[i][1], ma, xb[2], xb[3]);
+                }
+            }
+            const float beta = __fmul_rn(__fmul_rn(tsc.x, tsc.y), __fmul_rn(d.kd, xs.y));
+            const uint32_t ex = s_ex + (uint32_t)((pw * 2 + hv) * 2048 + lane * 16);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t out[2][2];      // [row half][channel tile]
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const uint4 e4 = ptx::lds128(ex + (uint32_t)((i * 2 + p) * 512));
+                    const float part[4] = {__uint_as_float(e4.x), __uint_as_float(e4.y), __uint_as_float(e4.z), __uint_as_float(e4.w)};
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int t = 32 * hv + 16 * i + 8 * hf + (lane >> 2);
+                        uint32_t xv;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv) : "r"(tile128(s_x, t, 2 * pw + p) + 4 * (lane & 3)));
+                        float v[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float own = hv ? y[2 + i][p][2 * hf + e] : y[i][p][2 * hf + e];
+                            // the two halves of the states in one order for both warps
+                            const float in = hv ? __fadd_rn(part[2 * hf + e], own) : __fadd_rn(own, part[2 * hf + e]);
+                            v[e] = __fmaf_rn(u[i][p][2 * hf + e], beta, in);
+                        }
+                        out[hf][p] = bf16x2_of(make_float2(__fmaf_rn(skip, bf16_lo(xv), v[0]), __fmaf_rn(skip, bf16_hi(xv), v[1])));
+                    }
+                }
+                // a quad holds 16 channels of a row in pairs; lane q of it gathers channels 4 q .. 4 q + 3
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int from = (lane & ~3) | (2 * (lane & 1));
+                    const uint32_t a0 = __shfl_sync(0xffffffffu, out[hf][0], from), a1 = __shfl_sync(0xffffffffu, out[hf][0], from + 1);
+                    const uint32_t b0 = __shfl_sync(0xffffffffu, out[hf][1], from), b1 = __shfl_sync(0xffffffffu, out[hf][1], from + 1);
+                    const int t = 32 * hv + 16 * i + 8 * hf + (lane >> 2);
+                    if (t < n)
+                        *reinterpret_cast<uint2*>(o.y + (int64_t)(t0 + t) * o.ldy + h * kP + 16 * pw + 4 * (lane & 3)) =
+                            lane & 2 ? make_uint2(b0, b1) : make_uint2(a0, a1);
+                }
+            }
+        }
+        // ---- the state at the chunk's end: w x as two fp16 parts
+        {
+            float D[8][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) D[j][0] = D[j][1] = D[j][2] = D[j][3] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                float2 w0 = *reinterpret_cast<const float2*>(d.wl + 16 * ks + 2 * (lane & 3));
+                float2 w1 = *reinterpret_cast<const float2*>(d.wl + 16 * ks + 8 + 2 * (lane & 3));
+                w0 = make_float2(__fmul_rn(w0.x, xs.x), __fmul_rn(w0.y, xs.x));
+                w1 = make_float2(__fmul_rn(w1.x, xs.x), __fmul_rn(w1.y, xs.x));
+                uint32_t xa[4], hi[4], lo[4];
+                frag_at<128>(s_x, 16 * ks, 16 * pw, lane, xa);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 ww = q < 2 ? w0 : w1;
+                    split_f16x2(__fmul_rn(bf16_lo(xa[q]), ww.x), __fmul_rn(bf16_hi(xa[q]), ww.y), hi[q], lo[q]);
+                }
+                uint32_t bb[4][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) frag_bt<256>(s_b, 16 * ks, 64 * hv + 16 * q, lane, bb[q]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) mma_h(D[q], lo, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) mma_h(D[q], hi, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
+            }
+            const float keep = d.done[kQ - 1], back = __fmul_rn(__fmul_rn(tsc.y, d.kd), xs.y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) S[j][q] = __fmaf_rn(D[j][q], back, __fmul_rn(S[j][q], keep));
+        }
     }
     ptx::cp_async_wait<0>();
-    if (o.final_state && (it.flags & kLast)) state_store(S, o.final_state + sh, w, lane);
+    if (o.final_state && (it.flags & kLast)) {
+        float* dst = o.final_state + sh + s_at;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(S[j][0], S[j][1]);
+            *reinterpret_cast<float2*>(dst + 8 * kN + 8 * j) = make_float2(S[j][2], S[j][3]);
+        }
+    }
 }
 
 }  // namespace
@@ -416,7 +647,7 @@ constexpr int kStateSmem = 2 * (16384 + 8192) + 16384 + 2 * (int)sizeof(Decay) +
 
 // ------------------------------------------------------------------------------- host
 
-Plan make_plan(int nheads, int total, int nseq, bool backward) {
+Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     Plan p{};
     // a CTA's fair share: two CTAs on each of 148 SMs; an item may be a quarter longer
     int64_t share = ((int64_t)total * nheads + 295) / 296;
@@ -435,6 +666,9 @@ Plan make_plan(int nheads, int total, int nseq, bool backward) {
     p.seq_items = o;   o = up256(o + sizeof(Item) * (size_t)p.cap_items);
     p.seq_slots = o;   o = up256(o + sizeof(int2) * (size_t)nseq);
     p.chunks = o;      o = up256(o + sizeof(Chunk) * (size_t)p.cap_chunks);
+    const size_t tiles = p.direct || backward ? 0 : (size_t)p.cap_chunks * ngroups;
+    p.tiles = o;       o = up256(o + tiles * 2 * kQ * kN * 2);
+    p.tile_scale = o;  o = up256(o + tiles * sizeof(float2));
     const size_t slots = (backward ? 2 : 1) * (size_t)p.cap_slots * nheads;
     p.seg_decay = o;   o = up256(o + 4 * slots);
     p.seg_state = o;
@@ -473,6 +707,8 @@ Args make_args(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int tot
     a.seq_items = reinterpret_cast<Item*>(ws + p.seq_items);
     a.seq_slots = reinterpret_cast<int2*>(ws + p.seq_slots);
     a.chunks = reinterpret_cast<Chunk*>(ws + p.chunks);
+    a.tiles = reinterpret_cast<uint16_t*>(ws + p.tiles);
+    a.tile_scale = reinterpret_cast<float2*>(ws + p.tile_scale);
     a.seg_state = reinterpret_cast<float*>(ws + p.seg_state);
     a.seg_decay = reinterpret_cast<float*>(ws + p.seg_decay);
     return a;
@@ -516,7 +752,8 @@ dfssm_status setup() {
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_ready[dev]) {
         const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        if (cudaFuncSetAttribute(scan_fwd_kernel, at, kFwdSmem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(scan_fwd_kernel<false>, at, kFwdSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(scan_fwd_kernel<true>, at, kFwdSmem) != cudaSuccess ||
             cudaFuncSetAttribute(scan_state_kernel<false>, at, kStateSmem) != cudaSuccess ||
             cudaFuncSetAttribute(scan_state_kernel<true>, at, kStateSmem) != cudaSuccess ||
             setup_bwd() != cudaSuccess)
@@ -557,7 +794,7 @@ extern "C" dfssm_status dfssm_ssm_scan_workspace_bytes(const dfssm_scan_dims* di
     const dfssm_status st = check_dims(dims, total, nseq);
     if (st != DFSSM_OK) return st;
     if (!bytes) return DFSSM_ERR_INVALID_ARG;
-    *bytes = backward ? bwd_workspace(dims, total, nseq) : make_plan(dims->nheads, total, nseq, false).total;
+    *bytes = backward ? bwd_workspace(dims, total, nseq) : make_plan(dims->nheads, dims->ngroups, total, nseq, false).total;
     return DFSSM_OK;
 }
 
@@ -569,7 +806,7 @@ extern "C" dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const df
     if (!y || !al16(y) || y_stride < (int64_t)dims->nheads * kP || y_stride % 8 != 0 || y_stride > ((int64_t)1 << 30) ||
         !al16(final_state))
         return DFSSM_ERR_INVALID_ARG;
-    const Plan p = make_plan(dims->nheads, total, nseq, false);
+    const Plan p = make_plan(dims->nheads, dims->ngroups, total, nseq, false);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < p.total)
         return DFSSM_ERR_INVALID_ARG;
     if ((st = setup()) != DFSSM_OK) return st;
@@ -580,6 +817,11 @@ extern "C" dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const df
     o.ldy = y_stride;
     o.final_state = final_state;
     if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, StateArgs{}, 1, s) != cudaSuccess) return DFSSM_ERR_CUDA;
-    scan_fwd_kernel<<<(a.direct ? nseq : a.cap_items) * a.nheads, kThreads, kFwdSmem, s>>>(a, o);
+    if (a.direct) {
+        scan_fwd_kernel<false><<<nseq * a.nheads, kFwdThreads, kFwdSmem, s>>>(a, o);
+    } else {
+        scan_tiles_kernel<<<2 * a.cap_chunks * dims->ngroups, 256, 0, s>>>(a);
+        scan_fwd_kernel<true><<<a.cap_items * a.nheads, kFwdThreads, kFwdSmem, s>>>(a, o);
+    }
     return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
 }

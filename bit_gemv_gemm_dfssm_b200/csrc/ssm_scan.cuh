@@ -12,6 +12,8 @@
 
 #include <cstdint>
 
+#include <cuda_fp16.h>
+
 #include "dfssm_internal.cuh"
 #include "epilogue.cuh"
 #include "ptx.cuh"
@@ -64,6 +66,8 @@ struct Args {
     Item* seq_items;                   // the same in sequence order
     int2* seq_slots;                   // [nseq] first slot and segments of a cut sequence (0 segments: not cut)
     Chunk* chunks;
+    uint16_t* tiles;                   // [chunks][groups][C, B][64][128] fp16, scaled (scan_tiles_kernel)
+    float2* tile_scale;                // [chunks][groups] 2^-k of C and of B
     float* seg_state;                  // [1 or 2][cap_slots][H][64][128]: what a cut sequence's segments start from
     float* seg_decay;                  // [1 or 2][cap_slots][H] (1: the gradient's, backward in time)
 };
@@ -120,6 +124,37 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the same with fp16 operands
+__device__ __forceinline__ void mma_h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The power of two 2^k that brings m (a largest magnitude, as bits) to [2^top, 2^(top + 1)), and 2^-k. k is kept
+// within +-100 (a zero maximum: the largest).
+__device__ __forceinline__ float2 pow2_scale(uint32_t m_bits, int top) {
+    const int k = max(-100, min(100, top + 127 - (int)(m_bits >> 23)));
+    return make_float2(__int_as_float((127 + k) << 23), __int_as_float((127 - k) << 23));
+}
+
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// (a, b) as two fp16 pairs whose sum is (a, b) to 2^-23 of each (or to 2^-25 below fp16's normal range)
+__device__ __forceinline__ void split_f16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    const float2 f = __half22float2(h);
+    lo = f16x2_of(__fsub_rn(a, f.x), __fsub_rn(b, f.y));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Fragments of a tile stored [row][col] (32-lane addresses; see the m16n8k16 register layout):
@@ -299,9 +334,9 @@ __device__ __forceinline__ void state_update(StateFrag& s, float keep, uint32_t 
 // ---- host side: the call's plan and workspace
 struct Plan {
     int seg_len, direct, cap_items, cap_chunks, cap_slots;
-    size_t count, items, seq_items, seq_slots, chunks, seg_state, seg_decay, total;
+    size_t count, items, seq_items, seq_slots, chunks, tiles, tile_scale, seg_state, seg_decay, total;
 };
-Plan make_plan(int nheads, int total, int nseq, bool backward);
+Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward);
 dfssm_status check_call(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int total, int nseq);
 dfssm_status setup();
 Args make_args(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int total, int nseq, const Plan& p, uint8_t* ws);

@@ -615,7 +615,7 @@ cudaError_t setup_bwd() {
 }
 
 size_t bwd_workspace(const dfssm_scan_dims* d, int total, int nseq) {
-    return bwd_ws(d, total, nseq, make_plan(d->nheads, total, nseq, true)).total;
+    return bwd_ws(d, total, nseq, make_plan(d->nheads, d->ngroups, total, nseq, true)).total;
 }
 
 }  // namespace scan
@@ -641,7 +641,7 @@ extern "C" dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const df
     const void* words[3] = {gr->ddt_bias, gr->da_log, gr->dd_skip};
     for (const void* p : words)
         if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return DFSSM_ERR_INVALID_ARG;
-    const Plan p = make_plan(dims->nheads, total, nseq, true);
+    const Plan p = make_plan(dims->nheads, dims->ngroups, total, nseq, true);
     const BwdWs w = bwd_ws(dims, total, nseq, p);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < w.total)
         return DFSSM_ERR_INVALID_ARG;

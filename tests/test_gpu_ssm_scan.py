@@ -2,8 +2,9 @@
 
 Tolerances. Every result is a sum of products, and its error is bounded by a factor f times the same
 sum of magnitudes (the recurrence run on absolute values):
-* x, B, C and dy enter exactly; the second bf16 operand (M, W, S, dS) is two parts, 2^-17 of its value (the
-  state's own update three parts, 2^-24); fp32 accumulators round at most 2^-23 per MMA step, at most 32
+* x, B, C and dy enter exactly. In y, M and S are one fp16 number each: half a step, 2^-11 of the value,
+  added to f for y. Elsewhere the second operand (M, W, S, dS) is two bf16 parts, 2^-17 of its value, or in the
+  state's own update three bf16 or two fp16 parts, 2^-22; fp32 accumulators round at most 2^-23 per MMA step, at most 32
   steps per chunk and result, 2^-18; a result passes through at most three such products: 2^-15.
 * a decay exp(cum_t - cum_s) carries the error of its exponent: the chunk's sums round 2^-24 of at most
   their largest value c (in units of log 2) in at most 8 steps: 2^-21 c; exp2f and the products with dt
@@ -179,7 +180,7 @@ def check_fwd(a, y, fin):
         mag, mend, _ = forward64(x.abs(), b.abs(), c.abs(), dt, decay, d.abs(), s0.abs())
         t0 = int(a["cu"][s])
         used[t0:t0 + n] = True
-        close(y[t0:t0 + n, :nh * P].reshape(n, nh, P), want, f * mag, 2.0 ** -8)
+        close(y[t0:t0 + n, :nh * P].reshape(n, nh, P), want, (f + 2.0 ** -11) * mag, 2.0 ** -8)
         if fin is not None:
             close(fin[s], end, (f - 2.0 ** -14 + 2.0 ** -16) * mend)
     assert (y[:, nh * P:] == 77).all() and (y[~used] == 77).all()          # padding columns, rows of no sequence
