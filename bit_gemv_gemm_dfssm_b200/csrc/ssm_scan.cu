@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
             } else {
                 len = t1 - t0;
                 nseg = len <= a.seg_len ? 1 : (len + a.seg_len - 1) / a.seg_len;
-                nch = (len + kQ - 1) / kQ;
+                nch = (len + a.chunk - 1) / a.chunk;
             }
         }
         int ti = 0, tc = 0, ts = 0;
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
             } else {
                 for (int k = 0; k < nseg; ++k) {
                     const int at = k * a.seg_len;
-                    a.seq_items[i0 + k] = Item{s, t0 + at, min(a.seg_len, len - at), c0 + at / kQ, s1 - cut + k,
+                    a.seq_items[i0 + k] = Item{s, t0 + at, min(a.seg_len, len - at), c0 + at / a.chunk, s1 - cut + k,
                                                (k == 0 ? kFirst : 0) | (k == nseg - 1 ? kLast : 0) | (nseg > 1 ? kCut : 0)};
                 }
             }
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
     }
     for (int i = threadIdx.x >> 5; i < n_items; i += kTableThreads / 32) {
         const Item it = a.seq_items[i];
-        for (int k = threadIdx.x & 31; kQ * k < it.len; k += 32)
-            a.chunks[it.chunk0 + k] = Chunk{it.t0 + kQ * k, min(kQ, it.len - kQ * k)};
+        for (int k = threadIdx.x & 31; a.chunk * k < it.len; k += 32)
+            a.chunks[it.chunk0 + k] = Chunk{it.t0 + a.chunk * k, min(a.chunk, it.len - a.chunk * k)};
     }
 }
 
@@ -132,7 +132,7 @@ struct FwdOut {
 };
 
 // ---- B and C in fp16
-// fp16 holds a bf16 value exactly over 2^-24 .. 2^15; a tile of 64 tokens is scaled by a power of two that brings its
+// fp16 holds a bf16 value exactly over 2^-24 .. 2^15; a tile is scaled by a power of two that brings its
 // largest magnitude to [2^3, 2^4), so that only values below 2^-17 of that lose bits, and G = C B^T stays below 2^15.
 
 constexpr int kTileTop = 3;
@@ -145,8 +145,8 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
 }
 
 // CTA (chunk, group, C or B): the tile, rows behind the chunk's tokens as zeros
-__global__ void __launch_bounds__(256) scan_tiles_kernel(const Args a) {
-    __shared__ uint32_t red[8];
+__global__ void __launch_bounds__(512) scan_tiles_kernel(const Args a) {
+    __shared__ uint32_t red[16];
     const int ngroups = a.nheads / a.per_group;
     const int side = blockIdx.x & 1, g = (blockIdx.x >> 1) % ngroups, ci = (blockIdx.x >> 1) / ngroups;
     if (ci >= a.count[1]) return;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256) scan_tiles_kernel(const Args a) {
     uint32_t m = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int row = (threadIdx.x >> 4) + 16 * i, pc = threadIdx.x & 15;
+        const int row = (threadIdx.x >> 4) + 32 * i, pc = threadIdx.x & 15;
         v[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < ch.n) v[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(ch.t0 + row) * ld + 8 * pc);
         m = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(m, v[i].x), v[i].y), v[i].z), v[i].w);
@@ -166,12 +166,12 @@ __global__ void __launch_bounds__(256) scan_tiles_kernel(const Args a) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, red[w]);
+    for (int w = 0; w < 16; ++w) m = max(m, red[w]);
     const float2 sc = pow2_scale(m, kTileTop);
-    uint16_t* dst = a.tiles + (((int64_t)ci * ngroups + g) * 2 + side) * (kQ * kN);
+    uint16_t* dst = a.tiles + (((int64_t)ci * ngroups + g) * 2 + side) * (128 * kN);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(dst + 8 * (threadIdx.x + 256 * i)) =
+        *reinterpret_cast<uint4*>(dst + 8 * (threadIdx.x + 512 * i)) =
             make_uint4(bf16x2_to_f16x2(v[i].x, sc.x), bf16x2_to_f16x2(v[i].y, sc.x), bf16x2_to_f16x2(v[i].z, sc.x),
                        bf16x2_to_f16x2(v[i].w, sc.x));
     if (threadIdx.x == 0) (side ? &a.tile_scale[(int64_t)ci * ngroups + g].y : &a.tile_scale[(int64_t)ci * ngroups + g].x)[0] = sc.y;
@@ -207,8 +207,7 @@ __device__ __forceinline__ void fwd_decay(FwdDecay& f, Decay& d, float raw0, flo
     if (lane == 0) f.kd = sc.y;
 }
 
-// TILES: C and B from scan_tiles_kernel; otherwise this kernel converts each chunk's tiles itself.
-template <bool TILES>
+// The kernel of short calls: it converts each chunk's tiles of B and C itself, so that a call is one launch.
 __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, const FwdOut o) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Decay scratch;                         // of warp 0
@@ -219,7 +218,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
     uint32_t* s_max = reinterpret_cast<uint32_t*>(dec + 2);                // [2][8]
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int pw = w & 3, hv = w >> 2;                // channels 16 pw ..; states 64 hv ..; tokens 32 hv .. of y
-    const int ngroups = a.nheads / a.per_group;
     const int h = blockIdx.x % a.nheads, g = h / a.per_group;
     Item it;
     if (!get_item(a, blockIdx.x / a.nheads, it) || it.len < 0) return;
@@ -232,14 +230,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
         if (k < n_ch) {
             const int t0 = it.t0 + k * kQ, n = min(kQ, it.len - k * kQ);
             const uint32_t st = base + (k & 1) * kStage;
-            if (TILES) {
-                const uint16_t* tl = a.tiles + ((int64_t)(it.chunk0 + k) * ngroups + g) * 2 * (kQ * kN);
-                load_tile<128, kFwdThreads>(st, tl, kN, 0, kQ, tid);
-                load_tile<128, kFwdThreads>(st + 16384, tl + kQ * kN, kN, 0, kQ, tid);
-            } else {
-                load_tile<128, kFwdThreads>(st, c, a.ldc, t0, n, tid);
-                load_tile<128, kFwdThreads>(st + 16384, b, a.ldb, t0, n, tid);
-            }
+            load_tile<128, kFwdThreads>(st, c, a.ldc, t0, n, tid);
+            load_tile<128, kFwdThreads>(st + 16384, b, a.ldb, t0, n, tid);
             load_tile<64, kFwdThreads>(st + 32768, x, a.ldx, t0, n, tid);
         }
         ptx::cp_async_commit();
@@ -286,9 +278,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
         __syncthreads();                 // this chunk's tiles and decays are there; the last one's are free
         fetch(k + 1);
         float2 tsc;                      // 2^-k of C and of B
-        if (TILES) {
-            tsc = a.tile_scale[(int64_t)(it.chunk0 + k) * ngroups + g];
-        } else {
+        {
             uint4 v[2][4];
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
@@ -647,18 +637,22 @@ constexpr int kStateSmem = 2 * (16384 + 8192) + 16384 + 2 * (int)sizeof(Decay) +
 
 // ------------------------------------------------------------------------------- host
 
+// Forward calls of up to this many tokens take the warp-MMA kernel in one launch.
+constexpr int kDirectTokens = 512;
+
 Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     Plan p{};
     // a CTA's fair share: two CTAs on each of 148 SMs; an item may be a quarter longer
     int64_t share = ((int64_t)total * nheads + 295) / 296;
     share += share / 4;
-    if (share < 512) share = 512;
-    p.seg_len = (int)((share + kQ - 1) / kQ * kQ);
-    if (p.seg_len > (total + kQ - 1) / kQ * kQ) p.seg_len = (total + kQ - 1) / kQ * kQ;
-    // small calls save the table's launch: every sequence is one item, in the order given
-    p.direct = !backward && total <= p.seg_len && total <= 4096;
+    if (share < 512) share = 512;                          // 512 tokens at least
+    p.seg_len = (int)((share + 127) / 128 * 128);
+    if (p.seg_len > (total + 127) / 128 * 128) p.seg_len = (total + 127) / 128 * 128;
+    // short calls save the launches of the table and of the tiles: every sequence is one item, in the order given
+    p.direct = !backward && total <= kDirectTokens;
+    p.chunk = backward ? kQ : 128;
     p.cap_items = total / p.seg_len + nseq;
-    p.cap_chunks = total / kQ + nseq;
+    p.cap_chunks = total / p.chunk + nseq;
     p.cap_slots = 2 * (total / p.seg_len) + 1;             // a cut sequence of n tokens has at most 2 n / seg_len segments
     size_t o = 256;                                        // error word
     p.count = o;       o += 256;
@@ -667,7 +661,7 @@ Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     p.seq_slots = o;   o = up256(o + sizeof(int2) * (size_t)nseq);
     p.chunks = o;      o = up256(o + sizeof(Chunk) * (size_t)p.cap_chunks);
     const size_t tiles = p.direct || backward ? 0 : (size_t)p.cap_chunks * ngroups;
-    p.tiles = o;       o = up256(o + tiles * 2 * kQ * kN * 2);
+    p.tiles = o;       o = up256(o + tiles * 2 * 128 * kN * 2);
     p.tile_scale = o;  o = up256(o + tiles * sizeof(float2));
     const size_t slots = (backward ? 2 : 1) * (size_t)p.cap_slots * nheads;
     p.seg_decay = o;   o = up256(o + 4 * slots);
@@ -698,6 +692,7 @@ Args make_args(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int tot
     a.nseq = nseq;
     a.seg_len = p.seg_len;
     a.direct = p.direct;
+    a.chunk = p.chunk;
     a.cap_items = p.cap_items;
     a.cap_chunks = p.cap_chunks;
     a.cap_slots = p.cap_slots;
@@ -720,6 +715,8 @@ dfssm_status check_dims(const dfssm_scan_dims* d, int total, int nseq) {
     if (d->nheads < 1 || d->nheads > 1024 || d->ngroups < 1 || d->nheads % d->ngroups != 0)
         return DFSSM_ERR_UNSUPPORTED_SHAPE;
     if (total < 1 || total > (1 << 22) || nseq < 1 || nseq > 65536) return DFSSM_ERR_UNSUPPORTED_SHAPE;
+    // rows of the tiles of B and C, which the tensor map counts in 32 bits
+    if (((int64_t)total / 128 + nseq) * d->ngroups * 256 > INT32_MAX) return DFSSM_ERR_UNSUPPORTED_SHAPE;
     return DFSSM_OK;
 }
 
@@ -752,8 +749,7 @@ dfssm_status setup() {
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_ready[dev]) {
         const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        if (cudaFuncSetAttribute(scan_fwd_kernel<false>, at, kFwdSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(scan_fwd_kernel<true>, at, kFwdSmem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(scan_fwd_kernel, at, kFwdSmem) != cudaSuccess || setup_tc() != cudaSuccess ||
             cudaFuncSetAttribute(scan_state_kernel<false>, at, kStateSmem) != cudaSuccess ||
             cudaFuncSetAttribute(scan_state_kernel<true>, at, kStateSmem) != cudaSuccess ||
             setup_bwd() != cudaSuccess)
@@ -812,16 +808,14 @@ extern "C" dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const df
     if ((st = setup()) != DFSSM_OK) return st;
     const Args a = make_args(dims, in, total, nseq, p, static_cast<uint8_t*>(workspace));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    FwdOut o{};
-    o.y = static_cast<uint16_t*>(y);
-    o.ldy = y_stride;
-    o.final_state = final_state;
-    if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, StateArgs{}, 1, s) != cudaSuccess) return DFSSM_ERR_CUDA;
     if (a.direct) {
-        scan_fwd_kernel<false><<<nseq * a.nheads, kFwdThreads, kFwdSmem, s>>>(a, o);
+        const FwdOut o{static_cast<uint16_t*>(y), y_stride, final_state};
+        scan_fwd_kernel<<<nseq * a.nheads, kFwdThreads, kFwdSmem, s>>>(a, o);
     } else {
-        scan_tiles_kernel<<<2 * a.cap_chunks * dims->ngroups, 256, 0, s>>>(a);
-        scan_fwd_kernel<true><<<a.cap_items * a.nheads, kFwdThreads, kFwdSmem, s>>>(a, o);
+        if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, StateArgs{}, 1, s) != cudaSuccess)
+            return DFSSM_ERR_CUDA;
+        scan_tiles_kernel<<<2 * a.cap_chunks * dims->ngroups, 512, 0, s>>>(a);
+        if (launch_tc(a, static_cast<uint16_t*>(y), y_stride, final_state, s) != cudaSuccess) return DFSSM_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
 }

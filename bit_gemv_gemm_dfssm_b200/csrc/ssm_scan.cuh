@@ -57,7 +57,8 @@ struct Args {
     const int32_t* cu;
     int nheads, per_group;             // heads; heads per group
     int total, nseq;
-    int seg_len;                       // longest item (a multiple of 64)
+    int seg_len;                       // longest item (a multiple of the chunk)
+    int chunk;                         // tokens per chunk of the table: 64, or 128 for the tensor-core forward
     int direct;                        // 1: no table, item i is sequence i
     int cap_items, cap_chunks, cap_slots;
     uint32_t* err;
@@ -66,7 +67,7 @@ struct Args {
     Item* seq_items;                   // the same in sequence order
     int2* seq_slots;                   // [nseq] first slot and segments of a cut sequence (0 segments: not cut)
     Chunk* chunks;
-    uint16_t* tiles;                   // [chunks][groups][C, B][64][128] fp16, scaled (scan_tiles_kernel)
+    uint16_t* tiles;                   // [chunks][groups][C, B][128][128] fp16, scaled (scan_tiles_kernel)
     float2* tile_scale;                // [chunks][groups] 2^-k of C and of B
     float* seg_state;                  // [1 or 2][cap_slots][H][64][128]: what a cut sequence's segments start from
     float* seg_decay;                  // [1 or 2][cap_slots][H] (1: the gradient's, backward in time)
@@ -333,7 +334,7 @@ __device__ __forceinline__ void state_update(StateFrag& s, float keep, uint32_t 
 
 // ---- host side: the call's plan and workspace
 struct Plan {
-    int seg_len, direct, cap_items, cap_chunks, cap_slots;
+    int seg_len, chunk, direct, cap_items, cap_chunks, cap_slots;
     size_t count, items, seq_items, seq_slots, chunks, tiles, tile_scale, seg_state, seg_decay, total;
 };
 Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward);
@@ -354,6 +355,9 @@ struct StateArgs {
 cudaError_t launch_segment_starts(const Args& a, const StateArgs& o, int directions, cudaStream_t s);
 // the states and, backward in time, their gradients at every chunk
 cudaError_t launch_states(const Args& a, const StateArgs& o, cudaStream_t s);
+// the forward kernel of long calls (ssm_scan_tc.cu)
+cudaError_t setup_tc();
+cudaError_t launch_tc(const Args& a, uint16_t* y, int64_t ldy, float* final_state, cudaStream_t s);
 cudaError_t setup_bwd();
 size_t bwd_workspace(const dfssm_scan_dims* dims, int total, int nseq);
 

@@ -1,0 +1,504 @@
+// The scan's forward pass for long calls on the 5th-generation tensor cores (ssm_scan.cuh has the formulas, with chunks
+// of 128 tokens here).
+//
+// A persistent-in-time CTA takes one head through one item, chunk by chunk. Per chunk four products, all fp16
+// operands with fp32 accumulators in tensor memory:
+//   G  = C B^T          128 x 128 x 128   both tiles as scan_tiles_kernel left them
+//   Yi = C S^T          128 x  64 x 128   S (the state, scaled, one fp16 part) stored [state][channel]
+//   Ya = M X            128 x  64 x 128   M = G exp(cum_t - cum_s) dt_s, causal, from tensor memory
+//   D  = B^T (w X)      128 x  64 x 128   twice: w x as two fp16 parts
+// and y = exp(cum_t) Yi + Ya + d_skip x, S = exp(cum_128) S + D. The state itself stays in fp32 registers; every
+// scale is a power of two. B^T, X, S and w X are read along their rows (M- or N-major operands), so nothing is
+// transposed.
+//
+// Roles (20 warps): TMA; MMA issue; decays (one warp); and four groups of four warps, one thread per row:
+//   M group: G from tensor memory -> M back into tensor memory;
+//   X group: x -> fp16 in place, w x -> two tiles;
+//   S group: thread n holds S[0..63][n]: S -> fp16 tile, then S = keep S + D;
+//   Y group: Yi, Ya, x -> y in bf16 over the x tile, out as whole rows.
+// They meet in mbarriers only, so that the products of one chunk run beside the conversions of the next. Every
+// wait is bounded.
+#include "ssm_scan.cuh"
+
+namespace dfssm {
+namespace scan {
+
+namespace {
+
+constexpr int kT = 128;                          // tokens per chunk
+constexpr int kTcThreads = 20 * 32;
+constexpr int kTile = 16384;                     // 128 rows of 128 bytes
+constexpr int kStageTc = 5 * kTile;              // C (2 column blocks), B (2), X
+struct TcDecay {
+    float cum[kT];       // log 2 units
+    float dts[kT];       // dt 2^kd
+    float wl[kT];        // dts exp(cum_128 - cum_t)
+    float done[kT];      // exp(cum_t)
+    float kd, kc, kb;    // 2^-kd, 2^-k of C, of B
+    float pad;
+};
+struct TcShared {
+    TcDecay dec[2];
+    float kx[2];         // 2^-k of the x tile
+    float ks[2];         // of the state tile
+    uint32_t red[2][4];  // maxima of the X and of the S group's warps
+    uint64_t in_full[2], in_empty[2], dec_full[2], dec_empty[2], g_full[2], g_empty[2];
+    uint64_t m_full, m_empty, x_full, wx_empty, d_full, d_empty, s_full, s_empty, y_full, y_empty, drain;
+    uint32_t tmem, abort;
+};
+constexpr int kTcSmem = 2 * kStageTc + 3 * kTile + (int)sizeof(TcShared) + 1024;
+static_assert(kTcSmem <= 232448, "shared memory");
+
+// tensor memory columns
+constexpr uint32_t kColG = 0, kColM = 256, kColYi = 320, kColYa = 384, kColD = 448;
+
+struct TcArgs {
+    Args a;
+    uint16_t* y;
+    int64_t ldy;
+    float* final_state;
+};
+
+constexpr uint32_t kIdescBase = (1u << 4) | ((uint32_t)(128 >> 4) << 24);       // D fp32, A and B fp16, M 128
+constexpr uint32_t kIdescG = kIdescBase | ((uint32_t)(128 >> 3) << 17);
+constexpr uint32_t kIdescY = kIdescBase | ((uint32_t)(64 >> 3) << 17) | (1u << 16);               // B along N
+constexpr uint32_t kIdescD = kIdescBase | ((uint32_t)(64 >> 3) << 17) | (1u << 16) | (1u << 15);  // A along M, B along N
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_x, const TcArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    const Args& a = p.a;
+    const int ngroups = a.nheads / a.per_group;
+    const int h = blockIdx.x % a.nheads, g = h / a.per_group;
+    Item it;
+    if (!get_item(a, blockIdx.x / a.nheads, it) || it.len < 0) return;
+    uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t base = ptx::smem_u32(smem);
+    const uint32_t s_wx = base + 2 * kStageTc, s_st = s_wx + 2 * kTile;
+    TcShared& sh = *reinterpret_cast<TcShared*>(smem + 2 * kStageTc + 3 * kTile);
+    volatile uint32_t* abort_flag = &sh.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_ch = (it.len + kT - 1) / kT;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(&sh.in_full[s], 1);
+            ptx::mbar_init(&sh.in_empty[s], 5);       // the MMAs, four Y warps
+            ptx::mbar_init(&sh.dec_full[s], 1);
+            ptx::mbar_init(&sh.dec_empty[s], 16);
+            ptx::mbar_init(&sh.g_full[s], 1);
+            ptx::mbar_init(&sh.g_empty[s], 4);
+        }
+        ptx::mbar_init(&sh.m_full, 4);
+        ptx::mbar_init(&sh.m_empty, 1);
+        ptx::mbar_init(&sh.x_full, 4);
+        ptx::mbar_init(&sh.wx_empty, 1);
+        ptx::mbar_init(&sh.d_full, 1);
+        ptx::mbar_init(&sh.d_empty, 4);
+        ptx::mbar_init(&sh.s_full, 4);
+        ptx::mbar_init(&sh.s_empty, 1);
+        ptx::mbar_init(&sh.y_full, 1);
+        ptx::mbar_init(&sh.y_empty, 4);
+        ptx::mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&sh.tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    // a bounded wait; a role that gives up takes all others along
+    auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (ptx::mbar_wait(bar, parity) && !*abort_flag) return true;
+        atomicOr(a.err, DFSSM_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {       // the whole warp, through lane 0
+        bool ok = true;
+        if (lane == 0) ok = wait1(bar, parity);
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar);
+    };
+    const int row = 32 * (warp & 3) + lane;          // of the groups' threads
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    auto piece = [](uint32_t tile, int r, int pc) { return tile + (uint32_t)(r * 128 + 16 * (pc ^ (r & 7))); };
+    auto sts128 = [](uint32_t at, const uint32_t* v) {
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int k = 0;
+            for (; k < n_ch; ++k) {
+                const int s = k & 1;
+                if (!wait1(&sh.in_empty[s], ((uint32_t)(k >> 1) & 1u) ^ 1u)) break;
+                uint8_t* st = smem + s * kStageTc;
+                const int trow = ((it.chunk0 + k) * ngroups + g) * 2 * kT;
+                ptx::mbar_arrive_expect_tx(&sh.in_full[s], kStageTc);
+                ptx::tma_load_2d(st, &map_t, 0, trow, &sh.in_full[s]);
+                ptx::tma_load_2d(st + kTile, &map_t, 64, trow, &sh.in_full[s]);
+                ptx::tma_load_2d(st + 2 * kTile, &map_t, 0, trow + kT, &sh.in_full[s]);
+                ptx::tma_load_2d(st + 3 * kTile, &map_t, 64, trow + kT, &sh.in_full[s]);
+                ptx::tma_load_2d(st + 4 * kTile, &map_x, h * kP, it.t0 + k * kT, &sh.in_full[s]);
+            }
+            if (*abort_flag)                           // the copies still in flight land before the CTA ends
+                for (int i = max(0, k - 2); i < k; ++i) ptx::mbar_wait(&sh.in_full[i & 1], (uint32_t)(i >> 1) & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            auto product_g = [&](int k) -> bool {
+                const int s = k & 1;
+                const uint32_t ph = (uint32_t)(k >> 1) & 1u, st = base + s * kStageTc;
+                if (!wait1(&sh.in_full[s], ph) || !wait1(&sh.g_empty[s], ph ^ 1u)) return false;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ptx::mma_f16(tmem + kColG + 128u * s, ptx::kmajor_sw128_desc(st + (j >> 2) * kTile) + 2 * (j & 3),
+                                 ptx::kmajor_sw128_desc(st + (2 + (j >> 2)) * kTile) + 2 * (j & 3), kIdescG, j > 0);
+                ptx::mma_commit(&sh.g_full[s]);
+                return true;
+            };
+            bool ok = n_ch == 0 || product_g(0);
+            for (int k = 0; k < n_ch && ok; ++k) {
+                const int s = k & 1;
+                const uint32_t ph = (uint32_t)k & 1u, st = base + s * kStageTc;
+                // D = B^T (w X): lo, then hi
+                ok = wait1(&sh.x_full, ph) && wait1(&sh.d_empty, ph ^ 1u);
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int part = 1; part >= 0; --part)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        ptx::mma_f16(tmem + kColD, ptx::mnmajor_sw128_desc(st + 2 * kTile + j * 2048, kTile),
+                                     ptx::mnmajor_sw128_desc(s_wx + part * kTile + j * 2048, 1024), kIdescD, part == 0 || j > 0);
+                ptx::mma_commit(&sh.d_full);
+                ptx::mma_commit(&sh.wx_empty);
+                if (k + 1 < n_ch) ok = product_g(k + 1);
+                // Yi = C S^T
+                ok = ok && wait1(&sh.s_full, ph) && wait1(&sh.y_empty, ph ^ 1u);
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ptx::mma_f16(tmem + kColYi, ptx::kmajor_sw128_desc(st + (j >> 2) * kTile) + 2 * (j & 3),
+                                 ptx::mnmajor_sw128_desc(s_st + j * 2048, 1024), kIdescY, j > 0);
+                ptx::mma_commit(&sh.s_empty);
+                // Ya = M X
+                ok = wait1(&sh.m_full, ph);
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ptx::mma_f16_ts(tmem + kColYa, tmem + kColM + 8 * j, ptx::mnmajor_sw128_desc(st + 4 * kTile + j * 2048, 1024),
+                                    kIdescY, j > 0);
+                ptx::mma_commit(&sh.m_empty);
+                ptx::mma_commit(&sh.y_full);
+                ptx::mma_commit(&sh.in_empty[s]);
+            }
+            if (!ok) {                                 // the MMAs issued so far end before tensor memory is given back
+                ptx::mma_commit(&sh.drain);
+                ptx::mbar_wait(&sh.drain, 0u);
+            }
+        }
+    } else if (warp == 2) {
+        // ---- decays: lane l has tokens 4 l .. 4 l + 3
+        const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
+        float raw[4], nxt[4];
+        auto load = [&](int k, float* r) {
+            const int t0 = it.t0 + k * kT, n = min(kT, it.len - k * kT);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = k < n_ch ? raw_dt(a, t0, n, h, 4 * lane + i) : 0.0f;
+        };
+        load(0, raw);
+        for (int k = 0; k < n_ch; ++k) {
+            load(k + 1, nxt);
+            const float2 tsc = a.tile_scale[(int64_t)(it.chunk0 + k) * ngroups + g];
+            const int n = min(kT, it.len - k * kT);
+            float dt[4], v[4], up = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dt[i] = 4 * lane + i < n ? softplus_dt(__fadd_rn(raw[i], bias)) : 0.0f;
+                v[i] = __fmul_rn(dt[i], a2);
+                up = __fadd_rn(up, v[i]);
+            }
+            float down = up;
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(dt[0], dt[1]), fmaxf(dt[2], dt[3]))));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, up, o), w = __shfl_down_sync(0xffffffffu, down, o);
+                if (lane >= o) up = __fadd_rn(up, u);
+                if (lane + o < 32) down = __fadd_rn(down, w);
+            }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 0.0f;
+            if (lane == 31) after = 0.0f;
+            const float2 sc = pow2_scale(m, -1);
+            float cum[4], left[4], dts[4];
+            cum[0] = __fadd_rn(before, v[0]);
+            left[3] = after;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) cum[i] = __fadd_rn(cum[i - 1], v[i]);
+#pragma unroll
+            for (int i = 2; i >= 0; --i) left[i] = __fadd_rn(left[i + 1], v[i + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dts[i] = __fmul_rn(dt[i], sc.x);
+            if (!wait(&sh.dec_empty[k & 1], ((uint32_t)(k >> 1) & 1u) ^ 1u)) break;
+            TcDecay& d = sh.dec[k & 1];
+            reinterpret_cast<float4*>(d.cum)[lane] = make_float4(cum[0], cum[1], cum[2], cum[3]);
+            reinterpret_cast<float4*>(d.dts)[lane] = make_float4(dts[0], dts[1], dts[2], dts[3]);
+            reinterpret_cast<float4*>(d.wl)[lane] =
+                make_float4(__fmul_rn(dts[0], exp2f(left[0])), __fmul_rn(dts[1], exp2f(left[1])),
+                            __fmul_rn(dts[2], exp2f(left[2])), __fmul_rn(dts[3], exp2f(left[3])));
+            reinterpret_cast<float4*>(d.done)[lane] = make_float4(exp2f(cum[0]), exp2f(cum[1]), exp2f(cum[2]), exp2f(cum[3]));
+            if (lane == 0) {
+                d.kd = sc.y;
+                d.kc = tsc.x;
+                d.kb = tsc.y;
+            }
+            arrive(&sh.dec_full[k & 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = nxt[i];
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ---- M: row t of G, columns s up to the row's block of 32
+        const int q4 = warp & 3;
+        for (int k = 0; k < n_ch; ++k) {
+            const int s2 = k & 1;
+            const uint32_t ph2 = (uint32_t)(k >> 1) & 1u;
+            const TcDecay& d = sh.dec[s2];
+            if (!wait(&sh.dec_full[s2], ph2) || !wait(&sh.g_full[s2], ph2) || !wait(&sh.m_empty, ((uint32_t)k & 1u) ^ 1u)) break;
+            ptx::tc_fence_after();
+            const float ct = d.cum[row];
+#pragma unroll 1
+            for (int cb = 0; cb < 4; ++cb) {
+                uint32_t o[16];
+                if (cb <= q4) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(t_lane + kColG + 128u * s2 + 32u * cb, r);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 cs = *reinterpret_cast<const float4*>(d.cum + 32 * cb + i);
+                        const float4 ds = *reinterpret_cast<const float4*>(d.dts + 32 * cb + i);
+                        float m0 = __fmul_rn(__fmul_rn(__uint_as_float(r[i]), ds.x), ex2(__fsub_rn(ct, cs.x)));
+                        float m1 = __fmul_rn(__fmul_rn(__uint_as_float(r[i + 1]), ds.y), ex2(__fsub_rn(ct, cs.y)));
+                        float m2 = __fmul_rn(__fmul_rn(__uint_as_float(r[i + 2]), ds.z), ex2(__fsub_rn(ct, cs.z)));
+                        float m3 = __fmul_rn(__fmul_rn(__uint_as_float(r[i + 3]), ds.w), ex2(__fsub_rn(ct, cs.w)));
+                        if (cb == q4) {
+                            if (i > lane) m0 = 0.0f;
+                            if (i + 1 > lane) m1 = 0.0f;
+                            if (i + 2 > lane) m2 = 0.0f;
+                            if (i + 3 > lane) m3 = 0.0f;
+                        }
+                        o[i / 2] = f16x2_of(m0, m1);
+                        o[i / 2 + 1] = f16x2_of(m2, m3);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = 0u;
+                }
+                ptx::tmem_st_32x32b_x16(t_lane + kColM + 16u * cb, o);
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            arrive(&sh.m_full);
+            if (lane == 0) {
+                ptx::mbar_arrive(&sh.g_empty[s2]);
+                ptx::mbar_arrive(&sh.dec_empty[s2]);
+            }
+        }
+    } else if (warp >= 8 && warp < 12) {
+        // ---- X: row t of x
+        bool ok = true;
+        for (int k = 0; k < n_ch; ++k) {
+            const int s2 = k & 1;
+            const uint32_t ph2 = (uint32_t)(k >> 1) & 1u;
+            const TcDecay& d = sh.dec[s2];
+            const uint32_t s_x = base + s2 * kStageTc + 4 * kTile;
+            ok = ok && wait(&sh.in_full[s2], ph2);
+            const bool live = row < it.len - k * kT;
+            uint4 v[8];
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = live ? ptx::lds128(piece(s_x, row, i)) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m = max(m, max((w4[q] << 16) & 0x7FFF0000u, w4[q] & 0x7FFF0000u));
+            }
+            m = __reduce_max_sync(0xffffffffu, m);
+            if (lane == 0) sh.red[0][warp & 3] = m;
+            ok = ok && wait(&sh.dec_full[s2], ph2) && wait(&sh.wx_empty, ((uint32_t)k & 1u) ^ 1u);
+            if (ptx::named_barrier_or(1, 128, !ok)) break;
+            const float2 xs = pow2_scale(max(max(sh.red[0][0], sh.red[0][1]), max(sh.red[0][2], sh.red[0][3])), 13);
+            const float w = __fmul_rn(d.wl[row], xs.x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t o[4], hi[4], lo[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float x0 = bf16_lo(w4[q]), x1 = bf16_hi(w4[q]);
+                    o[q] = f16x2_of(__fmul_rn(x0, xs.x), __fmul_rn(x1, xs.x));
+                    split_f16x2(__fmul_rn(x0, w), __fmul_rn(x1, w), hi[q], lo[q]);
+                }
+                sts128(piece(s_x, row, i), o);
+                sts128(piece(s_wx, row, i), hi);
+                sts128(piece(s_wx + kTile, row, i), lo);
+            }
+            if (row == 0) sh.kx[s2] = xs.y;
+            ptx::fence_proxy_async_smem();
+            if (ptx::named_barrier_or(1, 128, false)) break;       // red may be written again; kx is there
+            arrive(&sh.x_full);
+            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[s2]);
+        }
+    } else if (warp >= 12 && warp < 16) {
+        // ---- S: thread n holds the head's 64 channels of state n
+        float S[kP];
+        const int64_t at = ((int64_t)it.seq * a.nheads + h) * kStateElems + row;
+        const float* src = it.flags & kCut ? a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems + row
+                                           : a.init ? a.init + at : nullptr;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) S[i] = src ? src[(int64_t)i * kN] : 0.0f;
+        bool ok = true;
+        for (int k = 0; k < n_ch; ++k) {
+            const int s2 = k & 1;
+            const uint32_t ph2 = (uint32_t)(k >> 1) & 1u, ph = (uint32_t)k & 1u;
+            const TcDecay& d = sh.dec[s2];
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < kP; ++i) m = max(m, __float_as_uint(S[i]) & 0x7FFFFFFFu);
+            m = __reduce_max_sync(0xffffffffu, m);
+            if (lane == 0) sh.red[1][warp & 3] = m;
+            ok = ok && wait(&sh.s_empty, ph ^ 1u);
+            if (ptx::named_barrier_or(2, 128, !ok)) break;
+            const float2 ss = pow2_scale(max(max(sh.red[1][0], sh.red[1][1]), max(sh.red[1][2], sh.red[1][3])), 13);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    o[q] = f16x2_of(__fmul_rn(S[8 * i + 2 * q], ss.x), __fmul_rn(S[8 * i + 2 * q + 1], ss.x));
+                sts128(piece(s_st, row, i), o);
+            }
+            if (row == 0) sh.ks[s2] = ss.y;
+            ptx::fence_proxy_async_smem();
+            if (ptx::named_barrier_or(2, 128, false)) break;
+            arrive(&sh.s_full);
+            ok = wait(&sh.dec_full[s2], ph2) && wait(&sh.d_full, ph);
+            if (!ok) continue;                         // the next barrier ends the group
+            ptx::tc_fence_after();
+            const float keep = d.done[kT - 1], back = __fmul_rn(__fmul_rn(d.kb, d.kd), *(volatile float*)&sh.kx[s2]);
+#pragma unroll
+            for (int c = 0; c < kP; c += 16) {
+                uint32_t r[16];
+                ptx::tmem_ld_32x32b_x16(t_lane + kColD + c, r);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[c + i] = __fmaf_rn(__uint_as_float(r[i]), back, __fmul_rn(S[c + i], keep));
+            }
+            ptx::tc_fence_before();
+            arrive(&sh.d_empty);
+            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[s2]);
+        }
+        if (ok && p.final_state && (it.flags & kLast)) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i) p.final_state[at + (int64_t)i * kN] = S[i];
+        }
+    } else if (warp >= 16) {
+        // ---- Y: row t of y
+        const float skip = a.d_skip[h];
+        for (int k = 0; k < n_ch; ++k) {
+            const int s2 = k & 1;
+            const uint32_t ph2 = (uint32_t)(k >> 1) & 1u, ph = (uint32_t)k & 1u;
+            const TcDecay& d = sh.dec[s2];
+            const uint32_t s_x = base + s2 * kStageTc + 4 * kTile;
+            if (!wait(&sh.dec_full[s2], ph2) || !wait(&sh.y_full, ph)) break;
+            ptx::tc_fence_after();
+            const float kx = *(volatile float*)&sh.kx[s2];
+            const float alpha = __fmul_rn(d.done[row], __fmul_rn(*(volatile float*)&sh.ks[s2], d.kc));
+            const float beta = __fmul_rn(__fmul_rn(d.kc, d.kb), __fmul_rn(d.kd, kx)), sx = __fmul_rn(skip, kx);
+#pragma unroll
+            for (int c = 0; c < kP; c += 16) {
+                uint32_t yi[16], ya[16], o[8];
+                ptx::tmem_ld_32x32b_x16(t_lane + kColYi + c, yi);
+                ptx::tmem_ld_32x32b_x16(t_lane + kColYa + c, ya);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 x4 = ptx::lds128(piece(s_x, row, (c >> 3) + i));
+                    const uint32_t w4[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 xf = __half22float2(*reinterpret_cast<const __half2*>(&w4[q]));
+                        const int e = 8 * i + 2 * q;
+                        const float v0 = __fmaf_rn(__uint_as_float(ya[e]), beta, __fmul_rn(__uint_as_float(yi[e]), alpha));
+                        const float v1 = __fmaf_rn(__uint_as_float(ya[e + 1]), beta, __fmul_rn(__uint_as_float(yi[e + 1]), alpha));
+                        o[4 * i + q] = bf16x2_of(make_float2(__fmaf_rn(sx, xf.x, v0), __fmaf_rn(sx, xf.y, v1)));
+                    }
+                    sts128(piece(s_x, row, (c >> 3) + i), o + 4 * i);       // y over the x that only this thread still reads
+                }
+            }
+            ptx::tc_fence_before();
+            arrive(&sh.y_empty);                       // the row stores of the warp are also visible to it behind this
+            const int n = min(kT, it.len - k * kT), t0 = it.t0 + k * kT;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 32 * (warp & 3) + 4 * i + (lane >> 3), pc = lane & 7;
+                const uint4 v = ptx::lds128(piece(s_x, r, pc));
+                if (r < n) *reinterpret_cast<uint4*>(p.y + (int64_t)(t0 + r) * p.ldy + h * kP + 8 * pc) = v;
+            }
+            ptx::fence_proxy_async_smem();             // the tile's next contents come by TMA
+            arrive(&sh.in_empty[s2]);
+            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[s2]);
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(2 * ld)};
+    cuuint32_t box[2] = {64, kT}, estr[2] = {1, 1};
+    return enc(map, type, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t setup_tc() {
+    return cudaFuncSetAttribute(scan_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+}
+
+cudaError_t launch_tc(const Args& a, uint16_t* y, int64_t ldy, float* final_state, cudaStream_t s) {
+    const int ngroups = a.nheads / a.per_group;
+    CUtensorMap mt, mx;
+    if (!encode(&mt, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.tiles, kN, (int64_t)a.cap_chunks * ngroups * 2 * kT, kN) ||
+        !encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, (int64_t)a.nheads * kP, a.total, a.ldx))
+        return cudaErrorInvalidValue;
+    TcArgs p{a, y, ldy, final_state};
+    scan_tc_kernel<<<a.cap_items * a.nheads, kTcThreads, kTcSmem, s>>>(mt, mx, p);
+    return cudaGetLastError();
+}
+
+}  // namespace scan
+}  // namespace dfssm

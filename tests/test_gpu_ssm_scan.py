@@ -254,6 +254,17 @@ def test_backward(lens, nh, ng, init, gap):
     assert dfssm.dfssm_ssm_read_error(ptr(ws), stream()) == (dfssm.DFSSM_OK, 0)
 
 
+@pytest.mark.parametrize("lens,nh,ng,init,gap", [([513], 1, 1, False, 0), ([128, 129, 0, 1, 127, 256], 4, 2, True, 5),
+                                                 ([640], 3, 1, True, 1), ([2] * 300, 2, 2, False, 0),
+                                                 ([0, 0, 600, 0], 2, 1, True, 600)])
+def test_forward_of_long_calls(lens, nh, ng, init, gap):
+    a = inputs(len(lens) * 100 + nh + 2, lens, nh, ng, init, gap)
+    y, fin, ws = run_fwd(a)
+    torch.cuda.synchronize()
+    check_fwd(a, y, fin)
+    assert dfssm.dfssm_ssm_read_error(ptr(ws), stream()) == (dfssm.DFSSM_OK, 0)
+
+
 @pytest.mark.parametrize("lens", [[1500], [700, 513, 512, 1100, 64]])
 def test_sequences_that_are_cut_into_segments(lens):
     a = inputs(5, lens, 2, 1, True, 7)
