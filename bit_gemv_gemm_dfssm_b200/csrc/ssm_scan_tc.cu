@@ -29,6 +29,7 @@ constexpr int kT = 128;                          // tokens per chunk
 constexpr int kTcThreads = 20 * 32;
 constexpr int kTile = 16384;                     // 128 rows of 128 bytes
 constexpr int kStageTc = 5 * kTile;              // C (2 column blocks), B (2), X
+constexpr int kCB = 4 * kTile;
 struct TcDecay {
     float cum[kT];       // log 2 units
     float dts[kT];       // dt 2^kd
@@ -36,13 +37,14 @@ struct TcDecay {
     float done[kT];      // exp(cum_t)
     float kd, kc, kb;    // 2^-kd, 2^-k of C, of B
     float pad;
+    float off[3][96];    // rows 32 (r + 1) .. of M: dts_s exp(cum_{32 (r + 1)} - cum_s) for the columns s in front
 };
 struct TcShared {
     TcDecay dec[2];
     float kx[2];         // 2^-k of the x tile
     float ks[2];         // of the state tile
     uint32_t red[2][4];  // maxima of the X and of the S group's warps
-    uint64_t in_full[2], in_empty[2], dec_full[2], dec_empty[2], g_full[2], g_empty[2];
+    uint64_t cb_full[2], cb_empty[2], xt_full[2], xt_empty[2], dec_full[2], dec_empty[2], g_full[2], g_empty[2];
     uint64_t m_full, m_empty, x_full, wx_empty, d_full, d_empty, s_full, s_empty, y_full, y_empty, drain;
     uint32_t tmem, abort;
 };
@@ -82,8 +84,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(&sh.in_full[s], 1);
-            ptx::mbar_init(&sh.in_empty[s], 5);       // the MMAs, four Y warps
+            ptx::mbar_init(&sh.cb_full[s], 1);
+            ptx::mbar_init(&sh.cb_empty[s], 1);       // the MMAs
+            ptx::mbar_init(&sh.xt_full[s], 1);
+            ptx::mbar_init(&sh.xt_empty[s], 4);       // the Y warps (behind the MMAs)
             ptx::mbar_init(&sh.dec_full[s], 1);
             ptx::mbar_init(&sh.dec_empty[s], 16);
             ptx::mbar_init(&sh.g_full[s], 1);
@@ -114,7 +118,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
 
     // a bounded wait; a role that gives up takes all others along
     auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (ptx::mbar_wait(bar, parity) && !*abort_flag) return true;
+        if (ptx::mbar_spin(bar, parity) && !*abort_flag) return true;
         atomicOr(a.err, DFSSM_DEVERR_TIMEOUT);
         *abort_flag = 1;
         return false;
@@ -140,70 +144,109 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             int k = 0;
             for (; k < n_ch; ++k) {
                 const int s = k & 1;
-                if (!wait1(&sh.in_empty[s], ((uint32_t)(k >> 1) & 1u) ^ 1u)) break;
+                const uint32_t ph = ((uint32_t)(k >> 1) & 1u) ^ 1u;
                 uint8_t* st = smem + s * kStageTc;
                 const int trow = ((it.chunk0 + k) * ngroups + g) * 2 * kT;
-                ptx::mbar_arrive_expect_tx(&sh.in_full[s], kStageTc);
-                ptx::tma_load_2d(st, &map_t, 0, trow, &sh.in_full[s]);
-                ptx::tma_load_2d(st + kTile, &map_t, 64, trow, &sh.in_full[s]);
-                ptx::tma_load_2d(st + 2 * kTile, &map_t, 0, trow + kT, &sh.in_full[s]);
-                ptx::tma_load_2d(st + 3 * kTile, &map_t, 64, trow + kT, &sh.in_full[s]);
-                ptx::tma_load_2d(st + 4 * kTile, &map_x, h * kP, it.t0 + k * kT, &sh.in_full[s]);
+                if (!wait1(&sh.cb_empty[s], ph)) break;
+                ptx::mbar_arrive_expect_tx(&sh.cb_full[s], kCB);
+                ptx::tma_load_2d(st, &map_t, 0, trow, &sh.cb_full[s]);
+                ptx::tma_load_2d(st + kTile, &map_t, 64, trow, &sh.cb_full[s]);
+                ptx::tma_load_2d(st + 2 * kTile, &map_t, 0, trow + kT, &sh.cb_full[s]);
+                ptx::tma_load_2d(st + 3 * kTile, &map_t, 64, trow + kT, &sh.cb_full[s]);
+                const bool ok = wait1(&sh.xt_empty[s], ph);
+                ptx::mbar_arrive_expect_tx(&sh.xt_full[s], kTile);
+                ptx::tma_load_2d(st + kCB, &map_x, h * kP, it.t0 + k * kT, &sh.xt_full[s]);
+                if (!ok) {
+                    ++k;
+                    break;
+                }
             }
             if (*abort_flag)                           // the copies still in flight land before the CTA ends
-                for (int i = max(0, k - 2); i < k; ++i) ptx::mbar_wait(&sh.in_full[i & 1], (uint32_t)(i >> 1) & 1u);
+                for (int i = max(0, k - 2); i < k; ++i) {
+                    ptx::mbar_wait(&sh.cb_full[i & 1], (uint32_t)(i >> 1) & 1u);
+                    ptx::mbar_wait(&sh.xt_full[i & 1], (uint32_t)(i >> 1) & 1u);
+                }
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            auto product_g = [&](int k) -> bool {
-                const int s = k & 1;
-                const uint32_t ph = (uint32_t)(k >> 1) & 1u, st = base + s * kStageTc;
-                if (!wait1(&sh.in_full[s], ph) || !wait1(&sh.g_empty[s], ph ^ 1u)) return false;
-                ptx::tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ptx::mma_f16(tmem + kColG + 128u * s, ptx::kmajor_sw128_desc(st + (j >> 2) * kTile) + 2 * (j & 3),
-                                 ptx::kmajor_sw128_desc(st + (2 + (j >> 2)) * kTile) + 2 * (j & 3), kIdescG, j > 0);
-                ptx::mma_commit(&sh.g_full[s]);
-                return true;
-            };
-            bool ok = n_ch == 0 || product_g(0);
-            for (int k = 0; k < n_ch && ok; ++k) {
-                const int s = k & 1;
-                const uint32_t ph = (uint32_t)k & 1u, st = base + s * kStageTc;
-                // D = B^T (w X): lo, then hi
-                ok = wait1(&sh.x_full, ph) && wait1(&sh.d_empty, ph ^ 1u);
-                if (!ok) break;
-                ptx::tc_fence_after();
-#pragma unroll
-                for (int part = 1; part >= 0; --part)
+            // Each product is issued as soon as what it reads is there and what it writes is free, whichever comes
+            // first; in a fixed order G of the next chunk held up the readouts until that chunk's tiles had come.
+            int kg = 0, kd = 0, ki = 0, ka = 0;        // chunks whose G, D, Yi, Ya are issued
+            int freed = 0;                             // chunks whose C and B tiles are released
+            uint32_t idle = 0;
+            uint64_t since = 0;
+            bool ok = true;
+            auto ready = [&](uint64_t* bar, int phases) { return ptx::mbar_test(bar, (uint32_t)phases & 1u); };
+            while (ok && (kg < n_ch || kd < n_ch || ki < n_ch || ka < n_ch)) {
+                bool moved = false;
+                if (kg < n_ch && ready(&sh.cb_full[kg & 1], kg >> 1) && ready(&sh.g_empty[kg & 1], (kg >> 1) ^ 1)) {
+                    const uint32_t st = base + (kg & 1) * kStageTc;
+                    ptx::tc_fence_after();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        ptx::mma_f16(tmem + kColD, ptx::mnmajor_sw128_desc(st + 2 * kTile + j * 2048, kTile),
-                                     ptx::mnmajor_sw128_desc(s_wx + part * kTile + j * 2048, 1024), kIdescD, part == 0 || j > 0);
-                ptx::mma_commit(&sh.d_full);
-                ptx::mma_commit(&sh.wx_empty);
-                if (k + 1 < n_ch) ok = product_g(k + 1);
-                // Yi = C S^T
-                ok = ok && wait1(&sh.s_full, ph) && wait1(&sh.y_empty, ph ^ 1u);
-                if (!ok) break;
-                ptx::tc_fence_after();
+                        ptx::mma_f16(tmem + kColG + 128u * (kg & 1), ptx::kmajor_sw128_desc(st + (j >> 2) * kTile) + 2 * (j & 3),
+                                     ptx::kmajor_sw128_desc(st + (2 + (j >> 2)) * kTile) + 2 * (j & 3), kIdescG, j > 0);
+                    ptx::mma_commit(&sh.g_full[kg & 1]);
+                    ++kg;
+                    moved = true;
+                }
+                if (kd < kg && ready(&sh.x_full, kd) && ready(&sh.d_empty, kd ^ 1)) {
+                    // D = B^T (w X): lo, then hi
+                    const uint32_t st = base + (kd & 1) * kStageTc;
+                    ptx::tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ptx::mma_f16(tmem + kColYi, ptx::kmajor_sw128_desc(st + (j >> 2) * kTile) + 2 * (j & 3),
-                                 ptx::mnmajor_sw128_desc(s_st + j * 2048, 1024), kIdescY, j > 0);
-                ptx::mma_commit(&sh.s_empty);
-                // Ya = M X
-                ok = wait1(&sh.m_full, ph);
-                if (!ok) break;
-                ptx::tc_fence_after();
+                    for (int part = 1; part >= 0; --part)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ptx::mma_f16_ts(tmem + kColYa, tmem + kColM + 8 * j, ptx::mnmajor_sw128_desc(st + 4 * kTile + j * 2048, 1024),
-                                    kIdescY, j > 0);
-                ptx::mma_commit(&sh.m_empty);
-                ptx::mma_commit(&sh.y_full);
-                ptx::mma_commit(&sh.in_empty[s]);
+                        for (int j = 0; j < 8; ++j)
+                            ptx::mma_f16(tmem + kColD, ptx::mnmajor_sw128_desc(st + 2 * kTile + j * 2048, kTile),
+                                         ptx::mnmajor_sw128_desc(s_wx + part * kTile + j * 2048, 1024), kIdescD,
+                                         part == 0 || j > 0);
+                    ptx::mma_commit(&sh.d_full);
+                    ptx::mma_commit(&sh.wx_empty);
+                    ++kd;
+                    moved = true;
+                }
+                if (ki < kg && ki <= ka && ready(&sh.s_full, ki) && ready(&sh.y_empty, ki ^ 1)) {
+                    // Yi = C S^T
+                    const uint32_t st = base + (ki & 1) * kStageTc;
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        ptx::mma_f16(tmem + kColYi, ptx::kmajor_sw128_desc(st + (j >> 2) * kTile) + 2 * (j & 3),
+                                     ptx::mnmajor_sw128_desc(s_st + j * 2048, 1024), kIdescY, j > 0);
+                    ptx::mma_commit(&sh.s_empty);
+                    ++ki;
+                    moved = true;
+                }
+                if (ka < ki && ka < kd && ready(&sh.m_full, ka)) {
+                    // Ya = M X (x is there: D of the chunk is issued)
+                    const uint32_t st = base + (ka & 1) * kStageTc;
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        ptx::mma_f16_ts(tmem + kColYa, tmem + kColM + 8 * j, ptx::mnmajor_sw128_desc(st + kCB + j * 2048, 1024),
+                                        kIdescY, j > 0);
+                    ptx::mma_commit(&sh.m_empty);
+                    ptx::mma_commit(&sh.y_full);
+                    ++ka;
+                    moved = true;
+                }
+                if (freed < min(kd, ki)) {             // G came before both
+                    ptx::mma_commit(&sh.cb_empty[freed & 1]);
+                    ++freed;
+                }
+                if (moved) {
+                    idle = 0;
+                    since = 0;
+                } else if ((++idle & 255u) == 0u) {
+                    const uint64_t t = ptx::globaltimer();
+                    if (since == 0) since = t;
+                    if (*abort_flag || t - since > 1000000000ull) {
+                        atomicOr(a.err, DFSSM_DEVERR_TIMEOUT);
+                        *abort_flag = 1;
+                        ok = false;
+                    }
+                }
             }
             if (!ok) {                                 // the MMAs issued so far end before tensor memory is given back
                 ptx::mma_commit(&sh.drain);
@@ -260,6 +303,14 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 make_float4(__fmul_rn(dts[0], exp2f(left[0])), __fmul_rn(dts[1], exp2f(left[1])),
                             __fmul_rn(dts[2], exp2f(left[2])), __fmul_rn(dts[3], exp2f(left[3])));
             reinterpret_cast<float4*>(d.done)[lane] = make_float4(exp2f(cum[0]), exp2f(cum[1]), exp2f(cum[2]), exp2f(cum[3]));
+#pragma unroll
+            for (int r = 0; r < 3; ++r) {
+                const float c0 = __shfl_sync(0xffffffffu, cum[0], 8 * (r + 1));
+                if (lane < 8 * (r + 1))
+                    reinterpret_cast<float4*>(d.off[r])[lane] =
+                        make_float4(__fmul_rn(dts[0], ex2(__fsub_rn(c0, cum[0]))), __fmul_rn(dts[1], ex2(__fsub_rn(c0, cum[1]))),
+                                    __fmul_rn(dts[2], ex2(__fsub_rn(c0, cum[2]))), __fmul_rn(dts[3], ex2(__fsub_rn(c0, cum[3]))));
+            }
             if (lane == 0) {
                 d.kd = sc.y;
                 d.kc = tsc.x;
@@ -279,35 +330,50 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             if (!wait(&sh.dec_full[s2], ph2) || !wait(&sh.g_full[s2], ph2) || !wait(&sh.m_empty, ((uint32_t)k & 1u) ^ 1u)) break;
             ptx::tc_fence_after();
             const float ct = d.cum[row];
+            // In front of the row's block the decay is a product: of the row (from the block's first token) and of the
+            // column (up to it, with dt, from the decays' warp). Both are <= 1.
+            const float at = ex2(__fsub_rn(ct, d.cum[32 * q4]));
+            const float2 at2 = make_float2(at, at);
 #pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
-                uint32_t o[16];
-                if (cb <= q4) {
-                    uint32_t r[32];
-                    ptx::tmem_ld_32x32b_x32(t_lane + kColG + 128u * s2 + 32u * cb, r);
-                    ptx::tmem_ld_wait();
+            for (int cb = 0; cb < 2 * q4; ++cb) {
+                uint32_t r[16], o[8];
+                ptx::tmem_ld_32x32b_x16(t_lane + kColG + 128u * s2 + 16u * cb, r);
+                ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 cs = *reinterpret_cast<const float4*>(d.cum + 32 * cb + i);
-                        const float4 ds = *reinterpret_cast<const float4*>(d.dts + 32 * cb + i);
-                        float m0 = __fmul_rn(__fmul_rn(__uint_as_float(r[i]), ds.x), ex2(__fsub_rn(ct, cs.x)));
-                        float m1 = __fmul_rn(__fmul_rn(__uint_as_float(r[i + 1]), ds.y), ex2(__fsub_rn(ct, cs.y)));
-                        float m2 = __fmul_rn(__fmul_rn(__uint_as_float(r[i + 2]), ds.z), ex2(__fsub_rn(ct, cs.z)));
-                        float m3 = __fmul_rn(__fmul_rn(__uint_as_float(r[i + 3]), ds.w), ex2(__fsub_rn(ct, cs.w)));
-                        if (cb == q4) {
-                            if (i > lane) m0 = 0.0f;
-                            if (i + 1 > lane) m1 = 0.0f;
-                            if (i + 2 > lane) m2 = 0.0f;
-                            if (i + 3 > lane) m3 = 0.0f;
-                        }
-                        o[i / 2] = f16x2_of(m0, m1);
-                        o[i / 2 + 1] = f16x2_of(m2, m3);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0u;
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 b = *reinterpret_cast<const float4*>(d.off[q4 - 1] + 16 * cb + i);
+                    const float2 m0 = fmul2(fmul2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), at2), make_float2(b.x, b.y));
+                    const float2 m1 = fmul2(fmul2(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), at2), make_float2(b.z, b.w));
+                    o[i / 2] = f16x2_of(m0.x, m0.y);
+                    o[i / 2 + 1] = f16x2_of(m1.x, m1.y);
                 }
-                ptx::tmem_st_32x32b_x16(t_lane + kColM + 16u * cb, o);
+                ptx::tmem_st_32x32b_x8(t_lane + kColM + 8u * cb, o);
+            }
+#pragma unroll 1
+            for (int cb = 2 * q4; cb < 2 * q4 + 2; ++cb) {         // the row's own block
+                uint32_t r[16], o[8];
+                ptx::tmem_ld_32x32b_x16(t_lane + kColG + 128u * s2 + 16u * cb, r);
+                ptx::tmem_ld_wait();
+                const int dg = lane - 16 * (cb & 1);               // columns of the piece up to the diagonal
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 cs = *reinterpret_cast<const float4*>(d.cum + 16 * cb + i);
+                    const float4 ds = *reinterpret_cast<const float4*>(d.dts + 16 * cb + i);
+                    const float m0 = i <= dg ? __fmul_rn(__fmul_rn(__uint_as_float(r[i]), ds.x), ex2(__fsub_rn(ct, cs.x))) : 0.0f;
+                    const float m1 = i + 1 <= dg ? __fmul_rn(__fmul_rn(__uint_as_float(r[i + 1]), ds.y), ex2(__fsub_rn(ct, cs.y))) : 0.0f;
+                    const float m2 = i + 2 <= dg ? __fmul_rn(__fmul_rn(__uint_as_float(r[i + 2]), ds.z), ex2(__fsub_rn(ct, cs.z))) : 0.0f;
+                    const float m3 = i + 3 <= dg ? __fmul_rn(__fmul_rn(__uint_as_float(r[i + 3]), ds.w), ex2(__fsub_rn(ct, cs.w))) : 0.0f;
+                    o[i / 2] = f16x2_of(m0, m1);
+                    o[i / 2 + 1] = f16x2_of(m2, m3);
+                }
+                ptx::tmem_st_32x32b_x8(t_lane + kColM + 8u * cb, o);
+            }
+            if (k == 0) {                                          // what lies behind it is never written again
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = 0u;
+#pragma unroll 1
+                for (int cb = 2 * q4 + 2; cb < 8; ++cb) ptx::tmem_st_32x32b_x8(t_lane + kColM + 8u * cb, o);
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
@@ -325,32 +391,39 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             const uint32_t ph2 = (uint32_t)(k >> 1) & 1u;
             const TcDecay& d = sh.dec[s2];
             const uint32_t s_x = base + s2 * kStageTc + 4 * kTile;
-            ok = ok && wait(&sh.in_full[s2], ph2);
+            ok = ok && wait(&sh.xt_full[s2], ph2);
             const bool live = row < it.len - k * kT;
-            uint4 v[8];
             uint32_t m = 0u;
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {
-                v[i] = live ? ptx::lds128(piece(s_x, row, i)) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const uint4 v = ptx::lds128(piece(s_x, row, i));
+                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) m = max(m, max((w4[q] << 16) & 0x7FFF0000u, w4[q] & 0x7FFF0000u));
             }
+            if (!live) m = 0u;
             m = __reduce_max_sync(0xffffffffu, m);
             if (lane == 0) sh.red[0][warp & 3] = m;
             ok = ok && wait(&sh.dec_full[s2], ph2) && wait(&sh.wx_empty, ((uint32_t)k & 1u) ^ 1u);
             if (ptx::named_barrier_or(1, 128, !ok)) break;
             const float2 xs = pow2_scale(max(max(sh.red[0][0], sh.red[0][1]), max(sh.red[0][2], sh.red[0][3])), 13);
             const float w = __fmul_rn(d.wl[row], xs.x);
-#pragma unroll
+            const float2 xs2 = make_float2(xs.x, xs.x), w2 = make_float2(w, w);
+#pragma unroll 1
             for (int i = 0; i < 8; ++i) {
-                const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint4 v = ptx::lds128(piece(s_x, row, i));
+                if (!live) v = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
                 uint32_t o[4], hi[4], lo[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float x0 = bf16_lo(w4[q]), x1 = bf16_hi(w4[q]);
-                    o[q] = f16x2_of(__fmul_rn(x0, xs.x), __fmul_rn(x1, xs.x));
-                    split_f16x2(__fmul_rn(x0, w), __fmul_rn(x1, w), hi[q], lo[q]);
+                    const float2 x2 = make_float2(bf16_lo(w4[q]), bf16_hi(w4[q]));
+                    const float2 a2 = fmul2(x2, xs2), b2 = fmul2(x2, w2);
+                    o[q] = f16x2_of(a2.x, a2.y);
+                    const __half2 hh = __floats2half2_rn(b2.x, b2.y);
+                    hi[q] = *reinterpret_cast<const uint32_t*>(&hh);
+                    const float2 f = __half22float2(hh);
+                    lo[q] = f16x2_of(__fsub_rn(b2.x, f.x), __fsub_rn(b2.y, f.y));
                 }
                 sts128(piece(s_x, row, i), o);
                 sts128(piece(s_wx, row, i), hi);
@@ -364,21 +437,25 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
         }
     } else if (warp >= 12 && warp < 16) {
         // ---- S: thread n holds the head's 64 channels of state n
-        float S[kP];
+        float2 S[kP / 2];
         const int64_t at = ((int64_t)it.seq * a.nheads + h) * kStateElems + row;
         const float* src = it.flags & kCut ? a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems + row
                                            : a.init ? a.init + at : nullptr;
 #pragma unroll
-        for (int i = 0; i < kP; ++i) S[i] = src ? src[(int64_t)i * kN] : 0.0f;
+        for (int i = 0; i < kP / 2; ++i)
+            S[i] = src ? make_float2(src[(int64_t)(2 * i) * kN], src[(int64_t)(2 * i + 1) * kN]) : make_float2(0.0f, 0.0f);
         bool ok = true;
         for (int k = 0; k < n_ch; ++k) {
             const int s2 = k & 1;
             const uint32_t ph2 = (uint32_t)(k >> 1) & 1u, ph = (uint32_t)k & 1u;
             const TcDecay& d = sh.dec[s2];
-            uint32_t m = 0u;
+            float f0 = 0.0f, f1 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kP; ++i) m = max(m, __float_as_uint(S[i]) & 0x7FFFFFFFu);
-            m = __reduce_max_sync(0xffffffffu, m);
+            for (int i = 0; i < kP / 2; ++i) {
+                f0 = fmaxf(f0, fabsf(S[i].x));
+                f1 = fmaxf(f1, fabsf(S[i].y));
+            }
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(f0, f1)));
             if (lane == 0) sh.red[1][warp & 3] = m;
             ok = ok && wait(&sh.s_empty, ph ^ 1u);
             if (ptx::named_barrier_or(2, 128, !ok)) break;
@@ -387,8 +464,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             for (int i = 0; i < 8; ++i) {
                 uint32_t o[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    o[q] = f16x2_of(__fmul_rn(S[8 * i + 2 * q], ss.x), __fmul_rn(S[8 * i + 2 * q + 1], ss.x));
+                for (int q = 0; q < 4; ++q) {
+                    const float2 v = fmul2(S[4 * i + q], make_float2(ss.x, ss.x));
+                    o[q] = f16x2_of(v.x, v.y);
+                }
                 sts128(piece(s_st, row, i), o);
             }
             if (row == 0) sh.ks[s2] = ss.y;
@@ -405,7 +484,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 ptx::tmem_ld_32x32b_x16(t_lane + kColD + c, r);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[c + i] = __fmaf_rn(__uint_as_float(r[i]), back, __fmul_rn(S[c + i], keep));
+                for (int i = 0; i < 8; ++i)
+                    S[c / 2 + i] = ffma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(back, back),
+                                         fmul2(S[c / 2 + i], make_float2(keep, keep)));
             }
             ptx::tc_fence_before();
             arrive(&sh.d_empty);
@@ -413,7 +494,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
         }
         if (ok && p.final_state && (it.flags & kLast)) {
 #pragma unroll
-            for (int i = 0; i < kP; ++i) p.final_state[at + (int64_t)i * kN] = S[i];
+            for (int i = 0; i < kP / 2; ++i) {
+                p.final_state[at + (int64_t)(2 * i) * kN] = S[i].x;
+                p.final_state[at + (int64_t)(2 * i + 1) * kN] = S[i].y;
+            }
         }
     } else if (warp >= 16) {
         // ---- Y: row t of y
@@ -428,7 +512,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             const float kx = *(volatile float*)&sh.kx[s2];
             const float alpha = __fmul_rn(d.done[row], __fmul_rn(*(volatile float*)&sh.ks[s2], d.kc));
             const float beta = __fmul_rn(__fmul_rn(d.kc, d.kb), __fmul_rn(d.kd, kx)), sx = __fmul_rn(skip, kx);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kP; c += 16) {
                 uint32_t yi[16], ya[16], o[8];
                 ptx::tmem_ld_32x32b_x16(t_lane + kColYi + c, yi);
@@ -442,9 +526,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                     for (int q = 0; q < 4; ++q) {
                         const float2 xf = __half22float2(*reinterpret_cast<const __half2*>(&w4[q]));
                         const int e = 8 * i + 2 * q;
-                        const float v0 = __fmaf_rn(__uint_as_float(ya[e]), beta, __fmul_rn(__uint_as_float(yi[e]), alpha));
-                        const float v1 = __fmaf_rn(__uint_as_float(ya[e + 1]), beta, __fmul_rn(__uint_as_float(yi[e + 1]), alpha));
-                        o[4 * i + q] = bf16x2_of(make_float2(__fmaf_rn(sx, xf.x, v0), __fmaf_rn(sx, xf.y, v1)));
+                        const float2 in = fmul2(make_float2(__uint_as_float(yi[e]), __uint_as_float(yi[e + 1])), make_float2(alpha, alpha));
+                        const float2 v = ffma2(make_float2(__uint_as_float(ya[e]), __uint_as_float(ya[e + 1])), make_float2(beta, beta), in);
+                        o[4 * i + q] = bf16x2_of(ffma2(xf, make_float2(sx, sx), v));
                     }
                     sts128(piece(s_x, row, (c >> 3) + i), o + 4 * i);       // y over the x that only this thread still reads
                 }
@@ -459,7 +543,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 if (r < n) *reinterpret_cast<uint4*>(p.y + (int64_t)(t0 + r) * p.ldy + h * kP + 8 * pc) = v;
             }
             ptx::fence_proxy_async_smem();             // the tile's next contents come by TMA
-            arrive(&sh.in_empty[s2]);
+            arrive(&sh.xt_empty[s2]);
             if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[s2]);
         }
     }
