@@ -137,9 +137,6 @@ struct FwdOut {
 
 constexpr int kTileTop = 3;
 
-__device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t m, uint32_t v) {
-    return max(m, max((v << 16) & 0x7FFF0000u, v & 0x7FFF0000u));
-}
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
     return f16x2_of(__fmul_rn(bf16_lo(v), scale), __fmul_rn(bf16_hi(v), scale));
 }

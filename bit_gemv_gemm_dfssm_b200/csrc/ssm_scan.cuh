@@ -141,6 +141,10 @@ __device__ __forceinline__ float2 pow2_scale(uint32_t m_bits, int top) {
     return make_float2(__int_as_float((127 + k) << 23), __int_as_float((127 - k) << 23));
 }
 
+// the larger of m and the magnitudes of two bf16 values, as fp32 bits
+__device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t m, uint32_t v) {
+    return max(m, max((v << 16) & 0x7FFF0000u, v & 0x7FFF0000u));
+}
 __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);

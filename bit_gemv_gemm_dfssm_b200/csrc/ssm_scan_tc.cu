@@ -18,6 +18,8 @@
 //   Y group: Yi, Ya, x -> y in bf16 over the x tile, out as whole rows.
 // They meet in mbarriers only, so that the products of one chunk run beside the conversions of the next. Every
 // wait is bounded.
+#include <cstddef>
+
 #include "ssm_scan.cuh"
 
 namespace dfssm {
@@ -26,11 +28,12 @@ namespace scan {
 namespace {
 
 constexpr int kT = 128;                          // tokens per chunk
+constexpr int kDec = 4;                          // chunks whose decays are kept
 constexpr int kTcThreads = 20 * 32;
 constexpr int kTile = 16384;                     // 128 rows of 128 bytes
 constexpr int kStageTc = 5 * kTile;              // C (2 column blocks), B (2), X
 constexpr int kCB = 4 * kTile;
-struct TcDecay {
+struct alignas(16) TcDecay {
     float cum[kT];       // log 2 units
     float dts[kT];       // dt 2^kd
     float wl[kT];        // dts exp(cum_128 - cum_t)
@@ -39,17 +42,20 @@ struct TcDecay {
     float pad;
     float off[3][96];    // rows 32 (r + 1) .. of M: dts_s exp(cum_{32 (r + 1)} - cum_s) for the columns s in front
 };
-struct TcShared {
-    TcDecay dec[2];
-    float kx[2];         // 2^-k of the x tile
-    float ks[2];         // of the state tile
-    uint32_t red[2][4];  // maxima of the X and of the S group's warps
-    uint64_t cb_full[2], cb_empty[2], xt_full[2], xt_empty[2], dec_full[2], dec_empty[2], g_full[2], g_empty[2];
+struct alignas(16) TcShared {
+    TcDecay dec[kDec];
+    float kx[kDec];      // 2^-k of the x tile; goes back with the decays
+    float ks[2];         // of the state tile; goes back with Yi
+    alignas(16) uint32_t red[2][2][4];  // [X, S group][chunk parity] maxima of the warps
+    uint64_t cb_full[2], cb_empty[2], xt_full[2], xt_empty[2], g_full[2], g_empty[2];
+    uint64_t dec_full[kDec], dec_empty[kDec];
     uint64_t m_full, m_empty, x_full, wx_empty, d_full, d_empty, s_full, s_empty, y_full, y_empty, drain;
     uint32_t tmem, abort;
 };
 constexpr int kTcSmem = 2 * kStageTc + 3 * kTile + (int)sizeof(TcShared) + 1024;
 static_assert(kTcSmem <= 232448, "shared memory");
+static_assert(offsetof(TcShared, red) % 16 == 0 && offsetof(TcDecay, off) % 16 == 0 && sizeof(TcDecay) % 16 == 0 &&
+              offsetof(TcDecay, dts) % 16 == 0 && offsetof(TcShared, cb_full) % 8 == 0, "vector accesses");
 
 // tensor memory columns
 constexpr uint32_t kColG = 0, kColM = 256, kColYi = 320, kColYa = 384, kColD = 448;
@@ -88,10 +94,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             ptx::mbar_init(&sh.cb_empty[s], 1);       // the MMAs
             ptx::mbar_init(&sh.xt_full[s], 1);
             ptx::mbar_init(&sh.xt_empty[s], 4);       // the Y warps (behind the MMAs)
-            ptx::mbar_init(&sh.dec_full[s], 1);
-            ptx::mbar_init(&sh.dec_empty[s], 16);
             ptx::mbar_init(&sh.g_full[s], 1);
             ptx::mbar_init(&sh.g_empty[s], 4);
+        }
+        for (int s = 0; s < kDec; ++s) {
+            ptx::mbar_init(&sh.dec_full[s], 1);
+            ptx::mbar_init(&sh.dec_empty[s], 16);     // every warp of the groups
         }
         ptx::mbar_init(&sh.m_full, 4);
         ptx::mbar_init(&sh.m_empty, 1);
@@ -118,7 +126,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
 
     // a bounded wait; a role that gives up takes all others along
     auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (ptx::mbar_spin(bar, parity) && !*abort_flag) return true;
+        if (ptx::mbar_wait(bar, parity) && !*abort_flag) return true;
         atomicOr(a.err, DFSSM_DEVERR_TIMEOUT);
         *abort_flag = 1;
         return false;
@@ -253,8 +261,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 ptx::mbar_wait(&sh.drain, 0u);
             }
         }
-    } else if (warp == 2) {
-        // ---- decays: lane l has tokens 4 l .. 4 l + 3
+    } else if (warp < 4) {
+        // ---- decays, two warps in turn: lane l has tokens 4 l .. 4 l + 3
         const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
         float raw[4], nxt[4];
         auto load = [&](int k, float* r) {
@@ -262,9 +270,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = k < n_ch ? raw_dt(a, t0, n, h, 4 * lane + i) : 0.0f;
         };
-        load(0, raw);
-        for (int k = 0; k < n_ch; ++k) {
-            load(k + 1, nxt);
+        load(warp - 2, raw);
+        for (int k = warp - 2; k < n_ch; k += 2) {
+            load(k + 2, nxt);
             const float2 tsc = a.tile_scale[(int64_t)(it.chunk0 + k) * ngroups + g];
             const int n = min(kT, it.len - k * kT);
             float dt[4], v[4], up = 0.0f;
@@ -295,8 +303,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             for (int i = 2; i >= 0; --i) left[i] = __fadd_rn(left[i + 1], v[i + 1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dts[i] = __fmul_rn(dt[i], sc.x);
-            if (!wait(&sh.dec_empty[k & 1], ((uint32_t)(k >> 1) & 1u) ^ 1u)) break;
-            TcDecay& d = sh.dec[k & 1];
+            if (!wait(&sh.dec_empty[k % kDec], ((uint32_t)(k / kDec) & 1u) ^ 1u)) break;
+            TcDecay& d = sh.dec[k % kDec];
             reinterpret_cast<float4*>(d.cum)[lane] = make_float4(cum[0], cum[1], cum[2], cum[3]);
             reinterpret_cast<float4*>(d.dts)[lane] = make_float4(dts[0], dts[1], dts[2], dts[3]);
             reinterpret_cast<float4*>(d.wl)[lane] =
@@ -316,7 +324,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 d.kc = tsc.x;
                 d.kb = tsc.y;
             }
-            arrive(&sh.dec_full[k & 1]);
+            arrive(&sh.dec_full[k % kDec]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) raw[i] = nxt[i];
         }
@@ -326,8 +334,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
         for (int k = 0; k < n_ch; ++k) {
             const int s2 = k & 1;
             const uint32_t ph2 = (uint32_t)(k >> 1) & 1u;
-            const TcDecay& d = sh.dec[s2];
-            if (!wait(&sh.dec_full[s2], ph2) || !wait(&sh.g_full[s2], ph2) || !wait(&sh.m_empty, ((uint32_t)k & 1u) ^ 1u)) break;
+            const TcDecay& d = sh.dec[k % kDec];
+            if (!wait(&sh.dec_full[k % kDec], (uint32_t)(k / kDec) & 1u) || !wait(&sh.g_full[s2], ph2) || !wait(&sh.m_empty, ((uint32_t)k & 1u) ^ 1u)) break;
             ptx::tc_fence_after();
             const float ct = d.cum[row];
             // In front of the row's block the decay is a product: of the row (from the block's first token) and of the
@@ -338,7 +346,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             for (int cb = 0; cb < 2 * q4; ++cb) {
                 uint32_t r[16], o[8];
                 ptx::tmem_ld_32x32b_x16(t_lane + kColG + 128u * s2 + 16u * cb, r);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r);
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
                     const float4 b = *reinterpret_cast<const float4*>(d.off[q4 - 1] + 16 * cb + i);
@@ -353,7 +361,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             for (int cb = 2 * q4; cb < 2 * q4 + 2; ++cb) {         // the row's own block
                 uint32_t r[16], o[8];
                 ptx::tmem_ld_32x32b_x16(t_lane + kColG + 128u * s2 + 16u * cb, r);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r);
                 const int dg = lane - 16 * (cb & 1);               // columns of the piece up to the diagonal
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
@@ -380,7 +388,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             arrive(&sh.m_full);
             if (lane == 0) {
                 ptx::mbar_arrive(&sh.g_empty[s2]);
-                ptx::mbar_arrive(&sh.dec_empty[s2]);
+                ptx::mbar_arrive(&sh.dec_empty[k % kDec]);
             }
         }
     } else if (warp >= 8 && warp < 12) {
@@ -389,7 +397,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
         for (int k = 0; k < n_ch; ++k) {
             const int s2 = k & 1;
             const uint32_t ph2 = (uint32_t)(k >> 1) & 1u;
-            const TcDecay& d = sh.dec[s2];
+            const TcDecay& d = sh.dec[k % kDec];
             const uint32_t s_x = base + s2 * kStageTc + 4 * kTile;
             ok = ok && wait(&sh.xt_full[s2], ph2);
             const bool live = row < it.len - k * kT;
@@ -403,10 +411,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             }
             if (!live) m = 0u;
             m = __reduce_max_sync(0xffffffffu, m);
-            if (lane == 0) sh.red[0][warp & 3] = m;
-            ok = ok && wait(&sh.dec_full[s2], ph2) && wait(&sh.wx_empty, ((uint32_t)k & 1u) ^ 1u);
+            uint32_t* red = sh.red[0][s2];
+            if (lane == 0) red[warp & 3] = m;
+            ok = ok && wait(&sh.dec_full[k % kDec], (uint32_t)(k / kDec) & 1u) && wait(&sh.wx_empty, ((uint32_t)k & 1u) ^ 1u);
             if (ptx::named_barrier_or(1, 128, !ok)) break;
-            const float2 xs = pow2_scale(max(max(sh.red[0][0], sh.red[0][1]), max(sh.red[0][2], sh.red[0][3])), 13);
+            const float2 xs = pow2_scale(max(max(red[0], red[1]), max(red[2], red[3])), 13);
             const float w = __fmul_rn(d.wl[row], xs.x);
             const float2 xs2 = make_float2(xs.x, xs.x), w2 = make_float2(w, w);
 #pragma unroll 1
@@ -429,11 +438,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 sts128(piece(s_wx, row, i), hi);
                 sts128(piece(s_wx + kTile, row, i), lo);
             }
-            if (row == 0) sh.kx[s2] = xs.y;
+            if (row == 0) sh.kx[k % kDec] = xs.y;
             ptx::fence_proxy_async_smem();
-            if (ptx::named_barrier_or(1, 128, false)) break;       // red may be written again; kx is there
             arrive(&sh.x_full);
-            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[s2]);
+            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[k % kDec]);
         }
     } else if (warp >= 12 && warp < 16) {
         // ---- S: thread n holds the head's 64 channels of state n
@@ -447,8 +455,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
         bool ok = true;
         for (int k = 0; k < n_ch; ++k) {
             const int s2 = k & 1;
-            const uint32_t ph2 = (uint32_t)(k >> 1) & 1u, ph = (uint32_t)k & 1u;
-            const TcDecay& d = sh.dec[s2];
+            const uint32_t ph = (uint32_t)k & 1u;
+            const TcDecay& d = sh.dec[k % kDec];
             float f0 = 0.0f, f1 = 0.0f;
 #pragma unroll
             for (int i = 0; i < kP / 2; ++i) {
@@ -456,10 +464,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 f1 = fmaxf(f1, fabsf(S[i].y));
             }
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(f0, f1)));
-            if (lane == 0) sh.red[1][warp & 3] = m;
+            uint32_t* red = sh.red[1][s2];
+            if (lane == 0) red[warp & 3] = m;
             ok = ok && wait(&sh.s_empty, ph ^ 1u);
             if (ptx::named_barrier_or(2, 128, !ok)) break;
-            const float2 ss = pow2_scale(max(max(sh.red[1][0], sh.red[1][1]), max(sh.red[1][2], sh.red[1][3])), 13);
+            const float2 ss = pow2_scale(max(max(red[0], red[1]), max(red[2], red[3])), 13);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t o[4];
@@ -472,17 +481,16 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             }
             if (row == 0) sh.ks[s2] = ss.y;
             ptx::fence_proxy_async_smem();
-            if (ptx::named_barrier_or(2, 128, false)) break;
             arrive(&sh.s_full);
-            ok = wait(&sh.dec_full[s2], ph2) && wait(&sh.d_full, ph);
+            ok = wait(&sh.dec_full[k % kDec], (uint32_t)(k / kDec) & 1u) && wait(&sh.d_full, ph);
             if (!ok) continue;                         // the next barrier ends the group
             ptx::tc_fence_after();
-            const float keep = d.done[kT - 1], back = __fmul_rn(__fmul_rn(d.kb, d.kd), *(volatile float*)&sh.kx[s2]);
+            const float keep = d.done[kT - 1], back = __fmul_rn(__fmul_rn(d.kb, d.kd), *(volatile float*)&sh.kx[k % kDec]);
 #pragma unroll
             for (int c = 0; c < kP; c += 16) {
                 uint32_t r[16];
                 ptx::tmem_ld_32x32b_x16(t_lane + kColD + c, r);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     S[c / 2 + i] = ffma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(back, back),
@@ -490,7 +498,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             }
             ptx::tc_fence_before();
             arrive(&sh.d_empty);
-            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[s2]);
+            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[k % kDec]);
         }
         if (ok && p.final_state && (it.flags & kLast)) {
 #pragma unroll
@@ -504,12 +512,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
         const float skip = a.d_skip[h];
         for (int k = 0; k < n_ch; ++k) {
             const int s2 = k & 1;
-            const uint32_t ph2 = (uint32_t)(k >> 1) & 1u, ph = (uint32_t)k & 1u;
-            const TcDecay& d = sh.dec[s2];
+            const uint32_t ph = (uint32_t)k & 1u;
+            const TcDecay& d = sh.dec[k % kDec];
             const uint32_t s_x = base + s2 * kStageTc + 4 * kTile;
-            if (!wait(&sh.dec_full[s2], ph2) || !wait(&sh.y_full, ph)) break;
+            if (!wait(&sh.dec_full[k % kDec], (uint32_t)(k / kDec) & 1u) || !wait(&sh.y_full, ph)) break;
             ptx::tc_fence_after();
-            const float kx = *(volatile float*)&sh.kx[s2];
+            const float kx = *(volatile float*)&sh.kx[k % kDec];
             const float alpha = __fmul_rn(d.done[row], __fmul_rn(*(volatile float*)&sh.ks[s2], d.kc));
             const float beta = __fmul_rn(__fmul_rn(d.kc, d.kb), __fmul_rn(d.kd, kx)), sx = __fmul_rn(skip, kx);
 #pragma unroll 1
@@ -517,7 +525,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
                 uint32_t yi[16], ya[16], o[8];
                 ptx::tmem_ld_32x32b_x16(t_lane + kColYi + c, yi);
                 ptx::tmem_ld_32x32b_x16(t_lane + kColYa + c, ya);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(yi);
+                ptx::reg_fence(ya);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint4 x4 = ptx::lds128(piece(s_x, row, (c >> 3) + i));
@@ -544,7 +553,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             }
             ptx::fence_proxy_async_smem();             // the tile's next contents come by TMA
             arrive(&sh.xt_empty[s2]);
-            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[s2]);
+            if (lane == 0) ptx::mbar_arrive(&sh.dec_empty[k % kDec]);
         }
     }
     __syncwarp();

@@ -240,7 +240,7 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int col = half * hw + c;
                 uint32_t r[32];
                 ptx::tmem_ld_32x32b_x32(tmem + (uint32_t)(buf * kBN + col) + ((uint32_t)(32 * q4) << 16), r);
-                ptx::tmem_ld_wait();
+                ptx::tmem_ld_wait(r);
                 if (c + 32 == hw) {           // the last read of this accumulator
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -660,7 +660,7 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
                 uint32_t r[32];
                 if (n > 0) {
                     ptx::tmem_ld_32x32b_x32(tmem + (uint32_t)(256 * i + col) + ((uint32_t)(32 * q4) << 16), r);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_wait(r);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) r[e] = 0u;
