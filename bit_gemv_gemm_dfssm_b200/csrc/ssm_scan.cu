@@ -26,8 +26,6 @@ namespace scan {
 
 namespace {
 
-constexpr int kThreads = 128;
-
 // ------------------------------------------------------------------------------- the work table
 
 constexpr int kTableThreads = 1024;
@@ -556,44 +554,68 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const flo
 
 // The state alone through an item: blockIdx.y 0 forward in time (u = x, v = B), 1 backward (u = dy, v = C: the
 // state's gradient). STORE: from its start, at every chunk to the workspace; otherwise from zero, the
-// item's own contribution and decay, for what starts behind it.
+// item's own contribution and decay, for what starts behind it. Eight warps; warp (pw, hv) holds the channels
+// 16 pw .. and the states 64 hv .. in fp32 accumulators. v comes in fp16 (scan_tiles_kernel), the weighted u enters
+// as two fp16 parts under a power-of-two scale of the warp's channels.
+struct StateDecay {
+    float wt[kQ];        // the weights of u
+    float keep;          // exp(cum_64)
+    float cum;           // cum_64
+    float pad[2];
+};
+constexpr int kStTile = 16384 + 8192;                                    // v, u
+constexpr int kStateSmem = 2 * kStTile + 8 * 2048 + 2 * (int)sizeof(StateDecay) + 128;
+
 template <bool STORE>
-__global__ void __launch_bounds__(kThreads, 3) scan_state_kernel(const Args a, const StateArgs o) {
-    constexpr int kSt = 16384 + 8192;
+__global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const StateArgs o) {
     extern __shared__ uint8_t smem_raw[];
+    __shared__ Decay scratch;                        // of warp 0
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
-    Decay* dec = reinterpret_cast<Decay*>(smem + 2 * kSt + 16384);
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const uint32_t stage = base + 2 * kSt + 4096 * w;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, pw = w & 3, hv = w >> 2;
+    const uint32_t stage = base + 2 * kStTile + 2048 * w;
+    StateDecay* dec = reinterpret_cast<StateDecay*>(smem + 2 * kStTile + 8 * 2048);
     const bool rev = blockIdx.y != 0;
+    const int ngroups = a.nheads / a.per_group;
     const int h = blockIdx.x % a.nheads, g = h / a.per_group;
     Item it;
     if (!get_item(a, blockIdx.x / a.nheads, it) || it.len < 0) return;
     if (!STORE && (!(it.flags & kCut) || (it.flags & (rev ? kFirst : kLast)))) return;     // nothing starts behind it
     const int n_ch = (it.len + kQ - 1) / kQ;
     const uint16_t* u = (rev ? o.dy : a.x) + (int64_t)h * kP;
-    const uint16_t* v = (rev ? a.c : a.b) + (int64_t)g * kN;
-    const int64_t ldu = rev ? o.lddy : a.ldx, ldv = rev ? a.ldc : a.ldb;
+    const int64_t ldu = rev ? o.lddy : a.ldx;
     auto chunk_of = [&](int k) { return rev ? n_ch - 1 - k : k; };
+    // a chunk's tile and scale; the forward pass's table has chunks of 128 tokens
+    auto tile_at = [&](int q) { return (int64_t)(it.chunk0 + (a.chunk == kQ ? q : q >> 1)) * ngroups + g; };
     auto fetch = [&](int k) {
         if (k < n_ch) {
             const int q = chunk_of(k), t0 = it.t0 + q * kQ, n = min(kQ, it.len - q * kQ);
-            const uint32_t st = base + (k & 1) * kSt;
-            load_tile<128, kThreads>(st, v, ldv, t0, n, tid);
-            load_tile<64, kThreads>(st + 16384, u, ldu, t0, n, tid);
+            const uint32_t st = base + (k & 1) * kStTile;
+            const uint16_t* tl = a.tiles + (tile_at(q) * 2 + (rev ? 0 : 1)) * (128 * kN) + (a.chunk == kQ ? 0 : (q & 1) * kQ * kN);
+            load_tile<128, 256>(st, tl, kN, 0, kQ, tid);
+            load_tile<64, 256>(st + 16384, u, ldu, t0, n, tid);
         }
         ptx::cp_async_commit();
     };
     fetch(0);
     const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
-    StateFrag S;
+    float S[8][4];
+    const int s_at = (16 * pw + (lane >> 2)) * kN + 64 * hv + 2 * (lane & 3);
     const int64_t sh = ((int64_t)it.seq * a.nheads + h) * kStateElems;
     const int64_t slot = ((int64_t)(rev ? a.cap_slots : 0) + it.slot) * a.nheads + h;
-    const float* start = rev ? o.dfinal : a.init;
-    if (STORE && (it.flags & kCut)) state_load(S, a.seg_state + slot * kStateElems, w, lane);
-    else if (STORE && start) state_load(S, start + sh, w, lane);
-    else state_zero(S);
+    {
+        const float* start = rev ? o.dfinal : a.init;
+        const float* src = !STORE ? nullptr : it.flags & kCut ? a.seg_state + slot * kStateElems : start ? start + sh : nullptr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float2 lo = make_float2(0.0f, 0.0f), hi = lo;
+            if (src) {
+                lo = *reinterpret_cast<const float2*>(src + s_at + 8 * j);
+                hi = *reinterpret_cast<const float2*>(src + s_at + 8 * kN + 8 * j);
+            }
+            S[j][0] = lo.x; S[j][1] = lo.y; S[j][2] = hi.x; S[j][3] = hi.y;
+        }
+    }
     float total = 0.0f, raw0 = 0.0f, raw1 = 0.0f;
     auto raws = [&](int k) {                    // the chunk's dt, one chunk before its decays are needed
         if (w != 0 || k >= n_ch) return;
@@ -603,34 +625,118 @@ __global__ void __launch_bounds__(kThreads, 3) scan_state_kernel(const Args a, c
     };
     auto decay = [&](int k) {
         if (w != 0 || k >= n_ch) return;
-        chunk_decay(dec[k & 1], raw0, raw1, min(kQ, it.len - chunk_of(k) * kQ), bias, a2, lane);
+        StateDecay& d = dec[k & 1];
+        chunk_decay(scratch, raw0, raw1, min(kQ, it.len - chunk_of(k) * kQ), bias, a2, lane);
+        __syncwarp();
+        float2 wt = reinterpret_cast<const float2*>(rev ? scratch.done : scratch.left)[lane];
+        if (!rev) {
+            const float2 dt = reinterpret_cast<const float2*>(scratch.dt)[lane];
+            wt = make_float2(__fmul_rn(wt.x, dt.x), __fmul_rn(wt.y, dt.y));
+        }
+        reinterpret_cast<float2*>(d.wt)[lane] = wt;
+        if (lane == 0) {
+            d.keep = scratch.done[kQ - 1];
+            d.cum = scratch.cum[kQ - 1];
+        }
     };
     raws(0);
     decay(0);
     raws(1);
     for (int k = 0; k < n_ch; ++k) {
-        const uint32_t st = base + (k & 1) * kSt;
-        const Decay& d = dec[k & 1];
+        const uint32_t s_v = base + (k & 1) * kStTile, s_u = s_v + 16384;
+        const StateDecay& d = dec[k & 1];
         ptx::cp_async_wait<0>();
         __syncthreads();
         fetch(k + 1);
         decay(k + 1);
         raws(k + 2);
-        if (STORE)
-            state_store_split(S, (rev ? o.dstates : o.states) + ((int64_t)(it.chunk0 + chunk_of(k)) * a.nheads + h) * 2 * kStateElems,
-                              stage, w, lane);
-        total = __fadd_rn(total, d.cum[kQ - 1]);
-        state_update(S, d.done[kQ - 1], st + 16384, st, rev ? d.done : d.left, d.dt, !rev, w, lane);
+        const float2 tsc = a.tile_scale[tile_at(chunk_of(k))];
+        if (STORE) {
+            // the warp's 16 rows x 64 states as bf16 high and low parts (2^-17 of each value), staged so that whole
+            // 128-byte rows go out
+            uint16_t* dst = (rev ? o.dstates : o.states) +
+                            ((int64_t)(it.chunk0 + chunk_of(k)) * a.nheads + h) * 2 * kStateElems + 16 * pw * kN + 64 * hv;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    uint32_t q[4], lo;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        split_bf16x2(S[j + (i >> 1)][2 * (i & 1)], S[j + (i >> 1)][2 * (i & 1) + 1], q[i], lo);
+                        if (part) q[i] = lo;
+                    }
+                    const int mi = lane >> 3;    // rows 0..7 and 8..15 of tile j, then of tile j + 1
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+                                 ::"r"(tile128(stage, 8 * (mi & 1) + (lane & 7), j + (mi >> 1))), "r"(q[0]), "r"(q[1]),
+                                 "r"(q[2]), "r"(q[3]) : "memory");
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 4 * i + (lane >> 3), pc = lane & 7;
+                    *reinterpret_cast<uint4*>(dst + part * kStateElems + row * kN + 8 * pc) = ptx::lds128(tile128(stage, row, pc));
+                }
+            }
+        }
+        // the scale of the weighted u, from its largest value: what a fast decay leaves keeps its bits
+        uint32_t um = 0u;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const float2 w0 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 2 * (lane & 3));
+            const float2 w1 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 8 + 2 * (lane & 3));
+            uint32_t ua[4];
+            frag_at<128>(s_u, 16 * ks, 16 * pw, lane, ua);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 ww = q < 2 ? w0 : w1;
+                um = max(um, max(__float_as_uint(fabsf(__fmul_rn(bf16_lo(ua[q]), ww.x))),
+                                 __float_as_uint(fabsf(__fmul_rn(bf16_hi(ua[q]), ww.y)))));
+            }
+        }
+        const float2 us = pow2_scale(__reduce_max_sync(0xffffffffu, um), 13);
+        float D[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) D[j][0] = D[j][1] = D[j][2] = D[j][3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const float2 w0 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 2 * (lane & 3));
+            const float2 w1 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 8 + 2 * (lane & 3));
+            uint32_t ua[4], hi[4], lo[4];
+            frag_at<128>(s_u, 16 * ks, 16 * pw, lane, ua);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 ww = q < 2 ? w0 : w1;
+                split_f16x2(__fmul_rn(__fmul_rn(bf16_lo(ua[q]), ww.x), us.x), __fmul_rn(__fmul_rn(bf16_hi(ua[q]), ww.y), us.x),
+                            hi[q], lo[q]);
+            }
+            uint32_t bb[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) frag_bt<256>(s_v, 16 * ks, 64 * hv + 16 * q, lane, bb[q]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) mma_h(D[q], lo, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) mma_h(D[q], hi, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
+        }
+        total = __fadd_rn(total, d.cum);
+        const float keep = d.keep, back = __fmul_rn(rev ? tsc.x : tsc.y, us.y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) S[j][q] = __fmaf_rn(D[j][q], back, __fmul_rn(S[j][q], keep));
     }
     ptx::cp_async_wait<0>();
-    if (!STORE) {
-        state_store(S, a.seg_state + slot * kStateElems, w, lane);
-        if (tid == 0) a.seg_decay[slot] = exp2f(total);
-    } else if (rev && o.dinit && (it.flags & kFirst)) {
-        state_store(S, o.dinit + sh, w, lane);
+    float* dst = !STORE ? a.seg_state + slot * kStateElems : rev && o.dinit && (it.flags & kFirst) ? o.dinit + sh : nullptr;
+    if (dst) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            *reinterpret_cast<float2*>(dst + s_at + 8 * j) = make_float2(S[j][0], S[j][1]);
+            *reinterpret_cast<float2*>(dst + s_at + 8 * kN + 8 * j) = make_float2(S[j][2], S[j][3]);
+        }
     }
+    if (!STORE && tid == 0) a.seg_decay[slot] = exp2f(total);
 }
-constexpr int kStateSmem = 2 * (16384 + 8192) + 16384 + 2 * (int)sizeof(Decay) + 128;
 
 // ------------------------------------------------------------------------------- host
 
@@ -657,7 +763,7 @@ Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     p.seq_items = o;   o = up256(o + sizeof(Item) * (size_t)p.cap_items);
     p.seq_slots = o;   o = up256(o + sizeof(int2) * (size_t)nseq);
     p.chunks = o;      o = up256(o + sizeof(Chunk) * (size_t)p.cap_chunks);
-    const size_t tiles = p.direct || backward ? 0 : (size_t)p.cap_chunks * ngroups;
+    const size_t tiles = p.direct ? 0 : (size_t)p.cap_chunks * ngroups;
     p.tiles = o;       o = up256(o + tiles * 2 * 128 * kN * 2);
     p.tile_scale = o;  o = up256(o + tiles * sizeof(float2));
     const size_t slots = (backward ? 2 : 1) * (size_t)p.cap_slots * nheads;
@@ -757,14 +863,14 @@ dfssm_status setup() {
 }
 
 cudaError_t launch_table(const Args& a, cudaStream_t s) {
-    if (a.direct) return cudaSuccess;
     scan_table_kernel<<<1, kTableThreads, 0, s>>>(a);
+    scan_tiles_kernel<<<2 * a.cap_chunks * (a.nheads / a.per_group), 512, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_segment_starts(const Args& a, const StateArgs& o, int directions, cudaStream_t s) {
     if (a.total <= a.seg_len) return cudaSuccess;          // no sequence can be cut
-    scan_state_kernel<false><<<dim3(a.cap_items * a.nheads, directions), kThreads, kStateSmem, s>>>(a, o);
+    scan_state_kernel<false><<<dim3(a.cap_items * a.nheads, directions), 256, kStateSmem, s>>>(a, o);
     scan_carry_kernel<<<dim3(a.nseq * a.nheads, directions), 256, 0, s>>>(a, a.init, o.dfinal);
     return cudaGetLastError();
 }
@@ -772,7 +878,7 @@ cudaError_t launch_segment_starts(const Args& a, const StateArgs& o, int directi
 cudaError_t launch_states(const Args& a, const StateArgs& o, cudaStream_t s) {
     cudaError_t e = launch_segment_starts(a, o, 2, s);
     if (e != cudaSuccess) return e;
-    scan_state_kernel<true><<<dim3(a.cap_items * a.nheads, 2), kThreads, kStateSmem, s>>>(a, o);
+    scan_state_kernel<true><<<dim3(a.cap_items * a.nheads, 2), 256, kStateSmem, s>>>(a, o);
     return cudaGetLastError();
 }
 
@@ -811,7 +917,6 @@ extern "C" dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const df
     } else {
         if (launch_table(a, s) != cudaSuccess || launch_segment_starts(a, StateArgs{}, 1, s) != cudaSuccess)
             return DFSSM_ERR_CUDA;
-        scan_tiles_kernel<<<2 * a.cap_chunks * dims->ngroups, 512, 0, s>>>(a);
         if (launch_tc(a, static_cast<uint16_t*>(y), y_stride, final_state, s) != cudaSuccess) return DFSSM_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;

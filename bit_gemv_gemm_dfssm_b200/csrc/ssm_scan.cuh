@@ -192,14 +192,6 @@ __device__ __forceinline__ void frag_bt(uint32_t base, int k0, int n0, int lane,
     ldmatrix_x4_trans(tile_at<W>(base, k0 + 8 * (mi & 1) + (lane & 7), (n0 >> 3) + (mi >> 1)), r);
 }
 
-// (a, b) as three bf16 pairs whose sum is (a, b) to 2^-24 (each difference is exact in fp32)
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = bf16x2_of(make_float2(a, b));
-    const float ra = __fsub_rn(a, bf16_lo(hi)), rb = __fsub_rn(b, bf16_hi(hi));
-    mid = bf16x2_of(make_float2(ra, rb));
-    lo = bf16x2_of(make_float2(__fsub_rn(ra, bf16_lo(mid)), __fsub_rn(rb, bf16_hi(mid))));
-}
-
 __device__ __forceinline__ float softplus_dt(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
 __device__ __forceinline__ float bf16f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
@@ -238,104 +230,6 @@ __device__ __forceinline__ float raw_dt(const Args& a, int t0, int n, int h, int
     return i < n ? bf16f(a.dt[(int64_t)(t0 + i) * a.lddt + h]) : 0.0f;
 }
 
-// A warp's slice of a state: channels 16 w .. 16 w + 15, all 128 states, as 16 accumulator tiles
-// (tile j: n = 8 j + 2 (lane % 4) + {0, 1}; registers 0, 1: p = lane / 4, registers 2, 3: p + 8)
-struct StateFrag {
-    float v[16][4];
-};
-__device__ __forceinline__ void state_load(StateFrag& s, const float* src, int w, int lane) {
-    const float* p = src + (16 * w + (lane >> 2)) * kN + 2 * (lane & 3);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float2 lo = *reinterpret_cast<const float2*>(p + 8 * j);
-        const float2 hi = *reinterpret_cast<const float2*>(p + 8 * kN + 8 * j);
-        s.v[j][0] = lo.x; s.v[j][1] = lo.y; s.v[j][2] = hi.x; s.v[j][3] = hi.y;
-    }
-}
-__device__ __forceinline__ void state_zero(StateFrag& s) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) s.v[j][0] = s.v[j][1] = s.v[j][2] = s.v[j][3] = 0.0f;
-}
-__device__ __forceinline__ void state_store(const StateFrag& s, float* dst, int w, int lane) {
-    float* p = dst + (16 * w + (lane >> 2)) * kN + 2 * (lane & 3);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        *reinterpret_cast<float2*>(p + 8 * j) = make_float2(s.v[j][0], s.v[j][1]);
-        *reinterpret_cast<float2*>(p + 8 * kN + 8 * j) = make_float2(s.v[j][2], s.v[j][3]);
-    }
-}
-// The warp's 16 rows of the state as bf16 high and low parts (2^-17 of each value) to dst, [64][128] each, high
-// part first; staged in 4 KB of the warp's own shared memory, so that whole 256-byte rows go out.
-__device__ __forceinline__ void state_store_split(const StateFrag& s, uint16_t* dst, uint32_t stage, int w, int lane) {
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            uint32_t q[4], lo;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                split_bf16x2(s.v[j + (i >> 1)][2 * (i & 1)], s.v[j + (i >> 1)][2 * (i & 1) + 1], q[i], lo);
-                if (part) q[i] = lo;
-            }
-            // matrices: rows 0..7 and 8..15 of tile j, then of tile j + 1
-            const int mi = lane >> 3;
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
-                         ::"r"(tile256(stage, 8 * (mi & 1) + (lane & 7), j + (mi >> 1))), "r"(q[0]), "r"(q[1]), "r"(q[2]),
-                         "r"(q[3]) : "memory");
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = 2 * i + (lane >> 4), pc = lane & 15;
-            *reinterpret_cast<uint4*>(dst + part * kStateElems + (16 * w + row) * kN + 8 * pc) =
-                ptx::lds128(tile256(stage, row, pc));
-        }
-    }
-    __syncwarp();
-}
-
-// s = keep s + sum_t wt[t] u_t v_t^T over the chunk: u tile [64][64], v tile [64][128]. The fp32 products
-// wt u enter the MMAs as three bf16 parts, so that the state keeps fp32's precision.
-__device__ __forceinline__ void state_update(StateFrag& s, float keep, uint32_t u, uint32_t v, const float* wt,
-                                             const float* dt, bool use_dt, int w, int lane) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s.v[j][i] = __fmul_rn(s.v[j][i], keep);
-#pragma unroll 1
-    for (int k = 0; k < kQ; k += 16) {
-        uint32_t r[4], hi[4], mid[4], lo[4];
-        frag_at<128>(u, k, 16 * w, lane, r);
-        float2 w0 = *reinterpret_cast<const float2*>(wt + k + 2 * (lane & 3));
-        float2 w1 = *reinterpret_cast<const float2*>(wt + k + 8 + 2 * (lane & 3));
-        if (use_dt) {
-            const float2 d0 = *reinterpret_cast<const float2*>(dt + k + 2 * (lane & 3));
-            const float2 d1 = *reinterpret_cast<const float2*>(dt + k + 8 + 2 * (lane & 3));
-            w0 = make_float2(__fmul_rn(w0.x, d0.x), __fmul_rn(w0.y, d0.y));
-            w1 = make_float2(__fmul_rn(w1.x, d1.x), __fmul_rn(w1.y, d1.y));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 ww = i < 2 ? w0 : w1;
-            split3(__fmul_rn(bf16_lo(r[i]), ww.x), __fmul_rn(bf16_hi(r[i]), ww.y), hi[i], mid[i], lo[i]);
-        }
-        // eight accumulators at a time, so that one's three MMAs are far apart
-#pragma unroll
-        for (int j = 0; j < 16; j += 8) {
-            uint32_t bb[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) frag_bt<256>(v, k, 8 * (j + 2 * q), lane, bb[q]);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mma(s.v[j + q], lo, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mma(s.v[j + q], mid, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mma(s.v[j + q], hi, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
-        }
-    }
-}
-
 // ---- host side: the call's plan and workspace
 struct Plan {
     int seg_len, chunk, direct, cap_items, cap_chunks, cap_slots;
@@ -345,6 +239,7 @@ Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward);
 dfssm_status check_call(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int total, int nseq);
 dfssm_status setup();
 Args make_args(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int total, int nseq, const Plan& p, uint8_t* ws);
+// the work table, and B and C in fp16
 cudaError_t launch_table(const Args& a, cudaStream_t s);
 struct StateArgs {
     const uint16_t* dy;

@@ -520,7 +520,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant_
             const float kx = *(volatile float*)&sh.kx[k % kDec];
             const float alpha = __fmul_rn(d.done[row], __fmul_rn(*(volatile float*)&sh.ks[s2], d.kc));
             const float beta = __fmul_rn(__fmul_rn(d.kc, d.kb), __fmul_rn(d.kd, kx)), sx = __fmul_rn(skip, kx);
-#pragma unroll 1
+#pragma unroll 2
             for (int c = 0; c < kP; c += 16) {
                 uint32_t yi[16], ya[16], o[8];
                 ptx::tmem_ld_32x32b_x16(t_lane + kColYi + c, yi);
