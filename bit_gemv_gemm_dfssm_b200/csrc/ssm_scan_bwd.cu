@@ -18,7 +18,7 @@
 // column sums from t on; both come from the same fp32 values, so that what cancels cancels (taken from
 // dy . y and x . dx, which carry different roundings, d a_log was off by 3e-4).
 //
-// scan_grad_kernel: CTA (chunk, group, split of the group's heads), 8 warps, one head after another with the
+// scan_grad_kernel: CTA (chunk, group, split of the group's heads), 16 warps, one head after another with the
 // next head's tiles on the way (cp.async), bf16 warp MMAs; fp32 operands (M, W, S, dS) as two bf16
 // parts (2^-17). Partial dB and dC of the splits and partial parameter sums per chunk are added in
 // order by two small kernels.
@@ -29,7 +29,7 @@ namespace scan {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 
 struct GradArgs {
     const uint16_t* dy;
@@ -49,17 +49,23 @@ struct GradArgs {
 // one head's tiles
 constexpr int kTx = 0, kTy = 8192, kTs = 16384, kTd = 16384 + 32768, kTile = 16384 + 2 * 32768;
 
-struct HeadVec {
+// a head's decays, written one head ahead and read one head behind: three of them
+struct HeadDecay {
     Decay d;
     float sig[kQ];             // d softplus
+};
+// a head's partial sums, read one head behind: two of them
+struct HeadSums {
     float k[4][kQ], wl[4][kQ]; // x . dx' of the four channel slices: whole, and the part that leaves the chunk
     float z[4][kQ];            // C . (dy S) of the four state slices
     float row[4][kQ];          // sums of E over s, per block of 16 s
-    float col[2][kQ];          // sums of E over t, per block of 32 t
-    float skip[8];             // per warp: sum dy x
-    float dot[8];              // per warp: <dS, S>
+    float col[4][kQ];          // sums of E over t, per block of 16 t
+    float skip[16];            // per warp: sum dy x
+    float dot[16];             // per warp: <dS, S>
 };
-constexpr int kGradSmem = 2 * 16384 + 2 * kTile + 2 * 8192 + 2 * (int)sizeof(HeadVec) + 128;
+constexpr int kVecAt = 2 * 16384 + 2 * kTile + 2 * 8192;
+constexpr int kGradSmem = kVecAt + 2 * (int)sizeof(HeadSums) + 3 * (int)sizeof(HeadDecay) + 128;
+static_assert(kGradSmem <= 227 * 1024, "shared memory of one CTA");
 
 // [64][128] bf16, contiguous in global memory, high then low part
 __device__ __forceinline__ void load_state_tiles(uint32_t dst, const uint16_t* src, int tid) {
@@ -75,7 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
     const uint32_t s_b = base, s_c = base + 16384, s_t = base + 32768, s_m = s_t + 2 * kTile;
-    HeadVec* vec = reinterpret_cast<HeadVec*>(smem + 32768 + 2 * kTile + 2 * 8192);
+    HeadSums* sums = reinterpret_cast<HeadSums*>(smem + kVecAt);
+    HeadDecay* decays = reinterpret_cast<HeadDecay*>(smem + kVecAt + 2 * sizeof(HeadSums));
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int ngroups = a.nheads / a.per_group;
     const int sp = blockIdx.x % o.splits, g = blockIdx.x / o.splits % ngroups, ci = blockIdx.x / o.splits / ngroups;
@@ -97,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         ptx::cp_async_commit();
     };
     auto vectors = [&](int h) {                   // one warp
-        HeadVec& v = vec[(h - h0) & 1];
+        if (h >= h1) return;
+        HeadDecay& v = decays[(h - h0) % 3];
         const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
         const float r0 = raw_dt(a, t0, n, h, 2 * lane), r1 = raw_dt(a, t0, n, h, 2 * lane + 1);
         chunk_decay(v.d, r0, r1, n, bias, a2, lane);
@@ -108,6 +116,60 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             v.sig[t] = x > 20.0f ? 1.0f : __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
         }
     };
+    // d dt of a head whose sums are there; one warp, lane l has tokens 2 l, 2 l + 1
+    auto finish = [&](int h) {
+        const HeadDecay& d = decays[(h - h0) % 3];
+        const HeadSums& v = sums[(h - h0) & 1];
+        const float A = -expf(a.a_log[h]);
+        float kp[2], q[2], wl[2], dot = 0.0f, sk = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            kp[i] = __fadd_rn(__fadd_rn(v.k[0][t], v.k[1][t]), __fadd_rn(v.k[2][t], v.k[3][t]));
+            wl[i] = __fmul_rn(d.d.dt[t],
+                              __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t])));
+            const float z = __fmul_rn(d.d.done[t],
+                                      __fadd_rn(__fadd_rn(v.z[0][t], v.z[1][t]), __fadd_rn(v.z[2][t], v.z[3][t])));
+            const float row = __fadd_rn(__fadd_rn(v.row[0][t], v.row[1][t]), __fadd_rn(v.row[2][t], v.row[3][t]));
+            q[i] = __fadd_rn(__fsub_rn(row, __fadd_rn(__fadd_rn(v.col[0][t], v.col[1][t]), __fadd_rn(v.col[2][t], v.col[3][t]))), z);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            dot = __fadd_rn(dot, v.dot[i]);
+            sk = __fadd_rn(sk, v.skip[i]);
+        }
+        // what enters at or after t and leaves it (from the right), what enters before t (from the left)
+        float suf = __fadd_rn(q[0], q[1]), pre = __fadd_rn(wl[0], wl[1]);
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const float u = __shfl_down_sync(0xffffffffu, suf, s), x = __shfl_up_sync(0xffffffffu, pre, s);
+            if (lane + s < 32) suf = __fadd_rn(suf, u);
+            if (lane >= s) pre = __fadd_rn(pre, x);
+        }
+        float after = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
+        if (lane == 31) after = 0.0f;
+        if (lane == 0) before = 0.0f;
+        const float over = __fmul_rn(d.d.done[kQ - 1], dot);
+        const float da[2] = {__fadd_rn(__fadd_rn(suf, before), over),
+                             __fadd_rn(__fadd_rn(__fadd_rn(q[1], after), __fadd_rn(before, wl[0])), over)};
+        float sb = 0.0f, sa = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            if (t >= n) continue;
+            const float dr = __fmul_rn(__fmaf_rn(A, da[i], kp[i]), d.sig[t]);
+            o.ddt[(int64_t)(t0 + t) * o.ldddt + h] = f32_to_bf16_bits(dr);
+            sb = __fadd_rn(sb, dr);
+            sa = __fmaf_rn(da[i], __fmul_rn(d.d.dt[t], A), sa);
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) {
+            sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, s));
+            sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, s));
+        }
+        if (lane == 0)
+            *reinterpret_cast<float4*>(o.sums + ((int64_t)ci * a.nheads + h) * 4) = make_float4(sb, sa, sk, 0.0f);
+    };
     load_tile<128, kThreads>(s_b, a.b + (int64_t)g * kN, a.ldb, t0, n, tid);
     load_tile<128, kThreads>(s_c, a.c + (int64_t)g * kN, a.ldc, t0, n, tid);
     fetch(h0);
@@ -115,74 +177,65 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
     ptx::cp_async_wait<0>();
     __syncthreads();
 
-    // G^T: warp (ws, wt) has rows s = 16 ws .., columns t = 32 wt ..
+    // G^T: warp (ws, wt) has rows s = 16 ws .., columns t = 16 wt ..; six of the sixteen have t < s everywhere
     const int ws = w & 3, wt = w >> 2;
-    float G[4][4], W[4][4];
+    float G[2][4], W[2][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) G[j][i] = W[j][i] = 0.0f;
+    if (wt >= ws) {
 #pragma unroll 2
-    for (int kk = 0; kk < kN; kk += 16) {
-        uint32_t ba[4];
-        frag_a<256>(s_b, 16 * ws, kk, lane, ba);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (32 * wt + 16 * j < 16 * ws) continue;                 // t < s everywhere
-            uint32_t cb[4];
-            frag_b<256>(s_c, 32 * wt + 16 * j, kk, lane, cb);
-            mma(G[2 * j], ba, cb[0], cb[1]);
-            mma(G[2 * j + 1], ba, cb[2], cb[3]);
+        for (int kk = 0; kk < kN; kk += 16) {
+            uint32_t ba[4], cb[4];
+            frag_a<256>(s_b, 16 * ws, kk, lane, ba);
+            frag_b<256>(s_c, 16 * wt, kk, lane, cb);
+            mma(G[0], ba, cb[0], cb[1]);
+            mma(G[1], ba, cb[2], cb[3]);
         }
     }
-    // dB rows s, dC rows t: 32 (w & 1) + 16 i .., columns 32 (w / 2) + 8 j ..
-    const int rw = 32 * (w & 1), cw = 32 * (w >> 1), pw = 16 * (w >> 1);
-    float dB[2][4][4], dC[2][4][4];
+    // warps 0 .. 7 have dC, rows t, the others dB, rows s: 32 (w & 1) + 16 i .., columns 32 (w / 2 % 4) + 8 j ..
+    const bool side = w >= 8;
+    const int rw = 32 * (w & 1), cw = 32 * ((w >> 1) & 3), pw = 16 * wt;
+    float acc[2][4][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) dB[i][j][q] = dC[i][j][q] = 0.0f;
+            for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.0f;
 
     for (int h = h0; h < h1; ++h) {
         const uint32_t st = s_t + ((h - h0) & 1) * kTile;
         const uint32_t s_x = st + kTx, s_y = st + kTy, s_s = st + kTs, s_d = st + kTd;
-        HeadVec& v = vec[(h - h0) & 1];
+        const Decay& dc = decays[(h - h0) % 3].d;
+        HeadSums& v = sums[(h - h0) & 1];
         const float skip = a.d_skip[h];
-        ptx::cp_async_wait<0>();
-        __syncthreads();                          // this head's tiles and vectors are there, the last one's are free
-        fetch(h + 1);
+        fetch(h + 1);                             // over the tiles of the head before, which all warps have left
+        // two of the warps without a part of Z
+        if (w == 3 && h > h0) finish(h - 1);
+        if (w == 2) vectors(h + 1);
 
         // ---- Z^T, then M^T to shared memory and W^T in registers
-        {
-            float Z[4][4];
+        if (wt >= ws) {
+            float Z[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) Z[j][0] = Z[j][1] = Z[j][2] = Z[j][3] = 0.0f;
+            for (int j = 0; j < 2; ++j) Z[j][0] = Z[j][1] = Z[j][2] = Z[j][3] = 0.0f;
 #pragma unroll
             for (int kk = 0; kk < kP; kk += 16) {
-                uint32_t xa[4];
+                uint32_t xa[4], yb[4];
                 frag_a<128>(s_x, 16 * ws, kk, lane, xa);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (32 * wt + 16 * j < 16 * ws) continue;
-                    uint32_t yb[4];
-                    frag_b<128>(s_y, 32 * wt + 16 * j, kk, lane, yb);
-                    mma(Z[2 * j], xa, yb[0], yb[1]);
-                    mma(Z[2 * j + 1], xa, yb[2], yb[3]);
-                }
+                frag_b<128>(s_y, 16 * wt, kk, lane, yb);
+                mma(Z[0], xa, yb[0], yb[1]);
+                mma(Z[1], xa, yb[2], yb[3]);
             }
             const int s = 16 * ws + (lane >> 2);
-            const float cs0 = v.d.cum[s], cs1 = v.d.cum[s + 8], ds0 = v.d.dt[s], ds1 = v.d.dt[s + 8];
+            const float cs0 = dc.cum[s], cs1 = dc.cum[s + 8], ds0 = dc.dt[s], ds1 = dc.dt[s + 8];
             float col0 = 0.0f, col1 = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 32 * wt + 8 * j + 2 * (lane & 3);
-                if (32 * wt + 16 * (j >> 1) < 16 * ws) {
-                    if (lane < 4) *reinterpret_cast<float2*>(v.row[ws] + t) = make_float2(0.0f, 0.0f);
-                    continue;
-                }
-                const float2 ct = *reinterpret_cast<const float2*>(v.d.cum + t);
+            for (int j = 0; j < 2; ++j) {
+                const int t = 16 * wt + 8 * j + 2 * (lane & 3);
+                const float2 ct = *reinterpret_cast<const float2*>(dc.cum + t);
                 float l[4];
                 l[0] = t >= s ? exp2f(__fsub_rn(ct.x, cs0)) : 0.0f;
                 l[1] = t + 1 >= s ? exp2f(__fsub_rn(ct.y, cs0)) : 0.0f;
@@ -205,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                     rs.y = __fadd_rn(rs.y, __shfl_xor_sync(0xffffffffu, rs.y, q));
                 }
                 if (lane < 4) *reinterpret_cast<float2*>(v.row[ws] + t) = rs;
-                const uint32_t p0 = tile128(s_m, s, 4 * wt + j) + 4 * (lane & 3);
-                const uint32_t p1 = tile128(s_m, s + 8, 4 * wt + j) + 4 * (lane & 3);
+                const uint32_t p0 = tile128(s_m, s, 2 * wt + j) + 4 * (lane & 3);
+                const uint32_t p1 = tile128(s_m, s + 8, 2 * wt + j) + 4 * (lane & 3);
                 ptx::sts32(p0, m0);
                 ptx::sts32(p1, m1);
                 ptx::sts32(p0 + 8192, n0);
@@ -225,170 +278,161 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 v.col[wt][s] = col0;
                 v.col[wt][s + 8] = col1;
             }
+        } else {
+            if (lane < 8) *reinterpret_cast<float2*>(v.row[ws] + 16 * wt + 2 * lane) = make_float2(0.0f, 0.0f);
+            else if (lane < 16) *reinterpret_cast<float2*>(v.col[wt] + 16 * ws + 2 * (lane - 8)) = make_float2(0.0f, 0.0f);
         }
         __syncthreads();                          // M^T is there
 
-        // ---- dx, rows s = rw + 16 i .., channels pw + 8 p ..
+        // ---- dx, rows s = 16 ws .., channels pw + 8 p ..
         {
-            float X[2][2][4];
+            float X[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) X[i][p][0] = X[i][p][1] = X[i][p][2] = X[i][p][3] = 0.0f;
+            for (int p = 0; p < 2; ++p) X[p][0] = X[p][1] = X[p][2] = X[p][3] = 0.0f;
 #pragma unroll 4
             for (int kk = 0; kk < kN; kk += 16) {
-                uint32_t dh[4], dl[4];
+                uint32_t dh[4], dl[4], ba[4];
                 frag_b<256>(s_d, pw, kk, lane, dh);
                 frag_b<256>(s_d + 16384, pw, kk, lane, dl);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t ba[4];
-                    frag_a<256>(s_b, rw + 16 * i, kk, lane, ba);
-                    mma(X[i][0], ba, dl[0], dl[1]);
-                    mma(X[i][1], ba, dl[2], dl[3]);
-                    mma(X[i][0], ba, dh[0], dh[1]);
-                    mma(X[i][1], ba, dh[2], dh[3]);
-                }
+                frag_a<256>(s_b, 16 * ws, kk, lane, ba);
+                mma(X[0], ba, dl[0], dl[1]);
+                mma(X[1], ba, dl[2], dl[3]);
+                mma(X[0], ba, dh[0], dh[1]);
+                mma(X[1], ba, dh[2], dh[3]);
             }
-            uint32_t xv[2][2][2], yv[2][2][2];    // x and dy where the accumulators are
+            uint32_t xv[2][2], yv[2][2];          // x and dy where the accumulators are
             float sk = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int hf = 0; hf < 2; ++hf) {
+                const int s = 16 * ws + 8 * hf + (lane >> 2);
+                const float e = dc.left[s];
+                float wl = 0.0f;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int s = rw + 16 * i + 8 * hf + (lane >> 2);
-                    const float e = v.d.left[s];
-                    float wl = 0.0f;
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const uint32_t at = 4 * (lane & 3);
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv[i][hf][p]) : "r"(tile128(s_x, s, (pw >> 3) + p) + at));
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv[i][hf][p]) : "r"(tile128(s_y, s, (pw >> 3) + p) + at));
-                        float& x0 = X[i][p][2 * hf];
-                        float& x1 = X[i][p][2 * hf + 1];
-                        x0 = __fmul_rn(x0, e);
-                        x1 = __fmul_rn(x1, e);
-                        wl = __fmaf_rn(x0, bf16_lo(xv[i][hf][p]), wl);
-                        wl = __fmaf_rn(x1, bf16_hi(xv[i][hf][p]), wl);
-                        sk = __fmaf_rn(bf16_lo(yv[i][hf][p]), bf16_lo(xv[i][hf][p]), sk);
-                        sk = __fmaf_rn(bf16_hi(yv[i][hf][p]), bf16_hi(xv[i][hf][p]), sk);
-                    }
-                    wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 1));
-                    wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 2));
-                    if ((lane & 3) == 0) v.wl[w >> 1][s] = wl;
+                for (int p = 0; p < 2; ++p) {
+                    const uint32_t at = 4 * (lane & 3);
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv[hf][p]) : "r"(tile128(s_x, s, (pw >> 3) + p) + at));
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv[hf][p]) : "r"(tile128(s_y, s, (pw >> 3) + p) + at));
+                    float& x0 = X[p][2 * hf];
+                    float& x1 = X[p][2 * hf + 1];
+                    x0 = __fmul_rn(x0, e);
+                    x1 = __fmul_rn(x1, e);
+                    wl = __fmaf_rn(x0, bf16_lo(xv[hf][p]), wl);
+                    wl = __fmaf_rn(x1, bf16_hi(xv[hf][p]), wl);
+                    sk = __fmaf_rn(bf16_lo(yv[hf][p]), bf16_lo(xv[hf][p]), sk);
+                    sk = __fmaf_rn(bf16_hi(yv[hf][p]), bf16_hi(xv[hf][p]), sk);
                 }
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                if (16 * kt < rw) continue;       // t < s everywhere
-                uint32_t yb[4];
-                frag_bt<128>(s_y, 16 * kt, pw, lane, yb);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (16 * kt < rw + 16 * i) continue;
-                    uint32_t mh[4], ml[4];
-                    frag_a<128>(s_m, rw + 16 * i, 16 * kt, lane, mh);
-                    frag_a<128>(s_m + 8192, rw + 16 * i, 16 * kt, lane, ml);
-                    mma(X[i][0], ml, yb[0], yb[1]);
-                    mma(X[i][1], ml, yb[2], yb[3]);
-                    mma(X[i][0], mh, yb[0], yb[1]);
-                    mma(X[i][1], mh, yb[2], yb[3]);
-                }
+                wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 1));
+                wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 2));
+                if ((lane & 3) == 0) v.wl[wt][s] = wl;
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int kt = 0; kt < 4; ++kt) {
+                if (kt < ws) continue;            // t < s everywhere
+                uint32_t yb[4], mh[4], ml[4];
+                frag_bt<128>(s_y, 16 * kt, pw, lane, yb);
+                frag_a<128>(s_m, 16 * ws, 16 * kt, lane, mh);
+                frag_a<128>(s_m + 8192, 16 * ws, 16 * kt, lane, ml);
+                mma(X[0], ml, yb[0], yb[1]);
+                mma(X[1], ml, yb[2], yb[3]);
+                mma(X[0], mh, yb[0], yb[1]);
+                mma(X[1], mh, yb[2], yb[3]);
+            }
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int s = rw + 16 * i + 8 * hf + (lane >> 2);
-                    const float dts = v.d.dt[s];
-                    float k = 0.0f;
+            for (int hf = 0; hf < 2; ++hf) {
+                const int s = 16 * ws + 8 * hf + (lane >> 2);
+                const float dts = dc.dt[s];
+                float k = 0.0f;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const float x0 = X[i][p][2 * hf], x1 = X[i][p][2 * hf + 1];
-                        k = __fmaf_rn(x0, bf16_lo(xv[i][hf][p]), k);
-                        k = __fmaf_rn(x1, bf16_hi(xv[i][hf][p]), k);
-                        if (s < n)
-                            *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
-                                bf16x2_of(make_float2(__fmaf_rn(dts, x0, __fmul_rn(skip, bf16_lo(yv[i][hf][p]))),
-                                                      __fmaf_rn(dts, x1, __fmul_rn(skip, bf16_hi(yv[i][hf][p])))));
-                    }
-                    k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 1));
-                    k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 2));
-                    if ((lane & 3) == 0) v.k[w >> 1][s] = k;
+                for (int p = 0; p < 2; ++p) {
+                    const float x0 = X[p][2 * hf], x1 = X[p][2 * hf + 1];
+                    k = __fmaf_rn(x0, bf16_lo(xv[hf][p]), k);
+                    k = __fmaf_rn(x1, bf16_hi(xv[hf][p]), k);
+                    if (s < n)
+                        *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
+                            bf16x2_of(make_float2(__fmaf_rn(dts, x0, __fmul_rn(skip, bf16_lo(yv[hf][p]))),
+                                                  __fmaf_rn(dts, x1, __fmul_rn(skip, bf16_hi(yv[hf][p])))));
                 }
+                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 1));
+                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 2));
+                if ((lane & 3) == 0) v.k[wt][s] = k;
+            }
 #pragma unroll
             for (int q = 16; q > 0; q >>= 1) sk = __fadd_rn(sk, __shfl_xor_sync(0xffffffffu, sk, q));
             if (lane == 0) v.skip[w] = sk;
         }
 
         // ---- dC += exp(cum_t) dy S, dB += dt_s exp(cum_64 - cum_s) x dS
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
+        {
             const uint32_t s_u = side ? s_x : s_y, s_v = side ? s_d : s_s;
-            float T[2][4][4];
+            float e[2][2], z[2][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) T[i][j][0] = T[i][j][1] = T[i][j][2] = T[i][j][3] = 0.0f;
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int r = rw + 16 * i + 8 * hf + (lane >> 2);
+                    e[i][hf] = side ? __fmul_rn(dc.dt[r], dc.left[r]) : dc.done[r];
+                    z[i][hf] = 0.0f;
+                }
 #pragma unroll
-            for (int kk = 0; kk < kP; kk += 16) {
-                uint32_t ua[2][4];
-                frag_a<128>(s_u, rw, kk, lane, ua[0]);
-                frag_a<128>(s_u, rw + 16, kk, lane, ua[1]);
+            for (int j = 0; j < 2; ++j) {         // 16 columns
+                float T[2][2][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) T[i][p][0] = T[i][p][1] = T[i][p][2] = T[i][p][3] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < kP; kk += 16) {
                     uint32_t vh[4], vl[4];
                     frag_bt<256>(s_v, kk, cw + 16 * j, lane, vh);
                     frag_bt<256>(s_v + 16384, kk, cw + 16 * j, lane, vl);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mma(T[i][2 * j], ua[i], vl[0], vl[1]);
-                        mma(T[i][2 * j + 1], ua[i], vl[2], vl[3]);
-                        mma(T[i][2 * j], ua[i], vh[0], vh[1]);
-                        mma(T[i][2 * j + 1], ua[i], vh[2], vh[3]);
+                        uint32_t ua[4];
+                        frag_a<128>(s_u, rw + 16 * i, kk, lane, ua);
+                        mma(T[i][0], ua, vl[0], vl[1]);
+                        mma(T[i][1], ua, vl[2], vl[3]);
+                        mma(T[i][0], ua, vh[0], vh[1]);
+                        mma(T[i][1], ua, vh[2], vh[3]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = rw + 16 * i + (lane >> 2);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        if (!side) {              // C_t . (dy S)_t over the warp's states
+                            uint32_t c0, c1;
+                            const uint32_t at = 4 * (lane & 3);
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c0) : "r"(tile256(s_c, r, (cw >> 3) + 2 * j + p) + at));
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c1) : "r"(tile256(s_c, r + 8, (cw >> 3) + 2 * j + p) + at));
+                            z[i][0] = __fmaf_rn(T[i][p][0], bf16_lo(c0), __fmaf_rn(T[i][p][1], bf16_hi(c0), z[i][0]));
+                            z[i][1] = __fmaf_rn(T[i][p][2], bf16_lo(c1), __fmaf_rn(T[i][p][3], bf16_hi(c1), z[i][1]));
+                        }
+                        float(&to)[4] = acc[i][2 * j + p];
+                        to[0] = __fmaf_rn(e[i][0], T[i][p][0], to[0]);
+                        to[1] = __fmaf_rn(e[i][0], T[i][p][1], to[1]);
+                        to[2] = __fmaf_rn(e[i][1], T[i][p][2], to[2]);
+                        to[3] = __fmaf_rn(e[i][1], T[i][p][3], to[3]);
                     }
                 }
             }
+            if (!side) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = rw + 16 * i + (lane >> 2);
-                const float e0 = side ? __fmul_rn(v.d.dt[r], v.d.left[r]) : v.d.done[r];
-                const float e1 = side ? __fmul_rn(v.d.dt[r + 8], v.d.left[r + 8]) : v.d.done[r + 8];
-                if (side == 0) {                  // C_t . (dy S)_t over the warp's states
-                    float z0 = 0.0f, z1 = 0.0f;
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t c0, c1;
-                        const uint32_t at = 4 * (lane & 3);
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c0) : "r"(tile256(s_c, r, (cw >> 3) + j) + at));
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c1) : "r"(tile256(s_c, r + 8, (cw >> 3) + j) + at));
-                        z0 = __fmaf_rn(T[i][j][0], bf16_lo(c0), __fmaf_rn(T[i][j][1], bf16_hi(c0), z0));
-                        z1 = __fmaf_rn(T[i][j][2], bf16_lo(c1), __fmaf_rn(T[i][j][3], bf16_hi(c1), z1));
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float t = z[i][hf];
+                        t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                        t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                        if ((lane & 3) == 0) v.z[w >> 1][rw + 16 * i + 8 * hf + (lane >> 2)] = t;
                     }
-#pragma unroll
-                    for (int q = 1; q < 4; q <<= 1) {
-                        z0 = __fadd_rn(z0, __shfl_xor_sync(0xffffffffu, z0, q));
-                        z1 = __fadd_rn(z1, __shfl_xor_sync(0xffffffffu, z1, q));
-                    }
-                    if ((lane & 3) == 0) {
-                        v.z[w >> 1][r] = z0;
-                        v.z[w >> 1][r + 8] = z1;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float(&acc)[4] = side ? dB[i][j] : dC[i][j];
-                    acc[0] = __fmaf_rn(e0, T[i][j][0], acc[0]);
-                    acc[1] = __fmaf_rn(e0, T[i][j][1], acc[1]);
-                    acc[2] = __fmaf_rn(e1, T[i][j][2], acc[2]);
-                    acc[3] = __fmaf_rn(e1, T[i][j][3], acc[3]);
-                }
             }
         }
         // ---- <dS, S>
         {
             float dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 const int idx = tid + kThreads * i, row = idx >> 4, pc = idx & 15;
                 const uint4 sh = ptx::lds128(tile256(s_s, row, pc)), sl = ptx::lds128(tile256(s_s + 16384, row, pc));
                 const uint4 dh = ptx::lds128(tile256(s_d, row, pc)), dl = ptx::lds128(tile256(s_d + 16384, row, pc));
@@ -404,73 +448,21 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             for (int q = 16; q > 0; q >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, q));
             if (lane == 0) v.dot[w] = dot;
         }
-        if (w == 7 && h + 1 < h1) vectors(h + 1);
-        __syncthreads();                          // the head's sums are there
-        // ---- d dt: lane l has tokens 2 l, 2 l + 1
-        if (w == 0) {
-            const float A = -expf(a.a_log[h]);
-            float kp[2], q[2], wl[2], dot = 0.0f, sk = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                kp[i] = __fadd_rn(__fadd_rn(v.k[0][t], v.k[1][t]), __fadd_rn(v.k[2][t], v.k[3][t]));
-                wl[i] = __fmul_rn(v.d.dt[t],
-                                  __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t])));
-                const float z = __fmul_rn(v.d.done[t],
-                                          __fadd_rn(__fadd_rn(v.z[0][t], v.z[1][t]), __fadd_rn(v.z[2][t], v.z[3][t])));
-                const float row = __fadd_rn(__fadd_rn(v.row[0][t], v.row[1][t]), __fadd_rn(v.row[2][t], v.row[3][t]));
-                q[i] = __fadd_rn(__fsub_rn(row, __fadd_rn(v.col[0][t], v.col[1][t])), z);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dot = __fadd_rn(dot, v.dot[i]);
-                sk = __fadd_rn(sk, v.skip[i]);
-            }
-            // what enters at or after t and leaves it (from the right), what enters before t (from the left)
-            float suf = __fadd_rn(q[0], q[1]), pre = __fadd_rn(wl[0], wl[1]);
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const float u = __shfl_down_sync(0xffffffffu, suf, s), x = __shfl_up_sync(0xffffffffu, pre, s);
-                if (lane + s < 32) suf = __fadd_rn(suf, u);
-                if (lane >= s) pre = __fadd_rn(pre, x);
-            }
-            float after = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
-            if (lane == 31) after = 0.0f;
-            if (lane == 0) before = 0.0f;
-            const float over = __fmul_rn(v.d.done[kQ - 1], dot);
-            const float da[2] = {__fadd_rn(__fadd_rn(suf, before), over),
-                                 __fadd_rn(__fadd_rn(__fadd_rn(q[1], after), __fadd_rn(before, wl[0])), over)};
-            float sb = 0.0f, sa = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                if (t >= n) continue;
-                const float dr = __fmul_rn(__fmaf_rn(A, da[i], kp[i]), v.sig[t]);
-                o.ddt[(int64_t)(t0 + t) * o.ldddt + h] = f32_to_bf16_bits(dr);
-                sb = __fadd_rn(sb, dr);
-                sa = __fmaf_rn(da[i], __fmul_rn(v.d.dt[t], A), sa);
-            }
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) {
-                sb = __fadd_rn(sb, __shfl_xor_sync(0xffffffffu, sb, s));
-                sa = __fadd_rn(sa, __shfl_xor_sync(0xffffffffu, sa, s));
-            }
-            if (lane == 0)
-                *reinterpret_cast<float4*>(o.sums + ((int64_t)ci * a.nheads + h) * 4) = make_float4(sb, sa, sk, 0.0f);
-        }
+        ptx::cp_async_wait<0>();
+        __syncthreads();                          // the head's sums and the next one's tiles are there
     }
-    ptx::cp_async_wait<0>();
+    if (w == 0) finish(h1 - 1);
 
     // ---- W^T as two bf16 parts, then dB += W^T C, dC += W B
     {
         const int s = 16 * ws + (lane >> 2);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             uint32_t h0v, l0v, h1v, l1v;
             split_bf16x2(W[j][0], W[j][1], h0v, l0v);
             split_bf16x2(W[j][2], W[j][3], h1v, l1v);
-            const uint32_t p0 = tile128(s_m, s, 4 * wt + j) + 4 * (lane & 3);
-            const uint32_t p1 = tile128(s_m, s + 8, 4 * wt + j) + 4 * (lane & 3);
+            const uint32_t p0 = tile128(s_m, s, 2 * wt + j) + 4 * (lane & 3);
+            const uint32_t p1 = tile128(s_m, s + 8, 2 * wt + j) + 4 * (lane & 3);
             ptx::sts32(p0, h0v);
             ptx::sts32(p1, h1v);
             ptx::sts32(p0 + 8192, l0v);
@@ -478,31 +470,29 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
 #pragma unroll 1
-        for (int kk = 0; kk < kQ; kk += 16) {
-            if (side ? kk + 15 < rw : kk > rw + 31) continue;      // dB: t >= s; dC: s <= t
-            uint32_t vb[2][4];
-            frag_bt<256>(side ? s_c : s_b, kk, cw, lane, vb[0]);
-            frag_bt<256>(side ? s_c : s_b, kk, cw + 16, lane, vb[1]);
+    for (int kk = 0; kk < kQ; kk += 16) {
+        if (side ? kk + 15 < rw : kk > rw + 31) continue;      // dB: t >= s; dC: s <= t
+        uint32_t vb[2][4];
+        frag_bt<256>(side ? s_c : s_b, kk, cw, lane, vb[0]);
+        frag_bt<256>(side ? s_c : s_b, kk, cw + 16, lane, vb[1]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int part = 1; part >= 0; --part) {
-                    uint32_t wa[4];
-                    if (side) frag_a<128>(s_m + part * 8192, rw + 16 * i, kk, lane, wa);
-                    else frag_at<128>(s_m + part * 8192, kk, rw + 16 * i, lane, wa);
+            for (int part = 1; part >= 0; --part) {
+                uint32_t wa[4];
+                if (side) frag_a<128>(s_m + part * 8192, rw + 16 * i, kk, lane, wa);
+                else frag_at<128>(s_m + part * 8192, kk, rw + 16 * i, lane, wa);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        mma(side ? dB[i][2 * j] : dC[i][2 * j], wa, vb[j][0], vb[j][1]);
-                        mma(side ? dB[i][2 * j + 1] : dC[i][2 * j + 1], wa, vb[j][2], vb[j][3]);
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    mma(acc[i][2 * j], wa, vb[j][0], vb[j][1]);
+                    mma(acc[i][2 * j + 1], wa, vb[j][2], vb[j][3]);
                 }
             }
         }
     }
     const int64_t ldp = (int64_t)ngroups * kN;
+    float* part = side ? o.db_part : o.dc_part;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -511,26 +501,26 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             if (r >= n) continue;
             const int64_t at = ((int64_t)sp * a.total + t0 + r) * ldp + g * kN + cw + 2 * (lane & 3);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                *reinterpret_cast<float2*>(o.db_part + at + 8 * j) = make_float2(dB[i][j][2 * hf], dB[i][j][2 * hf + 1]);
-                *reinterpret_cast<float2*>(o.dc_part + at + 8 * j) = make_float2(dC[i][j][2 * hf], dC[i][j][2 * hf + 1]);
-            }
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float2*>(part + at + 8 * j) = make_float2(acc[i][j][2 * hf], acc[i][j][2 * hf + 1]);
         }
 }
 
-// dB and dC: the splits' parts added in order, 4 columns per thread; CTA per chunk (rows of no chunk stay)
+// dB and dC: the splits' parts added in order, 4 columns per thread; 8 CTAs per chunk (one: 24 us for 6 chunks of
+// 16 parts), rows of no chunk stay
 __global__ void __launch_bounds__(256) scan_sum_kernel(const Args a, const float* __restrict__ db_part,
                                                        const float* __restrict__ dc_part, int splits, uint16_t* db,
                                                        int64_t lddb, uint16_t* dc, int64_t lddc) {
-    if ((int)blockIdx.x >= a.count[1]) return;
-    const Chunk ch = a.chunks[blockIdx.x];
+    if ((int)(blockIdx.x >> 3) >= a.count[1]) return;
+    const Chunk ch = a.chunks[blockIdx.x >> 3];
     const int cols = a.nheads / a.per_group * kN, per = cols / 4;
     const float* part = blockIdx.y ? dc_part : db_part;
     uint16_t* out = blockIdx.y ? dc : db;
     const int64_t ld = blockIdx.y ? lddc : lddb;
-    for (int i = threadIdx.x; i < ch.n * per; i += 256) {
+    for (int i = (blockIdx.x & 7) * 256 + threadIdx.x; i < ch.n * per; i += 8 * 256) {
         const int r = i / per, c = 4 * (i - r * per);
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
         for (int k = 0; k < splits; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(part + ((int64_t)k * a.total + ch.t0 + r) * cols + c);
             s = make_float4(__fadd_rn(s.x, v.x), __fadd_rn(s.y, v.y), __fadd_rn(s.z, v.z), __fadd_rn(s.w, v.w));
@@ -670,7 +660,7 @@ extern "C" dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const df
     if (launch_table(a, s) != cudaSuccess || launch_states(a, st_args, s) != cudaSuccess)
         return DFSSM_ERR_CUDA;
     scan_grad_kernel<<<p.cap_chunks * dims->ngroups * sp.splits, kThreads, kGradSmem, s>>>(a, o);
-    scan_sum_kernel<<<dim3(p.cap_chunks, 2), 256, 0, s>>>(a, o.db_part, o.dc_part, sp.splits,
+    scan_sum_kernel<<<dim3(8 * p.cap_chunks, 2), 256, 0, s>>>(a, o.db_part, o.dc_part, sp.splits,
                                                           static_cast<uint16_t*>(gr->db), gr->db_stride,
                                                           static_cast<uint16_t*>(gr->dc), gr->dc_stride);
     scan_params_kernel<<<dims->nheads, 256, 0, s>>>(a, o.sums, gr->ddt_bias, gr->da_log, gr->dd_skip);
