@@ -282,85 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             if (lane < 8) *reinterpret_cast<float2*>(v.row[ws] + 16 * wt + 2 * lane) = make_float2(0.0f, 0.0f);
             else if (lane < 16) *reinterpret_cast<float2*>(v.col[wt] + 16 * ws + 2 * (lane - 8)) = make_float2(0.0f, 0.0f);
         }
-        __syncthreads();                          // M^T is there
-
-        // ---- dx, rows s = 16 ws .., channels pw + 8 p ..
-        {
-            float X[2][4];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) X[p][0] = X[p][1] = X[p][2] = X[p][3] = 0.0f;
-#pragma unroll 4
-            for (int kk = 0; kk < kN; kk += 16) {
-                uint32_t dh[4], dl[4], ba[4];
-                frag_b<256>(s_d, pw, kk, lane, dh);
-                frag_b<256>(s_d + 16384, pw, kk, lane, dl);
-                frag_a<256>(s_b, 16 * ws, kk, lane, ba);
-                mma(X[0], ba, dl[0], dl[1]);
-                mma(X[1], ba, dl[2], dl[3]);
-                mma(X[0], ba, dh[0], dh[1]);
-                mma(X[1], ba, dh[2], dh[3]);
-            }
-            uint32_t xv[2][2], yv[2][2];          // x and dy where the accumulators are
-            float sk = 0.0f;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int s = 16 * ws + 8 * hf + (lane >> 2);
-                const float e = dc.left[s];
-                float wl = 0.0f;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const uint32_t at = 4 * (lane & 3);
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv[hf][p]) : "r"(tile128(s_x, s, (pw >> 3) + p) + at));
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv[hf][p]) : "r"(tile128(s_y, s, (pw >> 3) + p) + at));
-                    float& x0 = X[p][2 * hf];
-                    float& x1 = X[p][2 * hf + 1];
-                    x0 = __fmul_rn(x0, e);
-                    x1 = __fmul_rn(x1, e);
-                    wl = __fmaf_rn(x0, bf16_lo(xv[hf][p]), wl);
-                    wl = __fmaf_rn(x1, bf16_hi(xv[hf][p]), wl);
-                    sk = __fmaf_rn(bf16_lo(yv[hf][p]), bf16_lo(xv[hf][p]), sk);
-                    sk = __fmaf_rn(bf16_hi(yv[hf][p]), bf16_hi(xv[hf][p]), sk);
-                }
-                wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 1));
-                wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 2));
-                if ((lane & 3) == 0) v.wl[wt][s] = wl;
-            }
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                if (kt < ws) continue;            // t < s everywhere
-                uint32_t yb[4], mh[4], ml[4];
-                frag_bt<128>(s_y, 16 * kt, pw, lane, yb);
-                frag_a<128>(s_m, 16 * ws, 16 * kt, lane, mh);
-                frag_a<128>(s_m + 8192, 16 * ws, 16 * kt, lane, ml);
-                mma(X[0], ml, yb[0], yb[1]);
-                mma(X[1], ml, yb[2], yb[3]);
-                mma(X[0], mh, yb[0], yb[1]);
-                mma(X[1], mh, yb[2], yb[3]);
-            }
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int s = 16 * ws + 8 * hf + (lane >> 2);
-                const float dts = dc.dt[s];
-                float k = 0.0f;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float x0 = X[p][2 * hf], x1 = X[p][2 * hf + 1];
-                    k = __fmaf_rn(x0, bf16_lo(xv[hf][p]), k);
-                    k = __fmaf_rn(x1, bf16_hi(xv[hf][p]), k);
-                    if (s < n)
-                        *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
-                            bf16x2_of(make_float2(__fmaf_rn(dts, x0, __fmul_rn(skip, bf16_lo(yv[hf][p]))),
-                                                  __fmaf_rn(dts, x1, __fmul_rn(skip, bf16_hi(yv[hf][p])))));
-                }
-                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 1));
-                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 2));
-                if ((lane & 3) == 0) v.k[wt][s] = k;
-            }
-#pragma unroll
-            for (int q = 16; q > 0; q >>= 1) sk = __fadd_rn(sk, __shfl_xor_sync(0xffffffffu, sk, q));
-            if (lane == 0) v.skip[w] = sk;
-        }
-
         // ---- dC += exp(cum_t) dy S, dB += dt_s exp(cum_64 - cum_s) x dS
         {
             const uint32_t s_u = side ? s_x : s_y, s_v = side ? s_d : s_s;
@@ -447,6 +368,83 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
 #pragma unroll
             for (int q = 16; q > 0; q >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, q));
             if (lane == 0) v.dot[w] = dot;
+        }
+        // ---- dx, rows s = 16 ws .., channels pw + 8 p ..
+        {
+            float X[2][4];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) X[p][0] = X[p][1] = X[p][2] = X[p][3] = 0.0f;
+#pragma unroll 4
+            for (int kk = 0; kk < kN; kk += 16) {
+                uint32_t dh[4], dl[4], ba[4];
+                frag_b<256>(s_d, pw, kk, lane, dh);
+                frag_b<256>(s_d + 16384, pw, kk, lane, dl);
+                frag_a<256>(s_b, 16 * ws, kk, lane, ba);
+                mma(X[0], ba, dl[0], dl[1]);
+                mma(X[1], ba, dl[2], dl[3]);
+                mma(X[0], ba, dh[0], dh[1]);
+                mma(X[1], ba, dh[2], dh[3]);
+            }
+            uint32_t xv[2][2], yv[2][2];          // x and dy where the accumulators are
+            float sk = 0.0f;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int s = 16 * ws + 8 * hf + (lane >> 2);
+                const float e = dc.left[s];
+                float wl = 0.0f;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const uint32_t at = 4 * (lane & 3);
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv[hf][p]) : "r"(tile128(s_x, s, (pw >> 3) + p) + at));
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv[hf][p]) : "r"(tile128(s_y, s, (pw >> 3) + p) + at));
+                    float& x0 = X[p][2 * hf];
+                    float& x1 = X[p][2 * hf + 1];
+                    x0 = __fmul_rn(x0, e);
+                    x1 = __fmul_rn(x1, e);
+                    wl = __fmaf_rn(x0, bf16_lo(xv[hf][p]), wl);
+                    wl = __fmaf_rn(x1, bf16_hi(xv[hf][p]), wl);
+                    sk = __fmaf_rn(bf16_lo(yv[hf][p]), bf16_lo(xv[hf][p]), sk);
+                    sk = __fmaf_rn(bf16_hi(yv[hf][p]), bf16_hi(xv[hf][p]), sk);
+                }
+                wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 1));
+                wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 2));
+                if ((lane & 3) == 0) v.wl[wt][s] = wl;
+            }
+            __syncthreads();                      // M^T is there
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                if (kt < ws) continue;            // t < s everywhere
+                uint32_t yb[4], mh[4], ml[4];
+                frag_bt<128>(s_y, 16 * kt, pw, lane, yb);
+                frag_a<128>(s_m, 16 * ws, 16 * kt, lane, mh);
+                frag_a<128>(s_m + 8192, 16 * ws, 16 * kt, lane, ml);
+                mma(X[0], ml, yb[0], yb[1]);
+                mma(X[1], ml, yb[2], yb[3]);
+                mma(X[0], mh, yb[0], yb[1]);
+                mma(X[1], mh, yb[2], yb[3]);
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int s = 16 * ws + 8 * hf + (lane >> 2);
+                const float dts = dc.dt[s];
+                float k = 0.0f;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float x0 = X[p][2 * hf], x1 = X[p][2 * hf + 1];
+                    k = __fmaf_rn(x0, bf16_lo(xv[hf][p]), k);
+                    k = __fmaf_rn(x1, bf16_hi(xv[hf][p]), k);
+                    if (s < n)
+                        *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
+                            bf16x2_of(make_float2(__fmaf_rn(dts, x0, __fmul_rn(skip, bf16_lo(yv[hf][p]))),
+                                                  __fmaf_rn(dts, x1, __fmul_rn(skip, bf16_hi(yv[hf][p])))));
+                }
+                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 1));
+                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 2));
+                if ((lane & 3) == 0) v.k[wt][s] = k;
+            }
+#pragma unroll
+            for (int q = 16; q > 0; q >>= 1) sk = __fadd_rn(sk, __shfl_xor_sync(0xffffffffu, sk, q));
+            if (lane == 0) v.skip[w] = sk;
         }
         ptx::cp_async_wait<0>();
         __syncthreads();                          // the head's sums and the next one's tiles are there
