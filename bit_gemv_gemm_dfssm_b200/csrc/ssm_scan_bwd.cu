@@ -294,47 +294,48 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                     e[i][hf] = side ? __fmul_rn(dc.dt[r], dc.left[r]) : dc.done[r];
                     z[i][hf] = 0.0f;
                 }
+            float T[2][4][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {         // 16 columns
-                float T[2][2][4];
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int j = 0; j < 4; ++j) T[i][j][0] = T[i][j][1] = T[i][j][2] = T[i][j][3] = 0.0f;
+#pragma unroll 1
+            for (int kk = 0; kk < kP; kk += 16) {
+                uint32_t ua[2][4];
+                frag_a<128>(s_u, rw, kk, lane, ua[0]);
+                frag_a<128>(s_u, rw + 16, kk, lane, ua[1]);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) T[i][p][0] = T[i][p][1] = T[i][p][2] = T[i][p][3] = 0.0f;
-#pragma unroll
-                for (int kk = 0; kk < kP; kk += 16) {
+                for (int j = 0; j < 2; ++j) {
                     uint32_t vh[4], vl[4];
                     frag_bt<256>(s_v, kk, cw + 16 * j, lane, vh);
                     frag_bt<256>(s_v + 16384, kk, cw + 16 * j, lane, vl);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint32_t ua[4];
-                        frag_a<128>(s_u, rw + 16 * i, kk, lane, ua);
-                        mma(T[i][0], ua, vl[0], vl[1]);
-                        mma(T[i][1], ua, vl[2], vl[3]);
-                        mma(T[i][0], ua, vh[0], vh[1]);
-                        mma(T[i][1], ua, vh[2], vh[3]);
+                        mma(T[i][2 * j], ua[i], vl[0], vl[1]);
+                        mma(T[i][2 * j + 1], ua[i], vl[2], vl[3]);
+                        mma(T[i][2 * j], ua[i], vh[0], vh[1]);
+                        mma(T[i][2 * j + 1], ua[i], vh[2], vh[3]);
                     }
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = rw + 16 * i + (lane >> 2);
+            for (int i = 0; i < 2; ++i) {
+                const int r = rw + 16 * i + (lane >> 2);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        if (!side) {              // C_t . (dy S)_t over the warp's states
-                            uint32_t c0, c1;
-                            const uint32_t at = 4 * (lane & 3);
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c0) : "r"(tile256(s_c, r, (cw >> 3) + 2 * j + p) + at));
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c1) : "r"(tile256(s_c, r + 8, (cw >> 3) + 2 * j + p) + at));
-                            z[i][0] = __fmaf_rn(T[i][p][0], bf16_lo(c0), __fmaf_rn(T[i][p][1], bf16_hi(c0), z[i][0]));
-                            z[i][1] = __fmaf_rn(T[i][p][2], bf16_lo(c1), __fmaf_rn(T[i][p][3], bf16_hi(c1), z[i][1]));
-                        }
-                        float(&to)[4] = acc[i][2 * j + p];
-                        to[0] = __fmaf_rn(e[i][0], T[i][p][0], to[0]);
-                        to[1] = __fmaf_rn(e[i][0], T[i][p][1], to[1]);
-                        to[2] = __fmaf_rn(e[i][1], T[i][p][2], to[2]);
-                        to[3] = __fmaf_rn(e[i][1], T[i][p][3], to[3]);
+                for (int j = 0; j < 4; ++j) {
+                    if (!side) {                  // C_t . (dy S)_t over the warp's states
+                        uint32_t c0, c1;
+                        const uint32_t at = 4 * (lane & 3);
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c0) : "r"(tile256(s_c, r, (cw >> 3) + j) + at));
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c1) : "r"(tile256(s_c, r + 8, (cw >> 3) + j) + at));
+                        z[i][0] = __fmaf_rn(T[i][j][0], bf16_lo(c0), __fmaf_rn(T[i][j][1], bf16_hi(c0), z[i][0]));
+                        z[i][1] = __fmaf_rn(T[i][j][2], bf16_lo(c1), __fmaf_rn(T[i][j][3], bf16_hi(c1), z[i][1]));
                     }
+                    float(&to)[4] = acc[i][j];
+                    to[0] = __fmaf_rn(e[i][0], T[i][j][0], to[0]);
+                    to[1] = __fmaf_rn(e[i][0], T[i][j][1], to[1]);
+                    to[2] = __fmaf_rn(e[i][1], T[i][j][2], to[2]);
+                    to[3] = __fmaf_rn(e[i][1], T[i][j][3], to[3]);
                 }
             }
             if (!side) {
