@@ -564,12 +564,12 @@ struct StateDecay {
     float pad[2];
 };
 constexpr int kStTile = 16384 + 8192;                                    // v, u
-constexpr int kStateSmem = 2 * kStTile + 8 * 2048 + 2 * (int)sizeof(StateDecay) + 128;
+constexpr int kStateSmem = 2 * kStTile + 8 * 2048 + 16 * (int)sizeof(StateDecay) + 128;
 
 template <bool STORE>
 __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const StateArgs o) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Decay scratch;                        // of warp 0
+    __shared__ Decay scratch_of[8];
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, pw = w & 3, hv = w >> 2;
@@ -616,16 +616,19 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
             S[j][0] = lo.x; S[j][1] = lo.y; S[j][2] = hi.x; S[j][3] = hi.y;
         }
     }
+    // the decays of eight chunks at a time, one per warp, in a ring of sixteen (one warp doing each chunk's in turn kept
+    // the others waiting at every chunk's barrier)
     float total = 0.0f, raw0 = 0.0f, raw1 = 0.0f;
-    auto raws = [&](int k) {                    // the chunk's dt, one chunk before its decays are needed
-        if (w != 0 || k >= n_ch) return;
+    auto raws = [&](int k) {
+        if (k >= n_ch) return;
         const int q = chunk_of(k), t0 = it.t0 + q * kQ, n = min(kQ, it.len - q * kQ);
         raw0 = raw_dt(a, t0, n, h, 2 * lane);
         raw1 = raw_dt(a, t0, n, h, 2 * lane + 1);
     };
     auto decay = [&](int k) {
-        if (w != 0 || k >= n_ch) return;
-        StateDecay& d = dec[k & 1];
+        if (k >= n_ch) return;
+        StateDecay& d = dec[k & 15];
+        Decay& scratch = scratch_of[w];
         chunk_decay(scratch, raw0, raw1, min(kQ, it.len - chunk_of(k) * kQ), bias, a2, lane);
         __syncwarp();
         float2 wt = reinterpret_cast<const float2*>(rev ? scratch.done : scratch.left)[lane];
@@ -639,17 +642,16 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
             d.cum = scratch.cum[kQ - 1];
         }
     };
-    raws(0);
-    decay(0);
-    raws(1);
+    raws(w);
+    decay(w);
     for (int k = 0; k < n_ch; ++k) {
         const uint32_t s_v = base + (k & 1) * kStTile, s_u = s_v + 16384;
-        const StateDecay& d = dec[k & 1];
+        const StateDecay& d = dec[k & 15];
         ptx::cp_async_wait<0>();
         __syncthreads();
         fetch(k + 1);
-        decay(k + 1);
-        raws(k + 2);
+        if ((k & 7) == 2) raws((k & ~7) + 8 + w);
+        if ((k & 7) == 4) decay((k & ~7) + 8 + w);
         const float2 tsc = a.tile_scale[tile_at(chunk_of(k))];
         if (STORE) {
             // the warp's 16 rows x 64 states as bf16 high and low parts (2^-17 of each value), staged so that whole

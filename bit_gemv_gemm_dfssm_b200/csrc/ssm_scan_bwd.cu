@@ -56,12 +56,12 @@ struct HeadDecay {
 };
 // a head's partial sums, read one head behind: two of them
 struct HeadSums {
-    float k[4][kQ], wl[4][kQ]; // x . dx' of the four channel slices: whole, and the part that leaves the chunk
+    float wl[4][kQ];           // x . dx' of the four channel slices, of the part that leaves the chunk
     float z[4][kQ];            // C . (dy S) of the four state slices
     float row[4][kQ];          // sums of E over s, per block of 16 s
-    float col[4][kQ];          // sums of E over t, per block of 16 t
-    float skip[16];            // per warp: sum dy x
-    float dot[16];             // per warp: <dS, S>
+    float col[4][kQ];          // sums of M o Z over t, per block of 16 t
+    float skip[kQ];            // dy . x
+    float dot[kThreads];       // <dS, S>
 };
 constexpr int kVecAt = 2 * 16384 + 2 * kTile + 2 * 8192;
 constexpr int kGradSmem = kVecAt + 2 * (int)sizeof(HeadSums) + 3 * (int)sizeof(HeadDecay) + 128;
@@ -121,22 +121,25 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         const HeadDecay& d = decays[(h - h0) % 3];
         const HeadSums& v = sums[(h - h0) & 1];
         const float A = -expf(a.a_log[h]);
-        float kp[2], q[2], wl[2], dot = 0.0f, sk = 0.0f;
+        float kp[2], q[2], wl[2], dot = 0.0f, sk = __fadd_rn(v.skip[2 * lane], v.skip[2 * lane + 1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
-            kp[i] = __fadd_rn(__fadd_rn(v.k[0][t], v.k[1][t]), __fadd_rn(v.k[2][t], v.k[3][t]));
-            wl[i] = __fmul_rn(d.d.dt[t],
-                              __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t])));
+            const float leaves = __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t]));
+            const float col = __fadd_rn(__fadd_rn(v.col[0][t], v.col[1][t]), __fadd_rn(v.col[2][t], v.col[3][t]));
+            kp[i] = __fadd_rn(leaves, col);               // x . (dS B), all of it
+            wl[i] = __fmul_rn(d.d.dt[t], leaves);
             const float z = __fmul_rn(d.d.done[t],
                                       __fadd_rn(__fadd_rn(v.z[0][t], v.z[1][t]), __fadd_rn(v.z[2][t], v.z[3][t])));
             const float row = __fadd_rn(__fadd_rn(v.row[0][t], v.row[1][t]), __fadd_rn(v.row[2][t], v.row[3][t]));
-            q[i] = __fadd_rn(__fsub_rn(row, __fadd_rn(__fadd_rn(v.col[0][t], v.col[1][t]), __fadd_rn(v.col[2][t], v.col[3][t]))), z);
+            q[i] = __fadd_rn(__fmaf_rn(-d.d.dt[t], col, row), z);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            dot = __fadd_rn(dot, v.dot[i]);
-            sk = __fadd_rn(sk, v.skip[i]);
+        for (int i = 0; i < kThreads / 32; ++i) dot = __fadd_rn(dot, v.dot[lane + 32 * i]);
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) {
+            dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, i));
+            sk = __fadd_rn(sk, __shfl_xor_sync(0xffffffffu, sk, i));
         }
         // what enters at or after t and leaves it (from the right), what enters before t (from the left)
         float suf = __fadd_rn(q[0], q[1]), pre = __fadd_rn(wl[0], wl[1]);
@@ -246,18 +249,22 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 uint32_t m0, n0, m1, n1;
                 split_bf16x2(m[0], m[1], m0, n0);
                 split_bf16x2(m[2], m[3], m1, n1);
-                // E, its sums over the warp's s for the thread's two t, and over the thread's t
-                const float e[4] = {__fmul_rn(__fmul_rn(m[0], ds0), Z[j][0]), __fmul_rn(__fmul_rn(m[1], ds0), Z[j][1]),
-                                    __fmul_rn(__fmul_rn(m[2], ds1), Z[j][2]), __fmul_rn(__fmul_rn(m[3], ds1), Z[j][3])};
-                col0 = __fadd_rn(col0, __fadd_rn(e[0], e[1]));
-                col1 = __fadd_rn(col1, __fadd_rn(e[2], e[3]));
-                float2 rs = make_float2(__fadd_rn(e[0], e[2]), __fadd_rn(e[1], e[3]));
+                // the sums of E over the warp's s for the thread's two t, and of M o Z over the thread's t
+                const float mz[4] = {__fmul_rn(m[0], Z[j][0]), __fmul_rn(m[1], Z[j][1]), __fmul_rn(m[2], Z[j][2]),
+                                     __fmul_rn(m[3], Z[j][3])};
+                col0 = __fadd_rn(col0, __fadd_rn(mz[0], mz[1]));
+                col1 = __fadd_rn(col1, __fadd_rn(mz[2], mz[3]));
+                float2 rs = make_float2(__fmaf_rn(mz[0], ds0, __fmul_rn(mz[2], ds1)), __fmaf_rn(mz[1], ds0, __fmul_rn(mz[3], ds1)));
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) {
                     rs.x = __fadd_rn(rs.x, __shfl_xor_sync(0xffffffffu, rs.x, q));
                     rs.y = __fadd_rn(rs.y, __shfl_xor_sync(0xffffffffu, rs.y, q));
                 }
                 if (lane < 4) *reinterpret_cast<float2*>(v.row[ws] + t) = rs;
+                if (t == s) v.skip[s] = Z[j][0];
+                if (t + 1 == s) v.skip[s] = Z[j][1];
+                if (t == s + 8) v.skip[s + 8] = Z[j][2];
+                if (t + 1 == s + 8) v.skip[s + 8] = Z[j][3];
                 const uint32_t p0 = tile128(s_m, s, 2 * wt + j) + 4 * (lane & 3);
                 const uint32_t p1 = tile128(s_m, s + 8, 2 * wt + j) + 4 * (lane & 3);
                 ptx::sts32(p0, m0);
@@ -366,9 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                     dot = __fmaf_rn(__fadd_rn(bf16_hi(a4[q]), bf16_hi(b4[q])), __fadd_rn(bf16_hi(c4[q]), bf16_hi(d4[q])), dot);
                 }
             }
-#pragma unroll
-            for (int q = 16; q > 0; q >>= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, q));
-            if (lane == 0) v.dot[w] = dot;
+            v.dot[tid] = dot;
         }
         // ---- dx, rows s = 16 ws .., channels pw + 8 p ..
         {
@@ -386,8 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 mma(X[0], ba, dh[0], dh[1]);
                 mma(X[1], ba, dh[2], dh[3]);
             }
-            uint32_t xv[2][2], yv[2][2];          // x and dy where the accumulators are
-            float sk = 0.0f;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int s = 16 * ws + 8 * hf + (lane >> 2);
@@ -396,16 +399,14 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     const uint32_t at = 4 * (lane & 3);
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv[hf][p]) : "r"(tile128(s_x, s, (pw >> 3) + p) + at));
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv[hf][p]) : "r"(tile128(s_y, s, (pw >> 3) + p) + at));
+                    uint32_t xv;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(xv) : "r"(tile128(s_x, s, (pw >> 3) + p) + at));
                     float& x0 = X[p][2 * hf];
                     float& x1 = X[p][2 * hf + 1];
                     x0 = __fmul_rn(x0, e);
                     x1 = __fmul_rn(x1, e);
-                    wl = __fmaf_rn(x0, bf16_lo(xv[hf][p]), wl);
-                    wl = __fmaf_rn(x1, bf16_hi(xv[hf][p]), wl);
-                    sk = __fmaf_rn(bf16_lo(yv[hf][p]), bf16_lo(xv[hf][p]), sk);
-                    sk = __fmaf_rn(bf16_hi(yv[hf][p]), bf16_hi(xv[hf][p]), sk);
+                    wl = __fmaf_rn(x0, bf16_lo(xv), wl);
+                    wl = __fmaf_rn(x1, bf16_hi(xv), wl);
                 }
                 wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 1));
                 wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 2));
@@ -428,24 +429,16 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             for (int hf = 0; hf < 2; ++hf) {
                 const int s = 16 * ws + 8 * hf + (lane >> 2);
                 const float dts = dc.dt[s];
-                float k = 0.0f;
+                if (s >= n) continue;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const float x0 = X[p][2 * hf], x1 = X[p][2 * hf + 1];
-                    k = __fmaf_rn(x0, bf16_lo(xv[hf][p]), k);
-                    k = __fmaf_rn(x1, bf16_hi(xv[hf][p]), k);
-                    if (s < n)
-                        *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
-                            bf16x2_of(make_float2(__fmaf_rn(dts, x0, __fmul_rn(skip, bf16_lo(yv[hf][p]))),
-                                                  __fmaf_rn(dts, x1, __fmul_rn(skip, bf16_hi(yv[hf][p])))));
+                    uint32_t yv;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv) : "r"(tile128(s_y, s, (pw >> 3) + p) + 4 * (lane & 3)));
+                    *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
+                        bf16x2_of(make_float2(__fmaf_rn(dts, X[p][2 * hf], __fmul_rn(skip, bf16_lo(yv))),
+                                              __fmaf_rn(dts, X[p][2 * hf + 1], __fmul_rn(skip, bf16_hi(yv)))));
                 }
-                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 1));
-                k = __fadd_rn(k, __shfl_xor_sync(0xffffffffu, k, 2));
-                if ((lane & 3) == 0) v.k[wt][s] = k;
             }
-#pragma unroll
-            for (int q = 16; q > 0; q >>= 1) sk = __fadd_rn(sk, __shfl_xor_sync(0xffffffffu, sk, q));
-            if (lane == 0) v.skip[w] = sk;
         }
         ptx::cp_async_wait<0>();
         __syncthreads();                          // the head's sums and the next one's tiles are there
