@@ -46,12 +46,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // -- logits kernel
-constexpr int kLgStages = 4;
-constexpr int kLgA = kBM * 128, kLgB = kBN * 128, kLgStage = kLgA + kLgB;     // 128 K bytes per stage
+constexpr int kLgRing = 4 * (kBM + kBN) * 128;          // stages of 128 K bytes of the tokens and of the table rows
+constexpr int kLgStages = 8;                            // at most; 4 of full tiles
 constexpr int kLgThreads = 12 * 32;      // TMA, MMA, 2 idle warps; 8 epilogue warps
 constexpr int kLgEpi = 256;
 constexpr int kLgOut = 8 * 2048;         // kGrad: an epilogue warp's 32 tokens x 32 columns
-constexpr int kLgSmem = kLgStages * kLgStage + kLgOut + 2 * kBN * 4 + 256 + 1024;
+constexpr int kLgSmem = kLgRing + kLgOut + 2 * kBN * 4 + 256 + 1024;
 
 // -- gradient kernel
 constexpr int kDhA = kBM * 128, kDhB = kBN * 128;      // 64 K values per stage and accumulator
@@ -68,6 +68,7 @@ struct LogitsArgs {
     const float* sx;
     int vocab, d, m;
     int bn;                              // table rows per tile: kBN or kBNFew
+    int a_bytes, stages;                 // of a stage: the tokens' rows; how many stages
     int v0, v_end;                       // table rows of this call
     float2* part;                        // kLse: [2 * v tiles][m]
     const float* lse;                    // kGrad
@@ -107,8 +108,8 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                    const LogitsArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t s_out = ptx::smem_u32(smem) + kLgStages * kLgStage;
-    float* s_scale = reinterpret_cast<float*>(smem + kLgStages * kLgStage + kLgOut); // [2][kBN]
+    const uint32_t s_out = ptx::smem_u32(smem) + kLgRing;
+    float* s_scale = reinterpret_cast<float*>(smem + kLgRing + kLgOut); // [2][kBN]
     uint64_t* full = reinterpret_cast<uint64_t*>(s_scale + 2 * kBN);                 // TMA bytes
     uint64_t* empty = full + kLgStages;                                              // MMA commit
     uint64_t* acc_full = empty + kLgStages;                                          // [2] MMA commit
@@ -121,11 +122,12 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int n_tiles = n_tt * ((a.v_end - a.v0 + a.bn - 1) / a.bn);
     const int hw = a.bn / 2;                          // columns of an epilogue warp's half: a multiple of 32
     const int n_k = (a.d + 127) / 128;
+    const int stages = a.stages, stage_bytes = a.a_bytes + a.bn * 128;
 
     // what follows in the stream may come in as CTAs end here; it waits for the whole grid before it reads
     ptx::pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kLgStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
         }
@@ -147,32 +149,37 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            int it = 0, s = 0;
+            uint32_t turn = 0;
             for (int tile = blockIdx.x; tile < n_tiles && !*abort_flag; tile += gridDim.x) {
                 const int vt = tile / n_tt, tt = tile - vt * n_tt;
                 for (int k = 0; k < n_k; ++k, ++it) {
-                    const int s = it % kLgStages;
-                    if (!ptx::mbar_wait(&empty[s], ((uint32_t)(it / kLgStages) & 1u) ^ 1u)) {
+                    if (!ptx::mbar_wait(&empty[s], turn ^ 1u)) {
                         give_up(a.err, abort_flag);
                         break;
                     }
-                    uint8_t* st = smem + s * kLgStage;
-                    ptx::mbar_arrive_expect_tx(&full[s], kLgA + a.bn * 128);
+                    uint8_t* st = smem + s * stage_bytes;
+                    ptx::mbar_arrive_expect_tx(&full[s], stage_bytes);
                     ptx::tma_load_2d(st, &map_q, k * 128, tt * kBM, &full[s]);
-                    ptx::tma_load_2d(st + kLgA, &map_e, k * 128, a.v0 + vt * a.bn, &full[s]);
+                    ptx::tma_load_2d(st + a.a_bytes, &map_e, k * 128, a.v0 + vt * a.bn, &full[s]);
+                    if (++s == stages) {
+                        s = 0;
+                        turn ^= 1u;
+                    }
                 }
             }
             // after a wait that gave up: the copies still in flight land before the CTA ends
             if (*abort_flag)
-                for (int i = max(0, it - kLgStages); i < it; ++i)
-                    ptx::mbar_wait(&full[i % kLgStages], (uint32_t)(i / kLgStages) & 1u);
+                for (int i = max(0, it - stages); i < it; ++i)
+                    ptx::mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u);
         }
     } else if (warp == 1) {
         if (lane == 0) {
             // kind::i8: D s32, A and B s8, both K-major
             const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(a.bn >> 3) << 17) |
                                    ((uint32_t)(kBM >> 4) << 24);
-            int it = 0, tc = 0;
+            int it = 0, tc = 0, s = 0;
+            uint32_t turn = 0;
             bool ok = true;
             for (int tile = blockIdx.x; tile < n_tiles && ok && !*abort_flag; tile += gridDim.x, ++tc) {
                 const int buf = tc & 1;
@@ -182,25 +189,30 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 ptx::tc_fence_after();
                 for (int k = 0; k < n_k; ++k, ++it) {
-                    const int s = it % kLgStages;
-                    if (!ptx::mbar_wait(&full[s], (uint32_t)(it / kLgStages) & 1u)) {
+                    if (!ptx::mbar_wait(&full[s], turn)) {
                         give_up(a.err, abort_flag);
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint64_t ad = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * kLgStage));
-                    const uint64_t bd = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * kLgStage + kLgA));
+                    // 128 rows of tokens from here on, of which those behind the call's last are the table's bytes:
+                    // their products go to lanes that nothing reads
+                    const uint64_t ad = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * stage_bytes));
+                    const uint64_t bd = ptx::kmajor_sw128_desc(ptx::smem_u32(smem + s * stage_bytes + a.a_bytes));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         ptx::mma_i8(tmem + (uint32_t)(buf * kBN), ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
                     ptx::mma_commit(&empty[s]);
+                    if (++s == stages) {
+                        s = 0;
+                        turn ^= 1u;
+                    }
                 }
                 if (ok) ptx::mma_commit(&acc_full[buf]);
             }
             if (*abort_flag)           // the MMAs issued so far complete before TMEM is given back
-                for (int i = max(0, it - kLgStages); i < it; ++i)
-                    ptx::mbar_wait(&empty[i % kLgStages], (uint32_t)(i / kLgStages) & 1u);
+                for (int i = max(0, it - stages); i < it; ++i)
+                    ptx::mbar_wait(&empty[i % stages], (uint32_t)(i / stages) & 1u);
         }
     } else if (warp >= 4) {
         const int e = threadIdx.x - 4 * 32, q4 = warp & 3, half = (warp - 4) >> 2;
@@ -749,6 +761,14 @@ inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 constexpr int kSms = 148;
 
+// A stage holds the tokens' rows that there are (in whole swizzle blocks of 8); the smaller it is, the more of them.
+int stage_tokens(int m) { return m < kBM ? (m + 7) / 8 * 8 : kBM; }
+int stage_count(int a_bytes, int bn) {
+    const int n = kLgRing / (a_bytes + bn * 128);
+    return n < kLgStages ? n : kLgStages;
+}
+static_assert(kBNFew >= kBM && kBNFew % 8 == 0, "the 128 rows that a product reads as tokens lie in the stage");
+
 int tile_rows(int m) { return m <= kBM ? kBNFew : kBN; }
 
 // How a gradient call is cut: token blocks, vocabulary pieces, the product's units over the CTAs.
@@ -901,7 +921,7 @@ extern "C" dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8
     float2* part = reinterpret_cast<float2*>(ws + w.part);
     CUtensorMap mq, me;
     const int bn = tile_rows(m);
-    if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q, d, m, d, kBM) ||
+    if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q, d, m, d, stage_tokens(m)) ||
         !encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, bn))
         return DFSSM_ERR_CUDA;
     LogitsArgs a{};
@@ -911,6 +931,8 @@ extern "C" dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8
     a.d = d;
     a.m = m;
     a.bn = bn;
+    a.a_bytes = stage_tokens(m) * 128;
+    a.stages = stage_count(a.a_bytes, bn);
     a.v0 = 0;
     a.v_end = vocab;
     a.part = part;
@@ -957,7 +979,7 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
     for (int t0 = 0; t0 < m && e == cudaSuccess; t0 += p.tok_block) {
         const int mb = m - t0 < p.tok_block ? m - t0 : p.tok_block;
         CUtensorMap mq, mg;
-        if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q + (int64_t)t0 * d, d, mb, d, kBM) ||
+        if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q + (int64_t)t0 * d, d, mb, d, stage_tokens(mb)) ||
             !encode_rows(&mg, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, g, p.piece, mb, p.piece, kBM))
             return DFSSM_ERR_CUDA;
         const int n_tt = (mb + kBM - 1) / kBM;
@@ -969,6 +991,8 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
             a.d = d;
             a.m = mb;
             a.bn = bn;
+            a.a_bytes = stage_tokens(mb) * 128;
+            a.stages = stage_count(a.a_bytes, bn);
             a.v0 = v0;
             a.v_end = vocab - v0 < p.piece ? vocab : v0 + p.piece;
             a.lse = lse + t0;
