@@ -135,8 +135,10 @@ __device__ __forceinline__ void mma_h(float (&d)[4], const uint32_t (&a)[4], uin
 }
 
 // The power of two 2^k that brings m (a largest magnitude, as bits) to [2^top, 2^(top + 1)), and 2^-k. k is kept
-// within +-100 (a zero maximum: the largest).
+// within +-100 (a zero maximum: the largest). An infinity or NaN among the values gives NaN: scaled by it, the finite ones
+// would go down to nothing unseen.
 __device__ __forceinline__ float2 pow2_scale(uint32_t m_bits, int top) {
+    if (m_bits >= 0x7F800000u) return make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
     const int k = max(-100, min(100, top + 127 - (int)(m_bits >> 23)));
     return make_float2(__int_as_float((127 + k) << 23), __int_as_float((127 - k) << 23));
 }

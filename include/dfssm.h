@@ -425,8 +425,11 @@ dfssm_status dfssm_ssm_scan_workspace_bytes(const dfssm_scan_dims* dims, int32_t
 
 /* y: total x (nheads headdim) bf16 (16-byte aligned, row stride y_stride a multiple of 8); final_state: as
  * init_state (which it may equal), the state behind each sequence's last token, or NULL. 1 <= total <=
- * 2^22, 1 <= nseq <= 65536, (total/128 + nseq) ngroups below 2^23. States are kept in fp32; a sequence is worked on in chunks of 64 or 128 tokens,
- * inside which a non-finite input can reach earlier tokens too (never another sequence).
+ * 2^22, 1 <= nseq <= 65536, (total/128 + nseq) ngroups below 2^23. States are kept in fp32; a sequence is
+ * worked on in chunks of 64 or 128 tokens. An Inf or NaN in x, b, c, dt or the initial state makes what it reaches Inf
+ * or NaN, and can do so to every channel of its head (of its group, from b and c) in its chunk, in front of it
+ * too, and behind it, but not in another sequence. Inside a chunk b and c are rounded to steps of 2^-28 of
+ * their group's largest magnitude (exact down to 2^-17 of it), the states' new part to 2^-38 of the largest addend.
  * workspace: 256-byte aligned, at least dfssm_ssm_scan_workspace_bytes, zeroed once before its first use.
  * Its first 4 bytes are a device error word (DFSSM_DEVERR_SEQLENS: a sequence whose offsets are negative,
  * descending or beyond total is skipped), read and cleared by dfssm_ssm_read_error; nothing else is kept

@@ -341,6 +341,25 @@ def test_a_sequence_that_is_not_finite_leaves_the_others_alone():
         assert torch.equal(r[k][rest], r2[k][rest])
 
 
+@pytest.mark.parametrize("lens", [[200, 30], [700, 30]])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_no_finite_value_is_wrong_beside_one_that_is_not(lens, bad):
+    """An entry of x, b or c that is not finite: what is finite in the results is what it was without it."""
+    a = inputs(15, lens, 2, 1, True)
+    y, fin, _ = run_fwd(a)
+    r, _ = run_bwd(a)
+    for col in (3, 2 * P + 5, 2 * P + N + 7):          # x of head 0, b, c
+        e = {**a, "row": a["row"].clone()}
+        e["row"][100, col] = bad
+        y2, fin2, _ = run_fwd(e)
+        r2, _ = run_bwd(e)
+        torch.cuda.synchronize()
+        for u, v in [(y, y2), (fin, fin2)] + [(r[k], r2[k]) for k in r]:
+            kept = torch.isfinite(v)
+            assert torch.isfinite(u).all() and torch.equal(u[kept], v[kept])
+        assert not torch.isfinite(y2[100]).all() and torch.isfinite(y2[lens[0]:]).all()
+
+
 def test_gradient_against_differences():
     """sum(dy y) + <dfinal, final> of the 64-bit recurrence along random directions of every input."""
     a = inputs(12, [70], 2, 1, True, 0, (0.01, 0.1))
