@@ -1,22 +1,21 @@
-// The state operations' recurrence over packed sequences of any length (dfssm_ssm_scan_fwd): what
-// ssm_step.cu does for one token, for the tokens of a prompt or a training batch.
+// The state operations' recurrence over packed sequences of any length (dfssm_ssm_scan_fwd): what ssm_step.cu does for one
+// token, for the tokens of a prompt or a training batch. This file has the work table, the forward kernel of short
+// calls, the kernels that carry states alone through a sequence, and the call's plan; ssm_scan_tc.cu has the forward
+// kernel of long calls, ssm_scan_bwd.cu the gradient.
 //
-// A CTA of 4 warps takes one head through one item (a sequence, or a segment of a long one), chunk by
-// chunk (ssm_scan.cuh has the formulas), with the head's 64 x 128 state in registers: warp w owns the
-// channels 16 w .. 16 w + 15, whose accumulator registers are at the same time the B fragments of the
-// state's readout. Per chunk, on bf16 warp MMAs with fp32 accumulation:
-//   G = C B^T (64 x 64, causal tiles only, warp w the rows 16 w ..), scaled to M = G exp(cum_t -
-//       cum_s) dt_s and stored as two bf16 parts (2^-17 of each value) for all warps;
-//   y = exp(cum_t) (C S^T) + M X + d_skip x, S as two bf16 parts: one rounding to bf16 at the end
-//       that counts;
-//   S = exp(cum_64) S + sum_s (w_s x_s) B_s^T, w_s x_s as three bf16 parts: the state, which
-//       goes on to the next tokens and is returned, keeps fp32's precision.
-// x, B and C are bf16 and enter exactly. The next chunk's tiles arrive by cp.async meanwhile.
+// A CTA takes one head through one item (a sequence, or a segment of a long one), chunk by chunk (ssm_scan.cuh has the
+// formulas), with the head's 64 x 128 state in fp32 registers. One CTA per (head, item) fills the GPU from about five
+// sequences of 64 heads on; with fewer, sequences longer than 1.25 times a CTA's fair share are cut into
+// segments, whose start states come from two small kernels before (each segment's own contribution, state products
+// only; then a carry over the segments). Items are handed out longest first.
 //
-// One CTA per (head, item) fills the GPU from about five sequences of 64 heads on; with fewer, sequences
-// longer than 1.25 times a CTA's fair share are cut into segments, whose start states come from two
-// small kernels before (each segment's own contribution, state MMAs only; then a carry over the
-// segments). Items are handed out longest first.
+// Operands are fp16 under power-of-two scales: x, B and C (bf16) enter exactly over 2^17 and more of range below their
+// chunk's largest value; M = G exp(cum_t - cum_s) dt_s and the state as the readout's operand are one fp16 number
+// each (2^-12 of the value, beside the output's own 2^-9); the weighted x that goes into the state is two (2^-23),
+// so that the state, which goes on to the next tokens and is returned, keeps fp32's precision.
+//
+// Short calls (scan_fwd_kernel, warp MMAs, chunks of 64 tokens) are one launch that converts its tiles itself. What a call of a few tokens costs is one launch, one chunk's chain of
+// loads, products and exchanges, and the states: 8.8 us for one sequence of 1 to 16 tokens, 15 us for 128.
 #include <mutex>
 
 #include "ssm_scan.cuh"
@@ -238,8 +237,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
     const int64_t sh = ((int64_t)it.seq * a.nheads + h) * kStateElems;
     const int s_at = (16 * pw + (lane >> 2)) * kN + 64 * hv + 2 * (lane & 3);
     {
-        const float* src = it.flags & kCut ? a.seg_state + ((int64_t)it.slot * a.nheads + h) * kStateElems
-                                           : a.init ? a.init + sh : nullptr;
+        const float* src = a.init ? a.init + sh : nullptr;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float2 lo = make_float2(0.0f, 0.0f), hi = lo;
@@ -510,7 +508,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
         }
     }
     ptx::cp_async_wait<0>();
-    if (o.final_state && (it.flags & kLast)) {
+    if (o.final_state) {
         float* dst = o.final_state + sh + s_at;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -742,8 +740,13 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
 
 // ------------------------------------------------------------------------------- host
 
-// Forward calls of up to this many tokens take the warp-MMA kernel in one launch.
-constexpr int kDirectTokens = 512;
+// Forward calls whose sequences have at most kDirectMean tokens on average take the warp-MMA kernel in one launch, where
+// even one sequence holding all the tokens is not long (kDirectTokens), or not long beside the work there is. Measured,
+// sequences x tokens, 64 heads, one launch against tensor cores behind table and tiles (us): 1 x 1 8.8 / 16.9,
+// 1 x 128 14.8 / 18.2, 1 x 256 25.5 / 20.8, 1 x 512 47 / 27.5, 2 x 256 25.6 / 21.6, 4 x 128 21.2 / 27.2, 4 x 256 36.9 / 36.1,
+// 16 x 64 43 / 81, 128 x 8 310 / 512.
+constexpr int kDirectMean = 128;
+constexpr int kDirectTokens = 1024;
 
 Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     Plan p{};
@@ -754,7 +757,8 @@ Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     p.seg_len = (int)((share + 127) / 128 * 128);
     if (p.seg_len > (total + 127) / 128 * 128) p.seg_len = (total + 127) / 128 * 128;
     // short calls save the launches of the table and of the tiles: every sequence is one item, in the order given
-    p.direct = !backward && total <= kDirectTokens;
+    p.direct = !backward && total <= (int64_t)kDirectMean * nseq &&
+               (total <= kDirectTokens || total <= (int64_t)nseq * nheads / 2);
     p.chunk = backward ? kQ : 128;
     p.cap_items = total / p.seg_len + nseq;
     p.cap_chunks = total / p.chunk + nseq;

@@ -256,7 +256,8 @@ def test_backward(lens, nh, ng, init, gap):
 
 @pytest.mark.parametrize("lens,nh,ng,init,gap", [([513], 1, 1, False, 0), ([128, 129, 0, 1, 127, 256], 4, 2, True, 5),
                                                  ([640], 3, 1, True, 1), ([2] * 300, 2, 2, False, 0),
-                                                 ([0, 0, 600, 0], 2, 1, True, 600)])
+                                                 ([0, 0, 600, 0], 2, 1, True, 600), ([1000] + [1] * 7, 2, 1, True, 0),
+                                                 ([40] * 40, 80, 1, True, 0), ([41] * 40, 80, 1, False, 0)])
 def test_forward_of_long_calls(lens, nh, ng, init, gap):
     a = inputs(len(lens) * 100 + nh + 2, lens, nh, ng, init, gap)
     y, fin, ws = run_fwd(a)
