@@ -4,18 +4,19 @@
 // kernel of long calls, ssm_scan_bwd.cu the gradient.
 //
 // A CTA takes one head through one item (a sequence, or a segment of a long one), chunk by chunk (ssm_scan.cuh has the
-// formulas), with the head's 64 x 128 state in fp32 registers. One CTA per (head, item) fills the GPU from about five
-// sequences of 64 heads on; with fewer, sequences longer than 1.25 times a CTA's fair share are cut into
-// segments, whose start states come from two small kernels before (each segment's own contribution, state products
-// only; then a carry over the segments). Items are handed out longest first.
+// formulas), with the head's 64 x 128 state in fp32 registers. One CTA per (head, item) fills the GPU from two or three
+// sequences of 64 heads on; with fewer, long sequences are cut into segments, whose start states come from two
+// small kernels before (each segment's own contribution, state products only; then a carry over the segments).
+// Items are handed out longest first.
 //
 // Operands are fp16 under power-of-two scales: x, B and C (bf16) enter exactly over 2^17 and more of range below their
 // chunk's largest value; M = G exp(cum_t - cum_s) dt_s and the state as the readout's operand are one fp16 number
-// each (2^-12 of the value, beside the output's own 2^-9); the weighted x that goes into the state is two (2^-23),
+// each (2^-11 of the value, beside the output's own 2^-8); the weighted x that goes into the state is two (2^-23),
 // so that the state, which goes on to the next tokens and is returned, keeps fp32's precision.
 //
-// Short calls (scan_fwd_kernel, warp MMAs, chunks of 64 tokens) are one launch that converts its tiles itself. What a call of a few tokens costs is one launch, one chunk's chain of
-// loads, products and exchanges, and the states: 8.8 us for one sequence of 1 to 16 tokens, 15 us for 128.
+// Short calls (scan_fwd_kernel, warp MMAs, chunks of 64 tokens) are one launch that converts its tiles itself. What a
+// call of a few tokens costs is one launch, one chunk's chain of loads, products and exchanges, and the
+// states: 64 heads, 8.8 us for one sequence of 1 to 16 tokens, 15 us for 128.
 #include <mutex>
 
 #include "ssm_scan.cuh"
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
                 atomicOr(a.err, DFSSM_DEVERR_SEQLENS);
             } else {
                 len = t1 - t0;
-                nseg = len <= a.seg_len ? 1 : (len + a.seg_len - 1) / a.seg_len;
+                nseg = len <= a.cut_at ? 1 : (len + a.seg_len - 1) / a.seg_len;
                 nch = (len + a.chunk - 1) / a.chunk;
             }
         }
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
             } else {
                 for (int k = 0; k < nseg; ++k) {
                     const int at = k * a.seg_len;
-                    a.seq_items[i0 + k] = Item{s, t0 + at, min(a.seg_len, len - at), c0 + at / a.chunk, s1 - cut + k,
+                    a.seq_items[i0 + k] = Item{s, t0 + at, nseg == 1 ? len : min(a.seg_len, len - at), c0 + at / a.chunk, s1 - cut + k,
                                                (k == 0 ? kFirst : 0) | (k == nseg - 1 ? kLast : 0) | (nseg > 1 ? kCut : 0)};
                 }
             }
@@ -750,12 +751,15 @@ constexpr int kDirectTokens = 1024;
 
 Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     Plan p{};
-    // a CTA's fair share: two CTAs on each of 148 SMs; an item may be a quarter longer
-    int64_t share = ((int64_t)total * nheads + 295) / 296;
-    share += share / 4;
-    if (share < 512) share = 512;                          // 512 tokens at least
+    // A segment is a CTA's fair share of 148 CTAs (backward: 296, for two directions), 512 tokens at least. A sequence
+    // is cut where that saves time: what is left of it after the first segment takes 34 ns a token, the cut
+    // 16 ns a token of a segment (the states of all segments but one, beforehand) and about 20 us of launches.
+    // Measured, uncut / cut, forward: 1 x 2,048 tokens, 64 heads 72 / 81 us, 1 x 1,500 54 / 62; 8 heads 72 / 49.
+    int64_t share = ((int64_t)total * nheads + 147) / 148;
+    if (share < 512) share = 512;
     p.seg_len = (int)((share + 127) / 128 * 128);
     if (p.seg_len > (total + 127) / 128 * 128) p.seg_len = (total + 127) / 128 * 128;
+    p.cut_at = p.seg_len + p.seg_len / 4 * 3 + 640;
     // short calls save the launches of the table and of the tiles: every sequence is one item, in the order given
     p.direct = !backward && total <= (int64_t)kDirectMean * nseq &&
                (total <= kDirectTokens || total <= (int64_t)nseq * nheads / 2);
@@ -775,7 +779,7 @@ Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward) {
     const size_t slots = (backward ? 2 : 1) * (size_t)p.cap_slots * nheads;
     p.seg_decay = o;   o = up256(o + 4 * slots);
     p.seg_state = o;
-    if (total > p.seg_len) o = up256(o + 4 * slots * kStateElems);
+    if (total > p.cut_at) o = up256(o + 4 * slots * kStateElems);
     p.total = o;
     return p;
 }
@@ -800,6 +804,7 @@ Args make_args(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int tot
     a.total = total;
     a.nseq = nseq;
     a.seg_len = p.seg_len;
+    a.cut_at = p.cut_at;
     a.direct = p.direct;
     a.chunk = p.chunk;
     a.cap_items = p.cap_items;
@@ -875,7 +880,7 @@ cudaError_t launch_table(const Args& a, cudaStream_t s) {
 }
 
 cudaError_t launch_segment_starts(const Args& a, const StateArgs& o, int directions, cudaStream_t s) {
-    if (a.total <= a.seg_len) return cudaSuccess;          // no sequence can be cut
+    if (a.total <= a.cut_at) return cudaSuccess;           // no sequence can be cut
     scan_state_kernel<false><<<dim3(a.cap_items * a.nheads, directions), 256, kStateSmem, s>>>(a, o);
     scan_carry_kernel<<<dim3(a.nseq * a.nheads, directions), 256, 0, s>>>(a, a.init, o.dfinal);
     return cudaGetLastError();

@@ -57,7 +57,8 @@ struct Args {
     const int32_t* cu;
     int nheads, per_group;             // heads; heads per group
     int total, nseq;
-    int seg_len;                       // longest item (a multiple of the chunk)
+    int seg_len;                       // tokens of a segment (a multiple of the chunk)
+    int cut_at;                        // sequences longer than this are cut into segments
     int chunk;                         // tokens per chunk of the table: 64, or 128 for the tensor-core forward
     int direct;                        // 1: no table, item i is sequence i
     int cap_items, cap_chunks, cap_slots;
@@ -234,7 +235,7 @@ __device__ __forceinline__ float raw_dt(const Args& a, int t0, int n, int h, int
 
 // ---- host side: the call's plan and workspace
 struct Plan {
-    int seg_len, chunk, direct, cap_items, cap_chunks, cap_slots;
+    int seg_len, cut_at, chunk, direct, cap_items, cap_chunks, cap_slots;
     size_t count, items, seq_items, seq_slots, chunks, tiles, tile_scale, seg_state, seg_decay, total;
 };
 Plan make_plan(int nheads, int ngroups, int total, int nseq, bool backward);

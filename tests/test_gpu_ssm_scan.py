@@ -266,7 +266,7 @@ def test_forward_of_long_calls(lens, nh, ng, init, gap):
     assert dfssm.dfssm_ssm_read_error(ptr(ws), stream()) == (dfssm.DFSSM_OK, 0)
 
 
-@pytest.mark.parametrize("lens", [[1500], [700, 513, 512, 1100, 64]])
+@pytest.mark.parametrize("lens", [[1500], [700, 513, 512, 1100, 64], [1537, 1536, 3, 2600], [4000]])
 def test_sequences_that_are_cut_into_segments(lens):
     a = inputs(5, lens, 2, 1, True, 7)
     y, fin, _ = run_fwd(a)
