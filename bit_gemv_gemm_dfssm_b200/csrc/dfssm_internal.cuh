@@ -216,4 +216,21 @@ __device__ __forceinline__ float bf16_bits_to_float(uint32_t b16) {
     return __uint_as_float(b16 << 16);
 }
 
+// Launch that may begin while the launch before it in the stream still runs; the kernel waits (pdl_wait) before it
+// touches what that one reads or writes.
+template <typename... K, typename... A>
+inline cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
+}
+
 }  // namespace dfssm

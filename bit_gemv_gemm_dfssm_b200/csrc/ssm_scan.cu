@@ -56,6 +56,7 @@ __device__ __forceinline__ int block_scan(int v, int* red, int& total) {
 __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a) {
     __shared__ int red[kTableThreads / 32];
     __shared__ int lens[kMaxSorted];
+    ptx::pdl_launch_dependents();
     int n_items = 0, n_chunks = 0, n_slots = 0;
     for (int s0 = 0; s0 < a.nseq; s0 += kTableThreads) {
         const int s = s0 + threadIdx.x;
@@ -142,6 +143,8 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
 // CTA (chunk, group, C or B): the tile, rows behind the chunk's tokens as zeros
 __global__ void __launch_bounds__(512) scan_tiles_kernel(const Args a) {
     __shared__ uint32_t red[16];
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
     const int ngroups = a.nheads / a.per_group;
     const int side = blockIdx.x & 1, g = (blockIdx.x >> 1) % ngroups, ci = (blockIdx.x >> 1) / ngroups;
     if (ci >= a.count[1]) return;
@@ -527,6 +530,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
 // CTA (sequence, head), y: 0 forward in time, 1 backward (from the last segment to the first).
 __global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const float* __restrict__ init,
                                                          const float* __restrict__ dfinal) {
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
     const int h = blockIdx.x % a.nheads, s = blockIdx.x / a.nheads, rev = blockIdx.y;
     const int i0 = a.seq_slots[s].x, i1 = i0 + a.seq_slots[s].y;
     if (i1 - i0 < 2) return;
@@ -569,6 +574,7 @@ template <bool STORE>
 __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const StateArgs o) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Decay scratch_of[8];
+    ptx::pdl_launch_dependents();
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, pw = w & 3, hv = w >> 2;
@@ -875,19 +881,21 @@ dfssm_status setup() {
 
 cudaError_t launch_table(const Args& a, cudaStream_t s) {
     scan_table_kernel<<<1, kTableThreads, 0, s>>>(a);
-    scan_tiles_kernel<<<2 * a.cap_chunks * (a.nheads / a.per_group), 512, 0, s>>>(a);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_after(scan_tiles_kernel, 2 * a.cap_chunks * (a.nheads / a.per_group), 512, 0, s, a);
 }
 
 cudaError_t launch_segment_starts(const Args& a, const StateArgs& o, int directions, cudaStream_t s) {
     if (a.total <= a.cut_at) return cudaSuccess;           // no sequence can be cut
+    // not launch_after: CTAs that come in beside the tiles' are packed two to an SM where one to an SM would do
+    // (16,384 tokens, 64 heads: 477 us, with it 597)
     scan_state_kernel<false><<<dim3(a.cap_items * a.nheads, directions), 256, kStateSmem, s>>>(a, o);
-    scan_carry_kernel<<<dim3(a.nseq * a.nheads, directions), 256, 0, s>>>(a, a.init, o.dfinal);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_after(scan_carry_kernel, dim3(a.nseq * a.nheads, directions), 256, 0, s, a, a.init, o.dfinal);
 }
 
 cudaError_t launch_states(const Args& a, const StateArgs& o, cudaStream_t s) {
-    cudaError_t e = launch_segment_starts(a, o, 2, s);
+    const cudaError_t e = launch_segment_starts(a, o, 2, s);
     if (e != cudaSuccess) return e;
     scan_state_kernel<true><<<dim3(a.cap_items * a.nheads, 2), 256, kStateSmem, s>>>(a, o);
     return cudaGetLastError();

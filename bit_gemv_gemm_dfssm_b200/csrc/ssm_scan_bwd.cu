@@ -78,6 +78,8 @@ __device__ __forceinline__ void load_state_tiles(uint32_t dst, const uint16_t* s
 
 __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, const GradArgs o) {
     extern __shared__ uint8_t smem_raw[];
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
     const uint32_t s_b = base, s_c = base + 16384, s_t = base + 32768, s_m = s_t + 2 * kTile;
@@ -503,6 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
 __global__ void __launch_bounds__(256) scan_sum_kernel(const Args a, const float* __restrict__ db_part,
                                                        const float* __restrict__ dc_part, int splits, uint16_t* db,
                                                        int64_t lddb, uint16_t* dc, int64_t lddc) {
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
     if ((int)(blockIdx.x >> 3) >= a.count[1]) return;
     const Chunk ch = a.chunks[blockIdx.x >> 3];
     const int cols = a.nheads / a.per_group * kN, per = cols / 4;
@@ -526,6 +530,7 @@ __global__ void __launch_bounds__(256) scan_sum_kernel(const Args a, const float
 __global__ void __launch_bounds__(256) scan_params_kernel(const Args a, const float* __restrict__ sums, float* ddt_bias,
                                                           float* da_log, float* dd_skip) {
     __shared__ float4 red[8];
+    ptx::pdl_wait();
     const int h = blockIdx.x, n = a.count[1];
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i = threadIdx.x; i < n; i += 256) {
@@ -651,10 +656,10 @@ extern "C" dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const df
     const StateArgs st_args{o.dy, dy_stride, dfinal_state, s_in, ds, gr->dinit_state};
     if (launch_table(a, s) != cudaSuccess || launch_states(a, st_args, s) != cudaSuccess)
         return DFSSM_ERR_CUDA;
-    scan_grad_kernel<<<p.cap_chunks * dims->ngroups * sp.splits, kThreads, kGradSmem, s>>>(a, o);
-    scan_sum_kernel<<<dim3(8 * p.cap_chunks, 2), 256, 0, s>>>(a, o.db_part, o.dc_part, sp.splits,
-                                                          static_cast<uint16_t*>(gr->db), gr->db_stride,
-                                                          static_cast<uint16_t*>(gr->dc), gr->dc_stride);
-    scan_params_kernel<<<dims->nheads, 256, 0, s>>>(a, o.sums, gr->ddt_bias, gr->da_log, gr->dd_skip);
-    return cudaGetLastError() == cudaSuccess ? DFSSM_OK : DFSSM_ERR_CUDA;
+    if (launch_after(scan_grad_kernel, p.cap_chunks * dims->ngroups * sp.splits, kThreads, kGradSmem, s, a, o) != cudaSuccess ||
+        launch_after(scan_sum_kernel, dim3(8 * p.cap_chunks, 2), 256, 0, s, a, o.db_part, o.dc_part, sp.splits,
+                     static_cast<uint16_t*>(gr->db), gr->db_stride, static_cast<uint16_t*>(gr->dc), gr->dc_stride) != cudaSuccess ||
+        launch_after(scan_params_kernel, dims->nheads, 256, 0, s, a, o.sums, gr->ddt_bias, gr->da_log, gr->dd_skip) != cudaSuccess)
+        return DFSSM_ERR_CUDA;
+    return DFSSM_OK;
 }

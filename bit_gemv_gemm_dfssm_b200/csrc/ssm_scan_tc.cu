@@ -75,6 +75,7 @@ constexpr uint32_t kIdescD = kIdescBase | ((uint32_t)(64 >> 3) << 17) | (1u << 1
 __global__ void __launch_bounds__(kTcThreads, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_x, const TcArgs p) {
     extern __shared__ uint8_t smem_raw[];
+    ptx::pdl_wait();                                 // the work table, the tiles, the segments' starts
     const Args& a = p.a;
     const int ngroups = a.nheads / a.per_group;
     const int h = blockIdx.x % a.nheads, g = h / a.per_group;
@@ -589,8 +590,7 @@ cudaError_t launch_tc(const Args& a, uint16_t* y, int64_t ldy, float* final_stat
         !encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, (int64_t)a.nheads * kP, a.total, a.ldx))
         return cudaErrorInvalidValue;
     TcArgs p{a, y, ldy, final_state};
-    scan_tc_kernel<<<a.cap_items * a.nheads, kTcThreads, kTcSmem, s>>>(mt, mx, p);
-    return cudaGetLastError();
+    return launch_after(scan_tc_kernel, a.cap_items * a.nheads, kTcThreads, kTcSmem, s, mt, mx, p);
 }
 
 }  // namespace scan

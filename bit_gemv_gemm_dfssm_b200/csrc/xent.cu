@@ -875,23 +875,6 @@ dfssm_status xent_setup(int* sm_count) {
     return DFSSM_OK;
 }
 
-// Launch that may begin while the launch before it in the stream still runs; the kernel waits (pdl_wait) before it
-// touches what that one reads or writes.
-template <typename... K, typename... A>
-cudaError_t launch_after(void (*kernel)(K...), int grid, int threads, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
-}
-
 dfssm_status check_xent(const dfssm_int8_table* t, int32_t m) {
     if (!t || !t->table || !t->scale || !al16(t->table) || !al16(t->scale)) return DFSSM_ERR_INVALID_ARG;
     if (t->d < 16 || t->d > kMaxDIn || t->d % 16 != 0 || t->vocab < 1 || t->vocab > (1 << 24))
