@@ -136,10 +136,6 @@ struct FwdOut {
 
 constexpr int kTileTop = 3;
 
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
-    return f16x2_of(__fmul_rn(bf16_lo(v), scale), __fmul_rn(bf16_hi(v), scale));
-}
-
 // CTA (chunk, group, C or B): the tile, rows behind the chunk's tokens as zeros
 __global__ void __launch_bounds__(512) scan_tiles_kernel(const Args a) {
     __shared__ uint32_t red[16];
@@ -562,10 +558,11 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const flo
 // 16 pw .. and the states 64 hv .. in fp32 accumulators. v comes in fp16 (scan_tiles_kernel), the weighted u enters
 // as two fp16 parts under a power-of-two scale of the warp's channels.
 struct StateDecay {
-    float wt[kQ];        // the weights of u
+    float wt[kQ];        // the weights of u, the largest in [1/2, 1)
     float keep;          // exp(cum_64)
     float cum;           // cum_64
-    float pad[2];
+    float kd;            // 2^-k of the weights
+    float pad;
 };
 constexpr int kStTile = 16384 + 8192;                                    // v, u
 constexpr int kStateSmem = 2 * kStTile + 8 * 2048 + 16 * (int)sizeof(StateDecay) + 128;
@@ -574,6 +571,7 @@ template <bool STORE>
 __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const StateArgs o) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Decay scratch_of[8];
+    __shared__ uint32_t s_max[2][8], u_max[2][8];    // the warps' largest |S| and |u|
     ptx::pdl_launch_dependents();
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
     uint8_t* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
@@ -641,14 +639,31 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
             const float2 dt = reinterpret_cast<const float2*>(scratch.dt)[lane];
             wt = make_float2(__fmul_rn(wt.x, dt.x), __fmul_rn(wt.y, dt.y));
         }
+        // the largest weight to [1/2, 1): what a fast decay leaves keeps its bits
+        const float2 sc = pow2_scale(__reduce_max_sync(0xffffffffu, max(__float_as_uint(wt.x), __float_as_uint(wt.y))), -1);
+        wt = make_float2(__fmul_rn(wt.x, sc.x), __fmul_rn(wt.y, sc.x));
         reinterpret_cast<float2*>(d.wt)[lane] = wt;
         if (lane == 0) {
             d.keep = scratch.done[kQ - 1];
             d.cum = scratch.cum[kQ - 1];
+            d.kd = sc.y;
         }
     };
     raws(w);
     decay(w);
+    auto largest = [&](int k) {                 // of S, for the chunk k behind it
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = fmaxf(m, fabsf(S[j][q]));
+        const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0) s_max[k & 1][w] = mb;
+    };
+    auto all_max = [](const uint32_t* m) { return max(max(max(m[0], m[1]), max(m[2], m[3])), max(max(m[4], m[5]), max(m[6], m[7]))); };
+    // the scales of the gradient kernel: its chunk of u (once all warps have seen it) and the state
+    auto scale_of = [&](int k) { return o.scale + ((int64_t)(it.chunk0 + chunk_of(k)) * a.nheads + h) * 4 + (rev ? 1 : 0); };
+    if (STORE) largest(0);
     for (int k = 0; k < n_ch; ++k) {
         const uint32_t s_v = base + (k & 1) * kStTile, s_u = s_v + 16384;
         const StateDecay& d = dec[k & 15];
@@ -659,8 +674,13 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
         if ((k & 7) == 4) decay((k & ~7) + 8 + w);
         const float2 tsc = a.tile_scale[tile_at(chunk_of(k))];
         if (STORE) {
-            // the warp's 16 rows x 64 states as bf16 high and low parts (2^-17 of each value), staged so that whole
-            // 128-byte rows go out
+            // the warp's 16 rows x 64 states as fp16 high and low parts (2^-23 of each value) under a power-of-two scale of
+            // the whole state, staged so that whole 128-byte rows go out
+            const float2 ss = pow2_scale(all_max(s_max[k & 1]), 13);
+            if (tid == 0) {
+                scale_of(k)[2] = ss.y;
+                if (k > 0) scale_of(k - 1)[0] = pow2_scale(all_max(u_max[(k - 1) & 1]), 13).y;
+            }
             uint16_t* dst = (rev ? o.dstates : o.states) +
                             ((int64_t)(it.chunk0 + chunk_of(k)) * a.nheads + h) * 2 * kStateElems + 16 * pw * kN + 64 * hv;
 #pragma unroll
@@ -671,7 +691,7 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
                     uint32_t q[4], lo;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        split_bf16x2(S[j + (i >> 1)][2 * (i & 1)], S[j + (i >> 1)][2 * (i & 1) + 1], q[i], lo);
+                        split_f16x2(__fmul_rn(S[j + (i >> 1)][2 * (i & 1)], ss.x), __fmul_rn(S[j + (i >> 1)][2 * (i & 1) + 1], ss.x), q[i], lo);
                         if (part) q[i] = lo;
                     }
                     const int mi = lane >> 3;    // rows 0..7 and 8..15 of tile j, then of tile j + 1
@@ -687,36 +707,32 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
                 }
             }
         }
-        // the scale of the weighted u, from its largest value: what a fast decay leaves keeps its bits
         uint32_t um = 0u;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            const float2 w0 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 2 * (lane & 3));
-            const float2 w1 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 8 + 2 * (lane & 3));
             uint32_t ua[4];
             frag_at<128>(s_u, 16 * ks, 16 * pw, lane, ua);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 ww = q < 2 ? w0 : w1;
-                um = max(um, max(__float_as_uint(fabsf(__fmul_rn(bf16_lo(ua[q]), ww.x))),
-                                 __float_as_uint(fabsf(__fmul_rn(bf16_hi(ua[q]), ww.y)))));
-            }
+            for (int q = 0; q < 4; ++q) um = abs_max_bf16x2(um, ua[q]);
         }
-        const float2 us = pow2_scale(__reduce_max_sync(0xffffffffu, um), 13);
+        um = __reduce_max_sync(0xffffffffu, um);
+        const float2 us = pow2_scale(um, 13);
+        if (STORE && lane == 0) u_max[k & 1][w] = um;
         float D[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j) D[j][0] = D[j][1] = D[j][2] = D[j][3] = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            const float2 w0 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 2 * (lane & 3));
-            const float2 w1 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 8 + 2 * (lane & 3));
+            float2 w0 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 2 * (lane & 3));
+            float2 w1 = *reinterpret_cast<const float2*>(d.wt + 16 * ks + 8 + 2 * (lane & 3));
+            w0 = make_float2(__fmul_rn(w0.x, us.x), __fmul_rn(w0.y, us.x));
+            w1 = make_float2(__fmul_rn(w1.x, us.x), __fmul_rn(w1.y, us.x));
             uint32_t ua[4], hi[4], lo[4];
             frag_at<128>(s_u, 16 * ks, 16 * pw, lane, ua);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float2 ww = q < 2 ? w0 : w1;
-                split_f16x2(__fmul_rn(__fmul_rn(bf16_lo(ua[q]), ww.x), us.x), __fmul_rn(__fmul_rn(bf16_hi(ua[q]), ww.y), us.x),
-                            hi[q], lo[q]);
+                split_f16x2(__fmul_rn(bf16_lo(ua[q]), ww.x), __fmul_rn(bf16_hi(ua[q]), ww.y), hi[q], lo[q]);
             }
             uint32_t bb[4][4];
 #pragma unroll
@@ -727,13 +743,18 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
             for (int q = 0; q < 8; ++q) mma_h(D[q], hi, bb[q >> 1][2 * (q & 1)], bb[q >> 1][2 * (q & 1) + 1]);
         }
         total = __fadd_rn(total, d.cum);
-        const float keep = d.keep, back = __fmul_rn(rev ? tsc.x : tsc.y, us.y);
+        const float keep = d.keep, back = __fmul_rn(__fmul_rn(rev ? tsc.x : tsc.y, d.kd), us.y);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) S[j][q] = __fmaf_rn(D[j][q], back, __fmul_rn(S[j][q], keep));
+        if (STORE) largest(k + 1);
     }
     ptx::cp_async_wait<0>();
+    if (STORE && n_ch > 0) {
+        __syncthreads();
+        if (tid == 0) scale_of(n_ch - 1)[0] = pow2_scale(all_max(u_max[(n_ch - 1) & 1]), 13).y;
+    }
     float* dst = !STORE ? a.seg_state + slot * kStateElems : rev && o.dinit && (it.flags & kFirst) ? o.dinit + sh : nullptr;
     if (dst) {
 #pragma unroll

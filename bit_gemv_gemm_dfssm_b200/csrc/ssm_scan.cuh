@@ -152,6 +152,9 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float scale) {
+    return f16x2_of(__fmul_rn(bf16_lo(v), scale), __fmul_rn(bf16_hi(v), scale));
+}
 // (a, b) as two fp16 pairs whose sum is (a, b) to 2^-23 of each (or to 2^-25 below fp16's normal range)
 __device__ __forceinline__ void split_f16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -250,6 +253,7 @@ struct StateArgs {
     const float* dfinal;       // [nseq][H][64][128] gradient of the final states, or NULL
     uint16_t* states;          // [chunks][H][2][64][128]: the state in front of every chunk
     uint16_t* dstates;         // the same: the gradient of the state behind it
+    float* scale;              // [chunks][H][4] 2^-k of x, dy, the states, their gradients
     float* dinit;              // [nseq][H][64][128] gradient of the initial states, or NULL
 };
 // the start states of the segments of cut sequences (nothing to do when none can be cut); directions 2: of their

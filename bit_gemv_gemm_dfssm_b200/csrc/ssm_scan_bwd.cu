@@ -34,8 +34,9 @@ constexpr int kThreads = 512;
 struct GradArgs {
     const uint16_t* dy;
     int64_t lddy;
-    const uint16_t* s_in;      // [chunks][H][2][64][128] states in front of the chunks
+    const uint16_t* s_in;      // [chunks][H][2][64][128] states in front of the chunks, fp16 high and low part
     const uint16_t* ds_out;    // the same: gradients behind them
+    const float4* scale;       // [chunks][H] 2^-k of x, dy, the states, the gradients
     uint16_t* dx;
     int64_t lddx;
     uint16_t* ddt;
@@ -53,13 +54,15 @@ constexpr int kTx = 0, kTy = 8192, kTs = 16384, kTd = 16384 + 32768, kTile = 163
 struct HeadDecay {
     Decay d;
     float sig[kQ];             // d softplus
+    float4 scale;              // 2^-k of x, dy, S, dS
 };
 // a head's partial sums, read one head behind: two of them
 struct HeadSums {
     float wl[4][kQ];           // x . dx' of the four channel slices, of the part that leaves the chunk
     float z[4][kQ];            // C . (dy S) of the four state slices
-    float row[4][kQ];          // sums of E over s, per block of 16 s
-    float col[4][kQ];          // sums of M o Z over t, per block of 16 t
+    float row[4][kQ];          // sums of E over s < t, per block of 16 s
+    float col[4][kQ];          // sums of M o Z over t > s, per block of 16 t
+    float own[kQ];             // M o Z at t = s
     float skip[kQ];            // dy . x
     float dot[kThreads];       // <dS, S>
 };
@@ -78,6 +81,7 @@ __device__ __forceinline__ void load_state_tiles(uint32_t dst, const uint16_t* s
 
 __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, const GradArgs o) {
     extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t wmax[kThreads / 32];
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     const uint32_t base = (ptx::smem_u32(smem_raw) + 127u) & ~127u;
@@ -110,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         HeadDecay& v = decays[(h - h0) % 3];
         const float bias = a.dt_bias[h], a2 = __fmul_rn(-expf(a.a_log[h]), kLog2e);
         const float r0 = raw_dt(a, t0, n, h, 2 * lane), r1 = raw_dt(a, t0, n, h, 2 * lane + 1);
+        if (lane == 0) v.scale = o.scale[(int64_t)ci * a.nheads + h];
         chunk_decay(v.d, r0, r1, n, bias, a2, lane);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             const int t = 2 * lane + i;
             const float leaves = __fadd_rn(__fadd_rn(v.wl[0][t], v.wl[1][t]), __fadd_rn(v.wl[2][t], v.wl[3][t]));
             const float col = __fadd_rn(__fadd_rn(v.col[0][t], v.col[1][t]), __fadd_rn(v.col[2][t], v.col[3][t]));
-            kp[i] = __fadd_rn(leaves, col);               // x . (dS B), all of it
+            kp[i] = __fadd_rn(__fadd_rn(leaves, col), v.own[t]);          // x . (dS B), all of it
             wl[i] = __fmul_rn(d.d.dt[t], leaves);
             const float z = __fmul_rn(d.d.done[t],
                                       __fadd_rn(__fadd_rn(v.z[0][t], v.z[1][t]), __fadd_rn(v.z[2][t], v.z[3][t])));
@@ -175,11 +180,31 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         if (lane == 0)
             *reinterpret_cast<float4*>(o.sums + ((int64_t)ci * a.nheads + h) * 4) = make_float4(sb, sa, sk, 0.0f);
     };
-    load_tile<128, kThreads>(s_b, a.b + (int64_t)g * kN, a.ldb, t0, n, tid);
-    load_tile<128, kThreads>(s_c, a.c + (int64_t)g * kN, a.ldc, t0, n, tid);
+    // x and dy of a head from bf16 to fp16 under their scales, in place
+    auto convert = [&](int h) {
+        const float4 sc = decays[(h - h0) % 3].scale;
+        const uint32_t st = s_t + ((h - h0) & 1) * kTile;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t at = tile128(st + (i ? kTy : kTx), tid >> 3, tid & 7);
+            const float up = __frcp_rn(i ? sc.y : sc.x);                  // a power of two: exact
+            const uint4 v = ptx::lds128(at);
+            const uint32_t q[4] = {bf16x2_to_f16x2(v.x, up), bf16x2_to_f16x2(v.y, up), bf16x2_to_f16x2(v.z, up),
+                                   bf16x2_to_f16x2(v.w, up)};
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]) : "memory");
+        }
+    };
+    static_assert(kThreads == kQ * kP / 8, "a piece per thread and tile");
+    const int64_t tl = (int64_t)ci * ngroups + g;
+    load_tile<128, kThreads>(s_c, a.tiles + tl * 2 * (128 * kN), kN, 0, kQ, tid);
+    load_tile<128, kThreads>(s_b, a.tiles + (tl * 2 + 1) * (128 * kN), kN, 0, kQ, tid);
+    const float2 kcb = a.tile_scale[tl];              // 2^-k of C, of B
+    const float kg = __fmul_rn(kcb.x, kcb.y);
     fetch(h0);
     if (w == 0) vectors(h0);
     ptx::cp_async_wait<0>();
+    __syncthreads();
+    convert(h0);
     __syncthreads();
 
     // G^T: warp (ws, wt) has rows s = 16 ws .., columns t = 16 wt ..; six of the sixteen have t < s everywhere
@@ -195,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             uint32_t ba[4], cb[4];
             frag_a<256>(s_b, 16 * ws, kk, lane, ba);
             frag_b<256>(s_c, 16 * wt, kk, lane, cb);
-            mma(G[0], ba, cb[0], cb[1]);
-            mma(G[1], ba, cb[2], cb[3]);
+            mma_h(G[0], ba, cb[0], cb[1]);
+            mma_h(G[1], ba, cb[2], cb[3]);
         }
     }
     // warps 0 .. 7 have dC, rows t, the others dB, rows s: 32 (w & 1) + 16 i .., columns 32 (w / 2 % 4) + 8 j ..
@@ -214,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         const uint32_t st = s_t + ((h - h0) & 1) * kTile;
         const uint32_t s_x = st + kTx, s_y = st + kTy, s_s = st + kTs, s_d = st + kTd;
         const Decay& dc = decays[(h - h0) % 3].d;
+        const float4& sc = decays[(h - h0) % 3].scale;
         HeadSums& v = sums[(h - h0) & 1];
         const float skip = a.d_skip[h];
         fetch(h + 1);                             // over the tiles of the head before, which all warps have left
@@ -231,11 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 uint32_t xa[4], yb[4];
                 frag_a<128>(s_x, 16 * ws, kk, lane, xa);
                 frag_b<128>(s_y, 16 * wt, kk, lane, yb);
-                mma(Z[0], xa, yb[0], yb[1]);
-                mma(Z[1], xa, yb[2], yb[3]);
+                mma_h(Z[0], xa, yb[0], yb[1]);
+                mma_h(Z[1], xa, yb[2], yb[3]);
             }
             const int s = 16 * ws + (lane >> 2);
             const float cs0 = dc.cum[s], cs1 = dc.cum[s + 8], ds0 = dc.dt[s], ds1 = dc.dt[s + 8];
+            const float kz = __fmul_rn(sc.x, sc.y), w0 = __fmul_rn(ds0, kz), w1 = __fmul_rn(ds1, kz), km = __fmul_rn(kz, kg);
             float col0 = 0.0f, col1 = 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -248,12 +275,19 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 l[3] = t + 1 >= s + 8 ? exp2f(__fsub_rn(ct.y, cs1)) : 0.0f;
                 const float m[4] = {__fmul_rn(G[j][0], l[0]), __fmul_rn(G[j][1], l[1]), __fmul_rn(G[j][2], l[2]),
                                     __fmul_rn(G[j][3], l[3])};
-                uint32_t m0, n0, m1, n1;
-                split_bf16x2(m[0], m[1], m0, n0);
-                split_bf16x2(m[2], m[3], m1, n1);
                 // the sums of E over the warp's s for the thread's two t, and of M o Z over the thread's t
-                const float mz[4] = {__fmul_rn(m[0], Z[j][0]), __fmul_rn(m[1], Z[j][1]), __fmul_rn(m[2], Z[j][2]),
+                float mz[4] = {__fmul_rn(m[0], Z[j][0]), __fmul_rn(m[1], Z[j][1]), __fmul_rn(m[2], Z[j][2]),
                                      __fmul_rn(m[3], Z[j][3])};
+                // the diagonal (where L = 1), kept apart: what enters at t leaves before it could decay
+                if (ws == wt) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (t + (q & 1) == s + 4 * (q & 2)) {
+                            v.skip[t + (q & 1)] = __fmul_rn(Z[j][q], kz);
+                            v.own[t + (q & 1)] = __fmul_rn(mz[q], km);
+                            mz[q] = 0.0f;
+                        }
+                }
                 col0 = __fadd_rn(col0, __fadd_rn(mz[0], mz[1]));
                 col1 = __fadd_rn(col1, __fadd_rn(mz[2], mz[3]));
                 float2 rs = make_float2(__fmaf_rn(mz[0], ds0, __fmul_rn(mz[2], ds1)), __fmaf_rn(mz[1], ds0, __fmul_rn(mz[3], ds1)));
@@ -262,21 +296,20 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                     rs.x = __fadd_rn(rs.x, __shfl_xor_sync(0xffffffffu, rs.x, q));
                     rs.y = __fadd_rn(rs.y, __shfl_xor_sync(0xffffffffu, rs.y, q));
                 }
-                if (lane < 4) *reinterpret_cast<float2*>(v.row[ws] + t) = rs;
-                if (t == s) v.skip[s] = Z[j][0];
-                if (t + 1 == s) v.skip[s] = Z[j][1];
-                if (t == s + 8) v.skip[s + 8] = Z[j][2];
-                if (t + 1 == s + 8) v.skip[s + 8] = Z[j][3];
+                if (lane < 4) *reinterpret_cast<float2*>(v.row[ws] + t) = make_float2(__fmul_rn(rs.x, km), __fmul_rn(rs.y, km));
                 const uint32_t p0 = tile128(s_m, s, 2 * wt + j) + 4 * (lane & 3);
                 const uint32_t p1 = tile128(s_m, s + 8, 2 * wt + j) + 4 * (lane & 3);
+                uint32_t m0, n0, m1, n1;
+                split_f16x2(m[0], m[1], m0, n0);
+                split_f16x2(m[2], m[3], m1, n1);
                 ptx::sts32(p0, m0);
                 ptx::sts32(p1, m1);
                 ptx::sts32(p0 + 8192, n0);
                 ptx::sts32(p1 + 8192, n1);
-                W[j][0] = __fmaf_rn(Z[j][0], __fmul_rn(l[0], ds0), W[j][0]);
-                W[j][1] = __fmaf_rn(Z[j][1], __fmul_rn(l[1], ds0), W[j][1]);
-                W[j][2] = __fmaf_rn(Z[j][2], __fmul_rn(l[2], ds1), W[j][2]);
-                W[j][3] = __fmaf_rn(Z[j][3], __fmul_rn(l[3], ds1), W[j][3]);
+                W[j][0] = __fmaf_rn(Z[j][0], __fmul_rn(l[0], w0), W[j][0]);
+                W[j][1] = __fmaf_rn(Z[j][1], __fmul_rn(l[1], w0), W[j][1]);
+                W[j][2] = __fmaf_rn(Z[j][2], __fmul_rn(l[2], w1), W[j][2]);
+                W[j][3] = __fmaf_rn(Z[j][3], __fmul_rn(l[3], w1), W[j][3]);
             }
 #pragma unroll
             for (int q = 1; q < 4; q <<= 1) {
@@ -284,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 col1 = __fadd_rn(col1, __shfl_xor_sync(0xffffffffu, col1, q));
             }
             if ((lane & 3) == 0) {
-                v.col[wt][s] = col0;
-                v.col[wt][s + 8] = col1;
+                v.col[wt][s] = __fmul_rn(col0, km);
+                v.col[wt][s + 8] = __fmul_rn(col1, km);
             }
         } else {
             if (lane < 8) *reinterpret_cast<float2*>(v.row[ws] + 16 * wt + 2 * lane) = make_float2(0.0f, 0.0f);
@@ -295,12 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         {
             const uint32_t s_u = side ? s_x : s_y, s_v = side ? s_d : s_s;
             float e[2][2], z[2][2];
+            const float kt = side ? __fmul_rn(sc.x, sc.w) : __fmul_rn(sc.y, sc.z);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const int r = rw + 16 * i + 8 * hf + (lane >> 2);
-                    e[i][hf] = side ? __fmul_rn(dc.dt[r], dc.left[r]) : dc.done[r];
+                    e[i][hf] = __fmul_rn(side ? __fmul_rn(dc.dt[r], dc.left[r]) : dc.done[r], kt);
                     z[i][hf] = 0.0f;
                 }
             float T[2][4][4];
@@ -320,10 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                     frag_bt<256>(s_v + 16384, kk, cw + 16 * j, lane, vl);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mma(T[i][2 * j], ua[i], vl[0], vl[1]);
-                        mma(T[i][2 * j + 1], ua[i], vl[2], vl[3]);
-                        mma(T[i][2 * j], ua[i], vh[0], vh[1]);
-                        mma(T[i][2 * j + 1], ua[i], vh[2], vh[3]);
+                        mma_h(T[i][2 * j], ua[i], vl[0], vl[1]);
+                        mma_h(T[i][2 * j + 1], ua[i], vl[2], vl[3]);
+                        mma_h(T[i][2 * j], ua[i], vh[0], vh[1]);
+                        mma_h(T[i][2 * j + 1], ua[i], vh[2], vh[3]);
                     }
                 }
             }
@@ -337,8 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                         const uint32_t at = 4 * (lane & 3);
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c0) : "r"(tile256(s_c, r, (cw >> 3) + j) + at));
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c1) : "r"(tile256(s_c, r + 8, (cw >> 3) + j) + at));
-                        z[i][0] = __fmaf_rn(T[i][j][0], bf16_lo(c0), __fmaf_rn(T[i][j][1], bf16_hi(c0), z[i][0]));
-                        z[i][1] = __fmaf_rn(T[i][j][2], bf16_lo(c1), __fmaf_rn(T[i][j][3], bf16_hi(c1), z[i][1]));
+                        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&c0));
+                        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&c1));
+                        z[i][0] = __fmaf_rn(T[i][j][0], f0.x, __fmaf_rn(T[i][j][1], f0.y, z[i][0]));
+                        z[i][1] = __fmaf_rn(T[i][j][2], f1.x, __fmaf_rn(T[i][j][3], f1.y, z[i][1]));
                     }
                     float(&to)[4] = acc[i][j];
                     to[0] = __fmaf_rn(e[i][0], T[i][j][0], to[0]);
@@ -355,30 +391,37 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                         float t = z[i][hf];
                         t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 1));
                         t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                        if ((lane & 3) == 0) v.z[w >> 1][rw + 16 * i + 8 * hf + (lane >> 2)] = t;
+                        if ((lane & 3) == 0) v.z[w >> 1][rw + 16 * i + 8 * hf + (lane >> 2)] = __fmul_rn(__fmul_rn(t, kt), kcb.x);
                     }
             }
         }
-        // ---- <dS, S>
+        // ---- <dS, S>: the diagonal of dS S^T, warp (ws, wt) the channels 16 ws .. and the states 32 wt ..
         {
-            float dot = 0.0f;
+            float D[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int idx = tid + kThreads * i, row = idx >> 4, pc = idx & 15;
-                const uint4 sh = ptx::lds128(tile256(s_s, row, pc)), sl = ptx::lds128(tile256(s_s + 16384, row, pc));
-                const uint4 dh = ptx::lds128(tile256(s_d, row, pc)), dl = ptx::lds128(tile256(s_d + 16384, row, pc));
-                const uint32_t a4[4] = {sh.x, sh.y, sh.z, sh.w}, b4[4] = {sl.x, sl.y, sl.z, sl.w};
-                const uint32_t c4[4] = {dh.x, dh.y, dh.z, dh.w}, d4[4] = {dl.x, dl.y, dl.z, dl.w};
+            for (int j = 0; j < 2; ++j) D[j][0] = D[j][1] = D[j][2] = D[j][3] = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    dot = __fmaf_rn(__fadd_rn(bf16_lo(a4[q]), bf16_lo(b4[q])), __fadd_rn(bf16_lo(c4[q]), bf16_lo(d4[q])), dot);
-                    dot = __fmaf_rn(__fadd_rn(bf16_hi(a4[q]), bf16_hi(b4[q])), __fadd_rn(bf16_hi(c4[q]), bf16_hi(d4[q])), dot);
+            for (int kk = 32 * wt; kk < 32 * wt + 32; kk += 16) {
+                uint32_t dh[4], dl[4], sh[4], sl[4];
+                frag_a<256>(s_d, 16 * ws, kk, lane, dh);
+                frag_a<256>(s_d + 16384, 16 * ws, kk, lane, dl);
+                frag_b<256>(s_s, 16 * ws, kk, lane, sh);
+                frag_b<256>(s_s + 16384, 16 * ws, kk, lane, sl);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {        // low by low is below 2^-24 of the product
+                    mma_h(D[j], dl, sh[2 * j], sh[2 * j + 1]);
+                    mma_h(D[j], dh, sl[2 * j], sl[2 * j + 1]);
+                    mma_h(D[j], dh, sh[2 * j], sh[2 * j + 1]);
                 }
             }
-            v.dot[tid] = dot;
+            // rows lane / 4 (+ 8), columns 2 (lane % 4), + 1 of tile j: on the diagonal of tile 0 its first two, of 1 its last
+            const int on = (lane >> 2) - 2 * (lane & 3);
+            const float dot = on == 0 ? __fadd_rn(D[0][0], D[1][2]) : on == 1 ? __fadd_rn(D[0][1], D[1][3]) : 0.0f;
+            v.dot[tid] = __fmul_rn(dot, __fmul_rn(sc.z, sc.w));
         }
         // ---- dx, rows s = 16 ws .., channels pw + 8 p ..
         {
+            const float kx = __fmul_rn(kcb.y, sc.w);
             float X[2][4];
 #pragma unroll
             for (int p = 0; p < 2; ++p) X[p][0] = X[p][1] = X[p][2] = X[p][3] = 0.0f;
@@ -388,15 +431,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 frag_b<256>(s_d, pw, kk, lane, dh);
                 frag_b<256>(s_d + 16384, pw, kk, lane, dl);
                 frag_a<256>(s_b, 16 * ws, kk, lane, ba);
-                mma(X[0], ba, dl[0], dl[1]);
-                mma(X[1], ba, dl[2], dl[3]);
-                mma(X[0], ba, dh[0], dh[1]);
-                mma(X[1], ba, dh[2], dh[3]);
+                mma_h(X[0], ba, dl[0], dl[1]);
+                mma_h(X[1], ba, dl[2], dl[3]);
+                mma_h(X[0], ba, dh[0], dh[1]);
+                mma_h(X[1], ba, dh[2], dh[3]);
             }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int s = 16 * ws + 8 * hf + (lane >> 2);
-                const float e = dc.left[s];
+                const float e = __fmul_rn(dc.left[s], kx);
                 float wl = 0.0f;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
@@ -407,14 +450,19 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                     float& x1 = X[p][2 * hf + 1];
                     x0 = __fmul_rn(x0, e);
                     x1 = __fmul_rn(x1, e);
-                    wl = __fmaf_rn(x0, bf16_lo(xv), wl);
-                    wl = __fmaf_rn(x1, bf16_hi(xv), wl);
+                    const float2 xf = __half22float2(*reinterpret_cast<const __half2*>(&xv));
+                    wl = __fmaf_rn(x0, xf.x, wl);
+                    wl = __fmaf_rn(x1, xf.y, wl);
                 }
                 wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 1));
                 wl = __fadd_rn(wl, __shfl_xor_sync(0xffffffffu, wl, 2));
-                if ((lane & 3) == 0) v.wl[wt][s] = wl;
+                if ((lane & 3) == 0) v.wl[wt][s] = __fmul_rn(wl, sc.x);
             }
-            __syncthreads();                      // M^T is there
+            ptx::cp_async_wait<0>();
+            __syncthreads();                      // M^T is there, and the next head's tiles
+            float Y[2][4];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) Y[p][0] = Y[p][1] = Y[p][2] = Y[p][3] = 0.0f;
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt) {
                 if (kt < ws) continue;            // t < s everywhere
@@ -422,11 +470,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 frag_bt<128>(s_y, 16 * kt, pw, lane, yb);
                 frag_a<128>(s_m, 16 * ws, 16 * kt, lane, mh);
                 frag_a<128>(s_m + 8192, 16 * ws, 16 * kt, lane, ml);
-                mma(X[0], ml, yb[0], yb[1]);
-                mma(X[1], ml, yb[2], yb[3]);
-                mma(X[0], mh, yb[0], yb[1]);
-                mma(X[1], mh, yb[2], yb[3]);
+                mma_h(Y[0], ml, yb[0], yb[1]);
+                mma_h(Y[1], ml, yb[2], yb[3]);
+                mma_h(Y[0], mh, yb[0], yb[1]);
+                mma_h(Y[1], mh, yb[2], yb[3]);
             }
+            if (h + 1 < h1) convert(h + 1);
+            const float ky = __fmul_rn(kg, sc.y), sky = __fmul_rn(skip, sc.y);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int s = 16 * ws + 8 * hf + (lane >> 2);
@@ -436,25 +486,40 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 for (int p = 0; p < 2; ++p) {
                     uint32_t yv;
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv) : "r"(tile128(s_y, s, (pw >> 3) + p) + 4 * (lane & 3)));
+                    const float2 yf = __half22float2(*reinterpret_cast<const __half2*>(&yv));
                     *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
-                        bf16x2_of(make_float2(__fmaf_rn(dts, X[p][2 * hf], __fmul_rn(skip, bf16_lo(yv))),
-                                              __fmaf_rn(dts, X[p][2 * hf + 1], __fmul_rn(skip, bf16_hi(yv)))));
+                        bf16x2_of(make_float2(
+                            __fmaf_rn(dts, __fmaf_rn(Y[p][2 * hf], ky, X[p][2 * hf]), __fmul_rn(sky, yf.x)),
+                            __fmaf_rn(dts, __fmaf_rn(Y[p][2 * hf + 1], ky, X[p][2 * hf + 1]), __fmul_rn(sky, yf.y))));
                 }
             }
         }
-        ptx::cp_async_wait<0>();
-        __syncthreads();                          // the head's sums and the next one's tiles are there
+        __syncthreads();                          // the head's sums and the next one's fp16 tiles are there
     }
     if (w == 0) finish(h1 - 1);
 
-    // ---- W^T as two bf16 parts, then dB += W^T C, dC += W B
+    // ---- W^T as two fp16 parts under the scale of its largest value, then dB += W^T C, dC += W B
+    {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = fmaxf(m, fabsf(W[j][q]));
+        const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0) wmax[w] = mb;
+    }
+    __syncthreads();
+    uint32_t mb = 0u;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) mb = max(mb, wmax[i]);
+    const float2 kw = pow2_scale(mb, 13);
     {
         const int s = 16 * ws + (lane >> 2);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t h0v, l0v, h1v, l1v;
-            split_bf16x2(W[j][0], W[j][1], h0v, l0v);
-            split_bf16x2(W[j][2], W[j][3], h1v, l1v);
+            split_f16x2(__fmul_rn(W[j][0], kw.x), __fmul_rn(W[j][1], kw.x), h0v, l0v);
+            split_f16x2(__fmul_rn(W[j][2], kw.x), __fmul_rn(W[j][3], kw.x), h1v, l1v);
             const uint32_t p0 = tile128(s_m, s, 2 * wt + j) + 4 * (lane & 3);
             const uint32_t p1 = tile128(s_m, s + 8, 2 * wt + j) + 4 * (lane & 3);
             ptx::sts32(p0, h0v);
@@ -464,6 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
         }
     }
     __syncthreads();
+    float T[2][4][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) T[i][j][0] = T[i][j][1] = T[i][j][2] = T[i][j][3] = 0.0f;
 #pragma unroll 1
     for (int kk = 0; kk < kQ; kk += 16) {
         if (side ? kk + 15 < rw : kk > rw + 31) continue;      // dB: t >= s; dC: s <= t
@@ -479,12 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
                 else frag_at<128>(s_m + part * 8192, kk, rw + 16 * i, lane, wa);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    mma(acc[i][2 * j], wa, vb[j][0], vb[j][1]);
-                    mma(acc[i][2 * j + 1], wa, vb[j][2], vb[j][3]);
+                    mma_h(T[i][2 * j], wa, vb[j][0], vb[j][1]);
+                    mma_h(T[i][2 * j + 1], wa, vb[j][2], vb[j][3]);
                 }
             }
         }
     }
+    const float kwv = __fmul_rn(kw.y, side ? kcb.x : kcb.y);
     const int64_t ldp = (int64_t)ngroups * kN;
     float* part = side ? o.db_part : o.dc_part;
 #pragma unroll
@@ -496,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             const int64_t at = ((int64_t)sp * a.total + t0 + r) * ldp + g * kN + cw + 2 * (lane & 3);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float2*>(part + at + 8 * j) = make_float2(acc[i][j][2 * hf], acc[i][j][2 * hf + 1]);
+                *reinterpret_cast<float2*>(part + at + 8 * j) =
+                    make_float2(__fmaf_rn(T[i][j][2 * hf], kwv, acc[i][j][2 * hf]), __fmaf_rn(T[i][j][2 * hf + 1], kwv, acc[i][j][2 * hf + 1]));
         }
 }
 
@@ -574,7 +646,7 @@ Split choose_split(int cap_chunks, int ngroups, int per_group) {
 }
 
 struct BwdWs {
-    size_t s_in, ds, db, dc, sums, total;
+    size_t s_in, ds, scale, db, dc, sums, total;
 };
 BwdWs bwd_ws(const dfssm_scan_dims* d, int total, int nseq, const Plan& p) {
     BwdWs w{};
@@ -585,6 +657,8 @@ BwdWs bwd_ws(const dfssm_scan_dims* d, int total, int nseq, const Plan& p) {
     o = up256(o + states);
     w.ds = o;
     o = up256(o + states);
+    w.scale = o;
+    o = up256(o + (size_t)p.cap_chunks * d->nheads * sizeof(float4));
     w.db = o;
     o = up256(o + (size_t)sp.splits * total * d->ngroups * kN * 4);
     w.dc = o;
@@ -653,7 +727,9 @@ extern "C" dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const df
     const Split sp = choose_split(p.cap_chunks, dims->ngroups, dims->nheads / dims->ngroups);
     o.splits = sp.splits;
     o.per_split = sp.per;
-    const StateArgs st_args{o.dy, dy_stride, dfinal_state, s_in, ds, gr->dinit_state};
+    float* scale = reinterpret_cast<float*>(ws + w.scale);
+    o.scale = reinterpret_cast<const float4*>(scale);
+    const StateArgs st_args{o.dy, dy_stride, dfinal_state, s_in, ds, scale, gr->dinit_state};
     if (launch_table(a, s) != cudaSuccess || launch_states(a, st_args, s) != cudaSuccess)
         return DFSSM_ERR_CUDA;
     if (launch_after(scan_grad_kernel, p.cap_chunks * dims->ngroups * sp.splits, kThreads, kGradSmem, s, a, o) != cudaSuccess ||
