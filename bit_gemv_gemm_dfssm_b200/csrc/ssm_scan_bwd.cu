@@ -4,8 +4,8 @@
 //   dx_t = dt_t dS_t B_t + d_skip dy_t;   dB_t = sum_h dt_t dS_t^T x_t;   dC_t = sum_h S_t^T dy_t
 //   d dt_t = x_t . dS_t B_t + A da_t,     da_t = <dS_t, exp(a_t) S_{t-1}>,  A = -exp(a_log)
 // For a chunk of 64 tokens with the state S in front of it and the gradient dS behind it (both from
-// sequential kernels, ssm_scan.cu, which leave one pair per chunk and head in the workspace as two
-// bf16 parts each), L[t, s] = exp(cum_t - cum_s) for s <= t:
+// scan_state_kernel, ssm_scan.cu, which leaves one pair per chunk and head in the workspace as two fp16 parts each),
+// L[t, s] = exp(cum_t - cum_s) for s <= t:
 //   G = C B^T, Z = dy x^T;   M = G o L;   W = sum_h Z o L dt_s
 //   dx_s = dt_s (sum_t M[t, s] dy_t + exp(cum_64 - cum_s) dS B_s) + d_skip dy_s
 //   dB   = W^T C + sum_h dt_s exp(cum_64 - cum_s) x_s dS
@@ -15,13 +15,21 @@
 //   da_t = sum_{t' >= t, s < t} E[t', s] + sum_{t' >= t} z_t' + sum_{s < t} w_s + exp(cum_64) <dS, S>
 // with E = M o Z dt_s, z_t = exp(cum_t) dy_t . S C_t (from the accumulators of dC) and w_s = dt_s exp(cum_64 -
 // cum_s) x_s . dS B_s (from those of dx). The first sum is that of E's row sums from t on less that of its
-// column sums from t on; both come from the same fp32 values, so that what cancels cancels (taken from
-// dy . y and x . dx, which carry different roundings, d a_log was off by 3e-4).
+// column sums from t on, without the diagonal, which would only cancel; both come from the same fp32 values, so that
+// what else cancels cancels (taken from dy . y and x . dx, which carry different roundings, d a_log was off by 3e-4).
+// x . dx without the skip is the column sums of M o Z, the diagonal, and x . dS B.
 //
 // scan_grad_kernel: CTA (chunk, group, split of the group's heads), 16 warps, one head after another with the
-// next head's tiles on the way (cp.async), bf16 warp MMAs; fp32 operands (M, W, S, dS) as two bf16
-// parts (2^-17). Partial dB and dC of the splits and partial parameter sums per chunk are added in
-// order by two small kernels.
+// next head's tiles on the way (cp.async) and the last one's d dt behind (a warp without a part of Z). fp16 warp MMAs;
+// x, dy, B and C are bf16 values under power-of-two scales (exact over 2^17 of range and more), M, W, S and dS two
+// fp16 parts (2^-23; as bf16 parts, 2^-17, they were what short sequences' d a_log was off by, 8e-6, and the kernel
+// 10% faster). Partial dB and dC of the splits and partial parameter sums per chunk are added in order by two
+// small kernels.
+//
+// Measured (4 x 2,048 tokens, 64 heads): 406 us of the call's 650, the states' kernel 250. Neither the tensor pipe nor
+// shared memory is near its limit (28 and 40 %): a head's chain of products, exchanges and sums between two
+// barriers bounds it, with one CTA per SM (228 KB); left out one at a time, Z and M cost 55 us, dC and dB 80, dx 45,
+// the loads 28. The states alone are 1.1 GB of traffic, 166 us of the HBM's rate.
 #include "ssm_scan.cuh"
 
 namespace dfssm {
@@ -264,29 +272,29 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             const float cs0 = dc.cum[s], cs1 = dc.cum[s + 8], ds0 = dc.dt[s], ds1 = dc.dt[s + 8];
             const float kz = __fmul_rn(sc.x, sc.y), w0 = __fmul_rn(ds0, kz), w1 = __fmul_rn(ds1, kz), km = __fmul_rn(kz, kg);
             float col0 = 0.0f, col1 = 0.0f;
+            const int on = (lane >> 2) - 2 * (lane & 3);      // which of the thread's two columns is on the diagonal
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = 16 * wt + 8 * j + 2 * (lane & 3);
                 const float2 ct = *reinterpret_cast<const float2*>(dc.cum + t);
                 float l[4];
-                l[0] = t >= s ? exp2f(__fsub_rn(ct.x, cs0)) : 0.0f;
-                l[1] = t + 1 >= s ? exp2f(__fsub_rn(ct.y, cs0)) : 0.0f;
-                l[2] = t >= s + 8 ? exp2f(__fsub_rn(ct.x, cs1)) : 0.0f;
-                l[3] = t + 1 >= s + 8 ? exp2f(__fsub_rn(ct.y, cs1)) : 0.0f;
+                l[0] = t >= s ? ex2(__fsub_rn(ct.x, cs0)) : 0.0f;
+                l[1] = t + 1 >= s ? ex2(__fsub_rn(ct.y, cs0)) : 0.0f;
+                l[2] = t >= s + 8 ? ex2(__fsub_rn(ct.x, cs1)) : 0.0f;
+                l[3] = t + 1 >= s + 8 ? ex2(__fsub_rn(ct.y, cs1)) : 0.0f;
                 const float m[4] = {__fmul_rn(G[j][0], l[0]), __fmul_rn(G[j][1], l[1]), __fmul_rn(G[j][2], l[2]),
                                     __fmul_rn(G[j][3], l[3])};
                 // the sums of E over the warp's s for the thread's two t, and of M o Z over the thread's t
                 float mz[4] = {__fmul_rn(m[0], Z[j][0]), __fmul_rn(m[1], Z[j][1]), __fmul_rn(m[2], Z[j][2]),
                                      __fmul_rn(m[3], Z[j][3])};
-                // the diagonal (where L = 1), kept apart: what enters at t leaves before it could decay
-                if (ws == wt) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (t + (q & 1) == s + 4 * (q & 2)) {
-                            v.skip[t + (q & 1)] = __fmul_rn(Z[j][q], kz);
-                            v.own[t + (q & 1)] = __fmul_rn(mz[q], km);
-                            mz[q] = 0.0f;
-                        }
+                // the diagonal (where L = 1), kept apart: what enters at t leaves before it could decay. It runs through
+                // the first half of tile 0 and the second of tile 1.
+                if (ws == wt && (unsigned)on < 2u) {
+                    const int d = t + on;
+                    v.skip[d] = __fmul_rn(on ? Z[j][2 * j + 1] : Z[j][2 * j], kz);
+                    v.own[d] = __fmul_rn(on ? mz[2 * j + 1] : mz[2 * j], km);
+                    if (on) mz[2 * j + 1] = 0.0f;
+                    else mz[2 * j] = 0.0f;
                 }
                 col0 = __fadd_rn(col0, __fadd_rn(mz[0], mz[1]));
                 col1 = __fadd_rn(col1, __fadd_rn(mz[2], mz[3]));
@@ -481,18 +489,23 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
             for (int hf = 0; hf < 2; ++hf) {
                 const int s = 16 * ws + 8 * hf + (lane >> 2);
                 const float dts = dc.dt[s];
-                if (s >= n) continue;
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     uint32_t yv;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv) : "r"(tile128(s_y, s, (pw >> 3) + p) + 4 * (lane & 3)));
+                    const uint32_t at = 4 * (lane & 3);
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(yv) : "r"(tile128(s_y, s, (pw >> 3) + p) + at));
                     const float2 yf = __half22float2(*reinterpret_cast<const __half2*>(&yv));
-                    *reinterpret_cast<uint32_t*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + pw + 8 * p + 2 * (lane & 3)) =
-                        bf16x2_of(make_float2(
-                            __fmaf_rn(dts, __fmaf_rn(Y[p][2 * hf], ky, X[p][2 * hf]), __fmul_rn(sky, yf.x)),
-                            __fmaf_rn(dts, __fmaf_rn(Y[p][2 * hf + 1], ky, X[p][2 * hf + 1]), __fmul_rn(sky, yf.y))));
+                    // over the x that the head is done with, to go out in whole 32-byte sectors
+                    ptx::sts32(tile128(s_x, s, (pw >> 3) + p) + at,
+                               bf16x2_of(make_float2(
+                                   __fmaf_rn(dts, __fmaf_rn(Y[p][2 * hf], ky, X[p][2 * hf]), __fmul_rn(sky, yf.x)),
+                                   __fmaf_rn(dts, __fmaf_rn(Y[p][2 * hf + 1], ky, X[p][2 * hf + 1]), __fmul_rn(sky, yf.y)))));
                 }
             }
+            __syncwarp();
+            const int s = 16 * ws + (lane >> 1), pc = (pw >> 3) + (lane & 1);
+            const uint4 row = ptx::lds128(tile128(s_x, s, pc));
+            if (s < n) *reinterpret_cast<uint4*>(o.dx + (int64_t)(t0 + s) * o.lddx + h * kP + 8 * pc) = row;
         }
         __syncthreads();                          // the head's sums and the next one's fp16 tiles are there
     }
