@@ -19,6 +19,9 @@
 // step. The gradient's CTAs are persistent, so that dw accumulates in registers over a CTA's
 // rows; one partial row per CTA goes to the workspace and a second kernel adds the partials.
 // Every order of summation is fixed by m and d.
+//
+// Measured, 16,384 x 2048 with a bf16 delta: forward 66 us, 6.6 TB/s; gradient with dw 79 + 7 us, 6.0 TB/s. One token:
+// the launch, 2.4 us in a graph, 5 us with the gradient's two.
 #include <cmath>
 #include <cstdint>
 
@@ -194,7 +197,7 @@ struct BwdArgs {
 };
 
 // One row group's loads in flight: the next rows' while the current ones are reduced and stored
-// (16,384 x 2048 with a bf16 gradient and a stream gradient: 94 -> 80 us).
+// (16,384 x 2048 with a bf16 gradient and a stream gradient, the call: 94 -> 88 us).
 template <int NV, bool BF>
 struct BwdRow {
     float r[NV][8];

@@ -553,10 +553,12 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const Args a, const flo
 }
 
 // The state alone through an item: blockIdx.y 0 forward in time (u = x, v = B), 1 backward (u = dy, v = C: the
-// state's gradient). STORE: from its start, at every chunk to the workspace; otherwise from zero, the
-// item's own contribution and decay, for what starts behind it. Eight warps; warp (pw, hv) holds the channels
+// state's gradient). STORE: from its start, at every chunk to the workspace, with the scales of the gradient kernel;
+// otherwise from zero, the item's own contribution and decay, for what starts behind it. Eight warps; warp (pw, hv) holds the channels
 // 16 pw .. and the states 64 hv .. in fp32 accumulators. v comes in fp16 (scan_tiles_kernel), the weighted u enters
-// as two fp16 parts under a power-of-two scale of the warp's channels.
+// as two fp16 parts under a power-of-two scale of the warp's channels (2^-23 of each, down to 2^-38 of the largest).
+// Bound by a chunk's chain of steps between two barriers and their instructions (half of the issue slots) with two
+// CTAs per SM, 4 us for a chunk of each: 4 x 2,048 tokens, 64 heads, both directions 250 us, 2.5 TB/s.
 struct StateDecay {
     float wt[kQ];        // the weights of u, the largest in [1/2, 1)
     float keep;          // exp(cum_64)

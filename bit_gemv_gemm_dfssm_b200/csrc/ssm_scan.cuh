@@ -1,10 +1,10 @@
-// Shared parts of the state scan over packed sequences (ssm_scan.cu, ssm_scan_bwd.cu): the work
+// Shared parts of the state scan over packed sequences (ssm_scan.cu, ssm_scan_tc.cu, ssm_scan_bwd.cu): the work
 // table, the decays of a chunk, shared-memory tiles and warp-MMA fragments.
 //
 // The recurrence of one head h (64 channels p, 128 states n; B and C shared by a group of heads):
 //   dt_t = softplus(dt_raw + dt_bias) (the argument itself above 20), a_t = -exp(a_log) dt_t
 //   S_t  = exp(a_t) S_{t-1} + dt_t x_t B_t^T,      y_t = S_t C_t + d_skip x_t
-// is worked on in chunks of 64 tokens (cum_t = a_1 + ... + a_t inside the chunk):
+// is worked on in chunks of 64 tokens, 128 in ssm_scan_tc.cu (cum_t = a_1 + ... + a_t inside the chunk):
 //   y_t   = sum_{s <= t} (C_t . B_s) exp(cum_t - cum_s) dt_s x_s + exp(cum_t) S_0 C_t + d_skip x_t
 //   S_end = exp(cum_64) S_0 + sum_s exp(cum_64 - cum_s) dt_s x_s B_s^T
 // All exponents are <= 0. Decays are kept in units of log 2.
@@ -40,7 +40,7 @@ enum { kFirst = 1, kLast = 2, kCut = 4 };   // first / last segment of its seque
 
 struct Chunk {
     int32_t t0;
-    int32_t n;         // 1 .. 64 tokens
+    int32_t n;         // 1 .. 64 (128) tokens
 };
 
 // What every kernel of a call gets.

@@ -11,13 +11,18 @@
 // scale is a power of two. B^T, X, S and w X are read along their rows (M- or N-major operands), so nothing is
 // transposed.
 //
-// Roles (20 warps): TMA; MMA issue; decays (one warp); and four groups of four warps, one thread per row:
+// Roles (20 warps): TMA; MMA issue; decays (two warps in turn); and four groups of four warps, one thread per row:
 //   M group: G from tensor memory -> M back into tensor memory;
 //   X group: x -> fp16 in place, w x -> two tiles;
 //   S group: thread n holds S[0..63][n]: S -> fp16 tile, then S = keep S + D;
 //   Y group: Yi, Ya, x -> y in bf16 over the x tile, out as whole rows.
 // They meet in mbarriers only, so that the products of one chunk run beside the conversions of the next. Every
 // wait is bounded.
+//
+// Measured (8 sequences, 16,384 tokens, 64 heads): 260 us, 4.7 us per chunk and SM, where the products take 20 % of the
+// tensor pipe and 250 MB 12 % of the HBM's rate: the chain G -> M -> Ya -> y and S -> D -> S of one chunk, each step
+// a hand-over between roles, bounds it. Chunks of 64 tokens on warp MMAs took 440 us; one role's loops unrolled
+// further, or twice the warps per role, were slower (instruction fetches; 290 to 320 us).
 #include <cstddef>
 
 #include "ssm_scan.cuh"

@@ -430,6 +430,7 @@ dfssm_status dfssm_ssm_scan_workspace_bytes(const dfssm_scan_dims* dims, int32_t
  * or NaN, and can do so to every channel of its head (of its group, from b and c) in its chunk, in front of it
  * too, and behind it, but not in another sequence. Inside a chunk b and c are rounded to steps of 2^-28 of
  * their group's largest magnitude (exact down to 2^-17 of it), the states' new part to 2^-38 of the largest addend.
+ * y overlaps no input.
  * workspace: 256-byte aligned, at least dfssm_ssm_scan_workspace_bytes, zeroed once before its first use.
  * Its first 4 bytes are a device error word (DFSSM_DEVERR_SEQLENS: a sequence whose offsets are negative,
  * descending or beyond total is skipped), read and cleared by dfssm_ssm_read_error; nothing else is kept
@@ -460,7 +461,8 @@ typedef struct {
 
 /* The gradient of sum(dy y) + sum(dfinal_state final_state) with respect to every input. dy: bf16 as y;
  * dfinal_state: as final_state, or NULL (zeros). Nothing of the forward call is needed; the states are
- * computed again. Workspace, errors and limits as for dfssm_ssm_scan_fwd (with backward = 1). */
+ * computed again and kept in the workspace (64 KB per 64 tokens and head). No gradient overlaps an input or dy.
+ * Errors and limits as for dfssm_ssm_scan_fwd (with backward = 1). */
 dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
                                 int32_t nseq, const void* dy, int64_t dy_stride, const float* dfinal_state,
                                 const dfssm_scan_grads* grads, void* workspace, size_t workspace_bytes,

@@ -12,8 +12,9 @@ binade, 2^-8 of the value at most) around sx q, itself off by 2^-18.
 
 The gradient: f g - f^3 c r with c = sum(g r)/d. The terms of c have both signs: its error is
 bounded by 45 2^-24 sum|g r|/d. dresid's error is then below 2^-18 (|f g| + f^3 |r| (sum|g r|/d +
-|c|) + |dstream|) elementwise; dnorm_w adds m terms (chains of at most ceil(m/592) rows per CTA,
-then up to 74 in order and 8 more) with |error| < (m/592 + 120) 2^-24 sum|dout r f| for each column.
+|c|) + |dstream|) elementwise; dnorm_w adds m terms (chains of at most ceil(m/444) rows per CTA,
+then up to 14 in order and 32 more; m <= 65536) with |error| < (m/444 + 47) 2^-24 sum|dout r f| <
+(m/592 + 120) 2^-24 sum|dout r f| for each column.
 """
 import numpy as np
 import pytest

@@ -3,8 +3,8 @@
 Tolerances. Every result is a sum of products, and its error is bounded by a factor f times the same
 sum of magnitudes (the recurrence run on absolute values):
 * x, B, C and dy enter exactly. In y, M and S are one fp16 number each: half a step, 2^-11 of the value,
-  added to f for y. Elsewhere the second operand (M, W, S, dS) is two bf16 parts, 2^-17 of its value, or in the
-  state's own update three bf16 or two fp16 parts, 2^-22; fp32 accumulators round at most 2^-23 per MMA step, at most 32
+  added to f for y. Elsewhere the second operand (M, W, S, dS, weighted x and dy) is two fp16 parts, 2^-22 of its value
+  (2^-17, two bf16 parts, are allowed); fp32 accumulators round at most 2^-23 per MMA step, at most 32
   steps per chunk and result, 2^-18; a result passes through at most three such products: 2^-15.
 * a decay exp(cum_t - cum_s) carries the error of its exponent: the chunk's sums round 2^-24 of at most
   their largest value c (in units of log 2) in at most 8 steps: 2^-21 c; exp2f and the products with dt
