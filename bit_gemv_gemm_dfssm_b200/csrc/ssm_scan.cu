@@ -56,7 +56,9 @@ __device__ __forceinline__ int block_scan(int v, int* red, int& total) {
 __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a) {
     __shared__ int red[kTableThreads / 32];
     __shared__ int lens[kMaxSorted];
+    __shared__ int end[2];               // items and chunks in front of the first sequence that does not fit
     ptx::pdl_launch_dependents();
+    if (threadIdx.x < 2) end[threadIdx.x] = 0x7FFFFFFF;
     int n_items = 0, n_chunks = 0, n_slots = 0;
     for (int s0 = 0; s0 < a.nseq; s0 += kTableThreads) {
         const int s = s0 + threadIdx.x;
@@ -77,14 +79,17 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
         const int i1 = n_items + block_scan(nseg, red, ti);
         const int c1 = n_chunks + block_scan(nch, red, tc);
         const int s1 = n_slots + block_scan(cut, red, ts);
-        // overlapping offsets could ask for more than the workspace holds
-        const bool fits = i1 <= a.cap_items && c1 <= a.cap_chunks && s1 <= a.cap_slots;
+        // Overlapping offsets could ask for more than the workspace holds. From the first sequence on that does not fit
+        // (the sums only grow) all are left out, so that every counted item and chunk is written below.
+        const bool fits = i1 <= a.cap_items && c1 <= a.cap_chunks && s1 <= a.cap_slots && end[0] == 0x7FFFFFFF;
+        __syncthreads();                // end[] of the sequences before is read
         if (s < a.nseq) {
             const int i0 = i1 - nseg, c0 = c1 - nch;
             a.seq_slots[s] = fits ? make_int2(s1 - cut, cut) : make_int2(0, 0);
             if (!fits) {
                 atomicOr(a.err, DFSSM_DEVERR_SEQLENS);
-                for (int k = 0; k < nseg && i0 + k < a.cap_items; ++k) a.seq_items[i0 + k] = Item{s, 0, -1, 0, 0, 0};
+                atomicMin(&end[0], i0);
+                atomicMin(&end[1], c0);
             } else {
                 for (int k = 0; k < nseg; ++k) {
                     const int at = k * a.seg_len;
@@ -96,7 +101,10 @@ __global__ void __launch_bounds__(kTableThreads) scan_table_kernel(const Args a)
         n_items = min(n_items + ti, a.cap_items);
         n_chunks = min(n_chunks + tc, a.cap_chunks);
         n_slots = min(n_slots + ts, a.cap_slots);
+        __syncthreads();                // end[] is written
     }
+    n_items = min(n_items, end[0]);
+    n_chunks = min(n_chunks, end[1]);
     __syncthreads();                    // the items of this CTA are visible to it
     if (threadIdx.x == 0) {
         a.count[0] = n_items;

@@ -325,6 +325,24 @@ def test_bad_offsets_are_reported_and_skipped():
     assert torch.equal(y[:30], good[:30]) and (y[30:] == 77).all()
 
 
+def test_offsets_that_overlap_leave_out_what_the_workspace_cannot_hold():
+    """The same 700 rows as three sequences (0..700, and back, twice): more chunks than the call's rows can have. What is
+    left is whole: the first sequence's results, its parameters' gradients among them."""
+    a = inputs(16, [700], 2, 1, False)
+    y, _, _ = run_fwd(a)
+    r, _ = run_bwd(a)
+    b = {**a, "lens": [700, 0, 700, 0, 700], "cu": torch.tensor([0, 700, 0, 700, 0, 700], dtype=torch.int32, device="cuda")}
+    y2, _, ws = run_fwd(b, final=None)
+    r2, ws2 = run_bwd(b)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2)
+    for k in r:
+        assert r[k] is None or torch.equal(r[k], r2[k]), k
+    for w in (ws, ws2):
+        st, bits = dfssm.dfssm_ssm_read_error(ptr(w), stream())
+        assert st == dfssm.DFSSM_ERR_DEVICE_CHECK and bits == dfssm.DFSSM_DEVERR_SEQLENS
+
+
 def test_a_sequence_that_is_not_finite_leaves_the_others_alone():
     a = inputs(11, [70, 90, 30], 2, 1, True)
     y, fin, _ = run_fwd(a)
