@@ -105,6 +105,26 @@ def test_training_step_from_a_graph():
         assert torch.equal(v, kept[k]), k
 
 
+def test_two_chains_at_once():
+    """Two chains with their own buffers, launched in turn on two streams that nothing orders."""
+    args = ([300, 5, 700], 4, 2, 900), ([64] * 9, 4, 1, 2000)
+    alone = [Chain(50 + i, *v) for i, v in enumerate(args)]
+    for c in alone:
+        c.step()
+    torch.cuda.synchronize()
+    both = [Chain(50 + i, *v) for i, v in enumerate(args)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, s in zip(both, streams):
+            with torch.cuda.stream(s):
+                c.step()
+    torch.cuda.synchronize()
+    for c, e in zip(both, alone):
+        for k, v in e.out.items():
+            assert torch.equal(v, c.out[k]), k
+
+
 def test_server_continues_token_by_token():
     """Two prompts in one call, then three tokens each from the states that call left, each token through the norm and
     the table: every call's states and losses against 64 bits."""
