@@ -16,8 +16,9 @@
 //
 // Short calls (scan_fwd_kernel, warp MMAs, chunks of 64 tokens) are one launch that converts its tiles itself. What a
 // call of a few tokens costs is one launch, one chunk's chain of loads, products and exchanges, and the
-// states: 64 heads, 8.8 us for one sequence of 1 to 16 tokens, 15 us for 128.
+// states: 64 heads, 5.5 us for one sequence of 1 to 16 tokens, 8.8 for 64, 14 for 128.
 #include <mutex>
+#include <type_traits>
 
 #include "ssm_scan.cuh"
 
@@ -270,7 +271,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
     raws(0);
     decay(0);
     raws(1);
-    for (int k = 0; k < n_ch; ++k) {
+    // A chunk, of whose four blocks of 16 tokens the first `blocks` hold tokens; what lies behind is neither worked on nor
+    // read. Short chunks (up to 16 and up to 32 tokens, a server's few at a time) have their own code: 64 sequences of
+    // 8 tokens, 64 heads 153 -> 98 us, one of 1 token 8.6 -> 5.5 us, 16 of 32 40 -> 31 us; with the count at run time, full
+    // chunks lost a quarter.
+    auto chunk = [&](int k, auto blocks) {
+        constexpr int nb = decltype(blocks)::value;
         const int t0 = it.t0 + k * kQ, n = min(kQ, it.len - k * kQ);
         const uint32_t st = base + (k & 1) * kStage;
         const uint32_t s_c = st, s_b = st + 16384, s_x = st + 32768;
@@ -285,7 +291,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
             for (int side = 0; side < 2; ++side) {
                 uint32_t m = 0u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) {     // 16 rows; the zeros behind the tokens are the same in fp16
+                    if (i >= nb) break;
                     v[side][i] = ptx::lds128(st + 16384 * side + 16 * (tid + kFwdThreads * i));
                     m = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(m, v[side][i].x), v[side][i].y),
                                                       v[side][i].z), v[side][i].w);
@@ -302,17 +309,19 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
                 const float2 sc = pow2_scale(m, kTileTop);
                 (side ? tsc.y : tsc.x) = sc.y;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    if (i >= nb) break;
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
                                  ::"r"(st + 16384 * side + 16 * (tid + kFwdThreads * i)),
                                  "r"(bf16x2_to_f16x2(v[side][i].x, sc.x)), "r"(bf16x2_to_f16x2(v[side][i].y, sc.x)),
                                  "r"(bf16x2_to_f16x2(v[side][i].z, sc.x)), "r"(bf16x2_to_f16x2(v[side][i].w, sc.x)) : "memory");
+                }
             }
             __syncthreads();
         }
 
         // ---- M in fp16, rows 16 pw + lane / 4 (+ 8), columns in blocks hv and hv + 2 of 16 up to the diagonal
-        {
+        if (pw < nb) {
             float G[2][2][4];
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -384,6 +393,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
                     sb[q] = f16x2_of(__fmul_rn(S[2 * kk + (q & 1)][q & 2], ss.x), __fmul_rn(S[2 * kk + (q & 1)][(q & 2) + 1], ss.x));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    if (i >= nb) break;
                     uint32_t ca[4];
                     frag_a<256>(s_c, 16 * i, 64 * hv + 16 * kk, lane, ca);
                     mma_h(y[i][0], ca, sb[0], sb[1]);
@@ -395,6 +405,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
             const uint32_t ex = s_ex + (uint32_t)((pw * 2 + (hv ^ 1)) * 2048 + lane * 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (i >= nb) break;
                 const float e0 = __fmul_rn(d.done[16 * i + (lane >> 2)], back), e1 = __fmul_rn(d.done[16 * i + 8 + (lane >> 2)], back);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
@@ -413,6 +424,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
         uint32_t xm = 0u;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
+            if (ks >= nb) break;
             uint32_t xa[4];
             frag_at<128>(s_x, 16 * ks, 16 * pw, lane, xa);
 #pragma unroll
@@ -430,14 +442,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
                 for (int p = 0; p < 2; ++p) u[i][p][0] = u[i][p][1] = u[i][p][2] = u[i][p][3] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                if (ks > 2 * hv + 1) break;
+                if (ks > 2 * hv + 1 || ks >= nb) break;
                 uint32_t xb[4];
                 frag_bt<128>(s_x, 16 * ks, 16 * pw, lane, xb);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) xb[q] = bf16x2_to_f16x2(xb[q], xs.x);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (ks > 2 * hv + i) continue;
+                    if (ks > 2 * hv + i || 2 * hv + i >= nb) continue;
                     uint32_t ma[4];
                     frag_a<128>(s_m, 32 * hv + 16 * i, 16 * ks, lane, ma);
                     mma_h(u[i][0], ma, xb[0], xb[1]);
@@ -448,6 +460,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
             const uint32_t ex = s_ex + (uint32_t)((pw * 2 + hv) * 2048 + lane * 16);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                if (2 * hv + i >= nb) break;
                 uint32_t out[2][2];      // [row half][channel tile]
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
@@ -489,6 +502,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
             for (int j = 0; j < 8; ++j) D[j][0] = D[j][1] = D[j][2] = D[j][3] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
+                if (ks >= nb) break;
                 float2 w0 = *reinterpret_cast<const float2*>(d.wl + 16 * ks + 2 * (lane & 3));
                 float2 w1 = *reinterpret_cast<const float2*>(d.wl + 16 * ks + 8 + 2 * (lane & 3));
                 w0 = make_float2(__fmul_rn(w0.x, xs.x), __fmul_rn(w0.y, xs.x));
@@ -514,6 +528,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2) scan_fwd_kernel(const Args a, 
 #pragma unroll
                 for (int q = 0; q < 4; ++q) S[j][q] = __fmaf_rn(D[j][q], back, __fmul_rn(S[j][q], keep));
         }
+    };
+    for (int k = 0; k < n_ch; ++k) {
+        const int left = it.len - k * kQ;
+        if (left <= 16) chunk(k, std::integral_constant<int, 1>{});
+        else if (left <= 32) chunk(k, std::integral_constant<int, 2>{});
+        else chunk(k, std::integral_constant<int, 4>{});
     }
     ptx::cp_async_wait<0>();
     if (o.final_state) {
@@ -780,9 +800,9 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
 
 // Forward calls whose sequences have at most kDirectMean tokens on average take the warp-MMA kernel in one launch, where
 // even one sequence holding all the tokens is not long (kDirectTokens), or not long beside the work there is. Measured,
-// sequences x tokens, 64 heads, one launch against tensor cores behind table and tiles (us): 1 x 1 8.8 / 16.9,
-// 1 x 128 14.8 / 18.2, 1 x 256 25.5 / 20.8, 1 x 512 47 / 27.5, 2 x 256 25.6 / 21.6, 4 x 128 21.2 / 27.2, 4 x 256 36.9 / 36.1,
-// 16 x 64 43 / 81, 128 x 8 310 / 512.
+// sequences x tokens, 64 heads, one launch against tensor cores behind table and tiles (us): 1 x 1 5.5 / 17,
+// 1 x 128 14 / 18, 1 x 256 25 / 20, 1 x 512 47 / 27, 2 x 256 26 / 21, 4 x 128 20.5 / 27, 4 x 256 37 / 32, 16 x 64 41 / 81,
+// 128 x 8 193 / 512.
 constexpr int kDirectMean = 128;
 constexpr int kDirectTokens = 1024;
 

@@ -233,7 +233,7 @@ def check_bwd(a, r):
 
 CASES = [([1], 1, 1, True, 0), ([64], 2, 1, False, 0), ([65, 0, 1, 63], 4, 2, True, 5), ([0], 3, 3, True, 2),
          ([5, 1, 0, 17], 64, 1, True, 0), ([130, 300], 6, 1, False, 3), ([200] * 3, 5, 5, True, 0),
-         ([3] * 70, 2, 1, False, 1)]
+         ([3] * 70, 2, 1, False, 1), ([16, 17, 32, 33, 49, 80], 2, 1, True, 0)]
 
 
 @pytest.mark.parametrize("lens,nh,ng,init,gap", CASES)
