@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_grad_kernel(const Args a, co
 }
 
 // dB and dC: the splits' parts added in order, 4 columns per thread; 8 CTAs per chunk (one: 24 us for 6 chunks of
-// 16 parts), rows of no chunk stay
+// 16 parts, 8: 7), rows of no chunk stay
 __global__ void __launch_bounds__(256) scan_sum_kernel(const Args a, const float* __restrict__ db_part,
                                                        const float* __restrict__ dc_part, int splits, uint16_t* db,
                                                        int64_t lddb, uint16_t* dc, int64_t lddc) {
@@ -639,14 +639,15 @@ __global__ void __launch_bounds__(256) scan_params_kernel(const Args a, const fl
     }
 }
 
-// Splits of a group's heads: the fewest waves of 148 CTAs, a CTA costing its heads and about one more
+// Splits of a group's heads: the fewest waves of 148 CTAs, a CTA costing its heads and about one more; up to 32 (60
+// tokens, 64 heads: 40 us, with 16 49, with 64 41)
 struct Split {
     int splits, per;
 };
 Split choose_split(int cap_chunks, int ngroups, int per_group) {
     Split best{1, per_group};
     double cost = 1e30;
-    for (int s = 1; s <= per_group && s <= 16; ++s) {
+    for (int s = 1; s <= per_group && s <= 32; ++s) {
         const int per = (per_group + s - 1) / s;
         const int64_t ctas = (int64_t)cap_chunks * ngroups * s;
         const double c = (double)((ctas + 147) / 148) * (per + 1);
