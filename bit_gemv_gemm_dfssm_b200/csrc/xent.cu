@@ -61,10 +61,12 @@ constexpr int kLgSmem = kLgRing + kLgOut + 2 * kBN * 4 + 256 + 1024;
 
 // -- gradient kernel
 constexpr int kDhA = kBM * 128, kDhB = kBN * 128;      // 64 K values per stage and accumulator
-constexpr int kDhConv = 256;             // converter threads (8 warps), the epilogue afterwards
-constexpr int kDhThreads = 4 * 32 + kDhConv;
-// 4 stages of one A tile and B, or 3 of two and B; barriers; the accumulators' staging rows
-constexpr int kDhSmem = 192 * 1024 + 256 + 8 * 4096 + 1024;
+// 4 stages of one A tile and B, or 3 of two and B. As many converter groups of four warps, so that a group keeps to one
+// stage and its waits for it are one phase apart; they write the accumulators out afterwards.
+constexpr int dh_stages(int nm) { return nm == 1 ? 4 : 3; }
+constexpr int dh_threads(int nm) { return 4 * 32 + 128 * dh_stages(nm); }
+// the stages; barriers; the accumulators' staging rows, 2 KB for each of up to 16 warps
+constexpr int kDhSmem = 192 * 1024 + 256 + 16 * 2048 + 1024;
 
 constexpr int kTokBlock = 2048;          // tokens whose gradient is worked on at a time
 constexpr size_t kGradBytes = 80u << 20; // about the fp16 piece that stays in the 126 MB L2
@@ -451,14 +453,14 @@ struct DhArgs {
     uint32_t* err;
 };
 
-// Warp 0 loads the fp16 gradients by TMA, warps 4..11 turn the table's bytes into the B operand and write the
+// Warp 0 loads the fp16 gradients by TMA, warps 4 and up turn the table's bytes into the B operand and write the
 // accumulators out, warp 1 issues the MMAs. A tile is 128 NM tokens x 256 channels: with NM = 2 (more than
 // 128 tokens) the expanded bytes serve two accumulators, which takes a quarter off the shared-memory traffic per
 // MMA that bounds NM = 1.
 template <int NM>
-__global__ void __launch_bounds__(kDhThreads, 1)
+__global__ void __launch_bounds__(dh_threads(NM), 1)
 xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
-    constexpr int kStages = NM == 1 ? 4 : 3, kA = NM * kDhA, kStage = kA + kDhB;
+    constexpr int kStages = dh_stages(NM), kA = NM * kDhA, kStage = kA + kDhB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + kStages * kStage);         // TMA bytes
@@ -485,11 +487,11 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&full_a[s], 1);
-            ptx::mbar_init(&full_b[s], kDhConv / 64);
+            ptx::mbar_init(&full_b[s], 4);
             ptx::mbar_init(&empty[s], 1);
         }
         ptx::mbar_init(acc_full, 1);
-        ptx::mbar_init(acc_empty, kDhConv / 32);
+        ptx::mbar_init(acc_empty, 4 * kStages);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -564,13 +566,14 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
                     ptx::mbar_wait(&empty[i % kStages], (uint32_t)(i / kStages) & 1u);
         }
     } else if (warp >= 4) {
-        // Converters, two groups of four warps that take turns at the stages (what a stage costs a warp in
-        // latency, from the wait for its release to the fence behind its stores, is then paid side by side). A
+        // Converters, a group of four warps per stage (what a stage costs a warp in latency, from its loads and the wait
+        // for its release to the fence behind its stores, is then paid side by side; two groups with two stages'
+        // loads each: 2,048 tokens 577 us instead of 563, 16 tokens the same 62). A
         // unit is 8 table rows (K) x 128 channels, lane l the channels 4 l .. 4 l + 3; warp w of a group takes the
         // K octets w and w + 4 of the stage, both channel halves. A 16-byte piece holds one channel's 8 K
         // values: row n, piece octet ^ (n & 7) of the 128-byte swizzle. Lane l stores its channels in the
-        // order i = (j + l/2) % 4, so that the 8 lanes of a store phase hit 8 pieces. Two of the group's stages
-        // are in flight. Whole stages take a path without bounds.
+        // order i = (j + l/2) % 4, so that the 8 lanes of a store phase hit 8 pieces. A group's next
+        // stage is in flight behind it. Whole stages take a path without bounds.
         const int w = (warp - 4) & 3, group = (warp - 4) >> 2;
         uint32_t sel[4], off[4];         // off: the thread's pieces of octet 0, first half, in a stage's B tile
 #pragma unroll
@@ -579,8 +582,8 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
             sel[j] = i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12);
             off[j] = nr * 128 + 16 * (nr & 7u);
         }
-        const uint32_t smem_b = ptx::smem_u32(smem) + kA, s_out = ptx::smem_u32(smem) + kStages * kStage + 256 + (warp - 4) * 4096;
-        const int q4 = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t smem_b = ptx::smem_u32(smem) + kA, s_out = ptx::smem_u32(smem) + kStages * kStage + 256 + (warp - 4) * 2048;
+        const int q4 = warp & 3;
         const uint32_t d32 = (uint32_t)a.d;
         int seg = 0, it0 = 0;            // segments done; stages of all segments before
         bool waited = false;
@@ -590,7 +593,7 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
             const bool all_c = c0 + kBN <= a.d;
             const int8_t* src = a.table + (int64_t)(a.v0 + 64 * lo + 8 * w) * a.d + c0 + 4 * lane;
             const int left = a.k_total - 64 * lo - 8 * w;        // live rows from the thread's first one on
-            uint32_t x[2][32];           // [stage in flight][octet, half, 8 rows]
+            uint32_t x[32];              // [octet, half, 8 rows]
             auto load = [&](int k, uint32_t* r) {
                 const int8_t* p = src + (int64_t)k * 64 * d32;
                 if (k < n && all_c && 64 * k + 40 <= left) {
@@ -646,17 +649,14 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
                 if (lane == 0) ptx::mbar_arrive(&full_b[st]);
                 return true;
             };
-            const int k0 = (it0 + group) & 1;      // this group's first stage of the segment
-            load(k0, x[0]);
-            load(k0 + 2, x[1]);
-            for (int k = k0; k < n; k += 4) {
-                if (!convert(k, x[0])) return false;
-                load(k + 4, x[0]);
-                if (k + 2 < n && !convert(k + 2, x[1])) return false;
-                load(k + 6, x[1]);
+            const int k0 = (group + kStages - it0 % kStages) % kStages;      // this group's first stage of the segment
+            load(k0, x);
+            for (int k = k0; k < n; k += kStages) {
+                if (!convert(k, x)) return false;
+                load(k + kStages, x);
             }
             it0 += n;
-            // ---- the accumulators: lane quarter warp & 3, channel half (warp - 4) / 4
+            // ---- the accumulators: lane quarter warp & 3, the groups' turns at blocks of 16 columns
             if (!waited) {
                 ptx::pdl_wait();                   // earlier readers of the partial sums
                 waited = true;
@@ -673,28 +673,28 @@ xent_dh_kernel(const __grid_constant__ CUtensorMap map_g, const DhArgs a) {
             }
             const int slot = blockIdx.x - cta_of(a.sp, (uint32_t)tile * a.sp.ns);
 #pragma unroll 1
-            for (int c = 0; c < NM * kBN / 2; c += 32) {
-                const int i = c / (kBN / 2), col = half * (kBN / 2) + c % (kBN / 2);
-                uint32_t r[32];
+            for (int c = 16 * group; c < NM * kBN; c += 16 * kStages) {
+                const int i = c / kBN, col = c % kBN;
+                uint32_t r[16];
                 if (n > 0) {
-                    ptx::tmem_ld_32x32b_x32(tmem + (uint32_t)(256 * i + col) + ((uint32_t)(32 * q4) << 16), r);
+                    ptx::tmem_ld_32x32b_x16(tmem + (uint32_t)(256 * i + col) + ((uint32_t)(32 * q4) << 16), r);
                     ptx::tmem_ld_wait(r);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = 0u;
+                    for (int e = 0; e < 16; ++e) r[e] = 0u;
                 }
-                // through the warp's 4 KB, so that a store covers four whole 128-byte rows
+                // through the warp's 2 KB, so that a store covers 64 bytes of 8 rows
                 __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 4; ++e)
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
-                                 ::"r"(s_out + (uint32_t)(lane * 128 + 16 * (e ^ (lane & 7)))), "r"(r[4 * e]), "r"(r[4 * e + 1]),
-                                 "r"(r[4 * e + 2]), "r"(r[4 * e + 3]) : "memory");
+                                 ::"r"(s_out + (uint32_t)(lane * 64 + 16 * (e ^ ((lane >> 1) & 3)))), "r"(r[4 * e]),
+                                 "r"(r[4 * e + 1]), "r"(r[4 * e + 2]), "r"(r[4 * e + 3]) : "memory");
                 __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int rr = 4 * e + (lane >> 3), pc = lane & 7, t = tok0 + i * kBM + 32 * q4 + rr;
-                    const uint4 v = ptx::lds128(s_out + (uint32_t)(rr * 128 + 16 * (pc ^ (rr & 7))));
+                for (int e = 0; e < 4; ++e) {
+                    const int rr = 8 * e + (lane >> 2), pc = lane & 3, t = tok0 + i * kBM + 32 * q4 + rr;
+                    const uint4 v = ptx::lds128(s_out + (uint32_t)(rr * 64 + 16 * (pc ^ ((rr >> 1) & 3))));
                     if (t < a.m && c0 + col + 4 * pc < a.d)
                         *reinterpret_cast<uint4*>(a.part + ((int64_t)slot * a.m + t) * a.d + c0 + col + 4 * pc) = v;
                 }
@@ -1006,7 +1006,7 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
             e = launch_after(xent_logits_kernel<kGrad>, tiles < sms ? tiles : sms, kLgThreads, kLgSmem, s, mq, me, a);
             const DhArgs b{table->table, d, mb, v0, a.v_end - v0, p.sp, part + (size_t)(v0 / p.piece) * p.slots * mb * d, err};
             if (e == cudaSuccess)
-                e = launch_after(p.nm == 1 ? xent_dh_kernel<1> : xent_dh_kernel<2>, p.sp.ctas, kDhThreads, kDhSmem, s, mg, b);
+                e = launch_after(p.nm == 1 ? xent_dh_kernel<1> : xent_dh_kernel<2>, p.sp.ctas, dh_threads(p.nm), kDhSmem, s, mg, b);
         }
         const int64_t n = (int64_t)mb * (d >> 2);
         if (e == cudaSuccess)
