@@ -24,10 +24,10 @@
 // two with max |s| K in [2^13, 2^14), keeps exp(l - lse) s[v] K below 2^14 and its smallest
 // kept step at 2^-38 max |s|, far below what bf16 output can show. Every order is fixed.
 //
-// Measured, 50,288 x 2048. 2,048 tokens: logits 136 us, 84 % of the tensor pipe (256 columns of kind::i8 take about
-// 200 cycles per 32 bytes of K); gradient 595 us in three pieces of 60 + 147, 55 % of the tensor pipe in the second, whose
+// Measured, 50,288 x 2048. 2,048 tokens: logits 122 to 137 us, 82 to 84 % of the tensor pipe (256 columns of kind::i8 take about
+// 200 cycles per 32 bytes of K); gradient 563 us in three pieces of 56 + 130, 54 % of the tensor pipe in the second, whose
 // bytes-to-fp16 conversion and shared-memory traffic bound it. 1 token: logits 23 us, 4.5 TB/s of the table, the join
-// 6 beside it; 16 tokens: gradient 61 us, the table twice, 24 + 46.
+// 6 beside it; 16 tokens: gradient 62 us, the table twice, 23 + 45.
 #include <cuda_fp16.h>
 
 #include <cmath>
