@@ -372,8 +372,9 @@ dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8_t* q, cons
  *   dh[t] = grad[t] * ( sum_v exp(l[t, v] - lse[t]) scale[v] table[v] - scale[target] table[target] )
  * lse: the forward call's (m fp32); grad: m fp32; dh: m x d bf16 (device, 16-byte aligned). Tokens
  * without a target (see above) get a row of zeros, whatever their sx, lse and grad hold. The
- * probabilities are rounded to fp16 for the product with the table, the sums kept in fp32, the target's
- * row taken off in fp32. */
+ * probabilities are rounded to fp16 for the product with the table, the sums kept in fp32; the target's
+ * factor exp(l - lse) - 1 is not rounded to fp16 (confident tokens, whose factor is near 0, keep their gradient's
+ * relative precision, as far as lse's own fp32 rounding lets it). */
 dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8_t* q, const float* sx,
                             const int32_t* targets, const float* lse, const float* grad, int32_t m, void* dh,
                             void* workspace, size_t workspace_bytes, void* stream);

@@ -221,3 +221,44 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     check(a, n3, l3, d3)
+
+
+def confident(a, left):
+    """`a` with a target of probability 1 - left[i] for token i: the token's largest logit, s_x by bisection in 64 bits."""
+    m = len(left)
+    one = logits64(dict(a, sx=torch.ones(m, device="cuda")))
+    tg = one.argmax(1)
+    gap = (one - one.amax(1, keepdim=True)).scatter_(1, tg[:, None], float("-inf"))
+    lo, hi = torch.zeros(m, dtype=torch.float64, device="cuda"), torch.full((m,), 1e3, dtype=torch.float64, device="cuda")
+    want = torch.tensor(left, dtype=torch.float64, device="cuda")
+    for _ in range(80):
+        mid = (lo + hi) / 2
+        rest = torch.exp(torch.logsumexp(gap * mid[:, None], 1))
+        more = rest / (1 + rest) > want
+        lo, hi = torch.where(more, mid, lo), torch.where(more, hi, mid)
+    return dict(a, tg=tg.to(torch.int32), sx=hi.float())
+
+
+@pytest.mark.parametrize("v,d", [(700, 512), (3000, 64), (50288, 256)])
+def test_gradient_of_confident_tokens(v, d):
+    """Targets of probability 0.9 to 0.99999: what is left of (p - 1) s E, not what cancels in it, sets the room.
+
+    The other rows as at the head of this file, over S' = their sum of p |s E|. The target's factor expm1(l - lse) is off
+    by half a step of its argument, two steps of expm1f and three roundings behind it: below 2^-21 of itself."""
+    left = [0.1, 1e-2, 1e-3, 1e-4, 3e-5, 1e-5]
+    a = confident(inputs(21 + v, len(left), v, d, 0.0), left)
+    _, lse, _ = fwd(a)
+    dh, _ = bwd(a, lse)
+    torch.cuda.synchronize()
+    lg, e, s, t0 = logits64(a), a["table"].double(), a["scale"].double(), a["tg"].long()[:, None]
+    x = lg - lse.double()[:, None]
+    off = torch.expm1(x.gather(1, t0))                                   # p - 1 of the target
+    p = torch.exp(x).scatter_(1, t0, 0.0)
+    hot = off * e[t0[:, 0]] * s[t0]
+    gr = a["grad"].double()[:, None]
+    want = gr * ((p * s) @ e + hot)
+    dp = 2.0 ** -24 * (16 * lg.abs().amax(1) + 8 * lse.double().abs() + 80)[:, None]
+    room = 2.0 ** -8 * want.abs() + gr * (((p * s) @ e.abs()) * (dp + 2.0 ** -11 + 2.0 ** -23 * (v / 16 + 148))
+                                         + 2.0 ** -21 * hot.abs() + 2.0 ** -38 * s.max() * 128 * v)
+    err = (dh.double() - want).abs()
+    assert (err <= room).all(), [f"{float(r):.3g}" for r in err.norm(dim=1) / want.norm(dim=1)]
