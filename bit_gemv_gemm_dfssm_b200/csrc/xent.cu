@@ -12,7 +12,8 @@
 // multiplied:
 //   kLse   one thread holds one token's row of the tile: running maximum and sum of 2^(l log2 e -
 //          max) over 128 columns, one (max, sum) pair per token and half tile to the workspace;
-//          xent_lse_kernel joins the pairs of a token and takes the target's logit by a dp4a dot;
+//          xent_lse_kernel joins the pairs of a token and takes the target's logit by a dp4a dot, which nll =
+//          log sum exp(l - l[target]) is formed from (a small loss keeps its digits beside large logits);
 //   kGrad  g = exp(l - lse) s[v] K as fp16 to the workspace, for a piece of the vocabulary, with 0 in the target's
 //          column, whose factor exp(l - lse) - 1 goes to the workspace in fp32.
 // xent_dh_kernel multiplies such a piece with its rows of the table (kind::f16): the table's
@@ -98,6 +99,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// A logit in units of log 2, of the exact sum as fp32: rounded alike wherever it is formed
+__device__ __forceinline__ float logit_unit(float sx) { return __fmul_rn(sx, kLog2e); }
+__device__ __forceinline__ float logit2(float dot, float scale, float unit) { return __fmul_rn(__fmul_rn(dot, scale), unit); }
 
 __device__ __forceinline__ bool is_token(int target, int vocab) { return target >= 0 && target < vocab; }
 
@@ -242,7 +247,7 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             sc[e] = e < a.bn && vbase + e < a.v_end ? a.scale[vbase + e] : 0.0f;
             const int t = tt * kBM + 32 * q4 + lane;
             const bool live = t < a.m;
-            const float k2 = live ? __fmul_rn(a.sx[t], kLog2e) : 0.0f;      // logits in units of log 2
+            const float k2 = live ? logit_unit(a.sx[t]) : 0.0f;
             float lse2 = 0.0f;
             bool counted = live;
             int target = -1;
@@ -277,10 +282,10 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     const float4 s4 = *reinterpret_cast<const float4*>(sc + col + i);
-                    z[i] = __fmul_rn(__fmul_rn((float)(int)r[i], s4.x), k2);
-                    z[i + 1] = __fmul_rn(__fmul_rn((float)(int)r[i + 1], s4.y), k2);
-                    z[i + 2] = __fmul_rn(__fmul_rn((float)(int)r[i + 2], s4.z), k2);
-                    z[i + 3] = __fmul_rn(__fmul_rn((float)(int)r[i + 3], s4.w), k2);
+                    z[i] = logit2((float)(int)r[i], s4.x, k2);
+                    z[i + 1] = logit2((float)(int)r[i + 1], s4.y, k2);
+                    z[i + 2] = logit2((float)(int)r[i + 2], s4.z, k2);
+                    z[i + 3] = logit2((float)(int)r[i + 3], s4.w, k2);
                 }
                 if (MODE == kLse) {
                     if (c + 32 > c_end) {
@@ -417,10 +422,18 @@ __global__ void __launch_bounds__(256) xent_lse_kernel(const float2* __restrict_
         }
     }
     if (lane != 0 || !live) return;
-    const float lse = __fmul_rn(__fadd_rn(mx, log2f(sum)), kLn2);
-    float loss = 0.0f;
-    if (is_token(tg, vocab)) loss = __fsub_rn(lse, __fmul_rn(sx[t], __fmul_rn(scale[tg], (float)acc)));
-    else if (tg != DFSSM_IGNORE_TARGET) atomicOr(err, DFSSM_DEVERR_TOKEN_ID);
+    const float more = log2f(sum);
+    float lse = __fmul_rn(__fadd_rn(mx, more), kLn2), loss = 0.0f;
+    if (is_token(tg, vocab)) {
+        // The target's logit with the roundings of its column: of the token's largest one, nothing is left but the
+        // logarithm of the sum (lse - l, each rounded at its own size, would cancel). lse is then that much above the
+        // exact logit.
+        const float top = logit2((float)acc, scale[tg], logit_unit(sx[t]));
+        loss = __fmul_rn(__fadd_rn(__fsub_rn(mx, top), more), kLn2);
+        if (top == mx) lse = (float)((double)acc * (double)scale[tg] * (double)sx[t] + (double)loss);
+    } else if (tg != DFSSM_IGNORE_TARGET) {
+        atomicOr(err, DFSSM_DEVERR_TOKEN_ID);
+    }
     nll[t] = loss;
     lse_out[t] = lse;
 }

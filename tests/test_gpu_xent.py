@@ -262,3 +262,32 @@ def test_gradient_of_confident_tokens(v, d):
                                          + 2.0 ** -21 * hot.abs() + 2.0 ** -38 * s.max() * 128 * v)
     err = (dh.double() - want).abs()
     assert (err <= room).all(), [f"{float(r):.3g}" for r in err.norm(dim=1) / want.norm(dim=1)]
+
+
+@pytest.mark.parametrize("v,d", [(700, 512), (3000, 2048)])
+def test_loss_of_confident_tokens_with_large_logits(v, d):
+    """Logits in the hundreds (the target's row has a near twin), losses of 1e-1 to 1e-4: the logits' own roundings do
+    not reach them.
+
+    The target's logit is the running maximum, bit for bit, so nll is the logarithm of 1 plus the others' share 1 - p,
+    which is off by the differences of two logits (16 2^-24 L) and 80 2^-24 of itself; the sums and joins round as at
+    the head of this file, 2^-24 of about 1 each; the logarithm and its factor 2^-22 of the loss. lse is the target's
+    logit in 64 bits plus that, rounded once."""
+    left = [0.1, 1e-2, 1e-3, 3e-4, 1e-4]
+    a = inputs(40 + v, len(left), v, d, 0.0)
+    top = logits64(dict(a, sx=torch.ones(len(left), device="cuda"))).argmax(1)
+    twin = (top + v // 2) % v
+    assert torch.cat([top, twin]).unique().numel() == 2 * len(left)
+    a["table"][twin] = a["table"][top]
+    a["scale"][twin] = a["scale"][top] * (1 - 2.0 ** -6)
+    a = confident(a, left)
+    nll, lse, _ = fwd(a)
+    torch.cuda.synchronize()
+    lg, t0 = logits64(a), a["tg"].long()[:, None]
+    hit = lg.gather(1, t0)[:, 0]
+    rest = torch.exp(torch.logsumexp(lg.scatter(1, t0, float("-inf")) - hit[:, None], 1))
+    want = torch.log1p(rest)
+    room = 2.0 ** -24 * (rest * (16 * lg.abs().amax(1) + 80) + 64 + 3 * (v / 4096 + 8)) + 2.0 ** -22 * want
+    err = (nll.double() - want).abs()
+    assert (err <= room).all(), [f"{float(r):.3g}" for r in err / want]
+    assert ((lse.double() - (hit + want)).abs() <= room + 2.0 ** -24 * (hit + want).abs()).all()
