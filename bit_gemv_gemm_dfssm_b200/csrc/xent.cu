@@ -100,8 +100,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// An infinite scale would drop out of a softmax where its row's sum is negative, and zero rows of others: NaN shows in all
+__device__ __forceinline__ float finite_or_nan(float v) {
+    return (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : v;
+}
+
 // A logit in units of log 2, of the exact sum as fp32: rounded alike wherever it is formed
-__device__ __forceinline__ float logit_unit(float sx) { return __fmul_rn(sx, kLog2e); }
+__device__ __forceinline__ float logit_unit(float sx) { return __fmul_rn(finite_or_nan(sx), kLog2e); }
 __device__ __forceinline__ float logit2(float dot, float scale, float unit) { return __fmul_rn(__fmul_rn(dot, scale), unit); }
 
 __device__ __forceinline__ bool is_token(int target, int vocab) { return target >= 0 && target < vocab; }
@@ -244,7 +249,7 @@ xent_logits_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const int buf = tc & 1;
             const int vbase = a.v0 + vt * a.bn;
             float* sc = s_scale + buf * kBN;
-            sc[e] = e < a.bn && vbase + e < a.v_end ? a.scale[vbase + e] : 0.0f;
+            sc[e] = e < a.bn && vbase + e < a.v_end ? finite_or_nan(a.scale[vbase + e]) : 0.0f;
             const int t = tt * kBM + 32 * q4 + lane;
             const bool live = t < a.m;
             const float k2 = live ? logit_unit(a.sx[t]) : 0.0f;
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(256) xent_lse_kernel(const float2* __restrict_
         // The target's logit with the roundings of its column: of the token's largest one, nothing is left but the
         // logarithm of the sum (lse - l, each rounded at its own size, would cancel). lse is then that much above the
         // exact logit.
-        const float top = logit2((float)acc, scale[tg], logit_unit(sx[t]));
+        const float top = logit2((float)acc, finite_or_nan(scale[tg]), logit_unit(sx[t]));
         loss = __fmul_rn(__fadd_rn(__fsub_rn(mx, top), more), kLn2);
         if (top == mx) lse = (float)((double)acc * (double)scale[tg] * (double)sx[t] + (double)loss);
     } else if (tg != DFSSM_IGNORE_TARGET) {

@@ -353,7 +353,8 @@ dfssm_status dfssm_add_rmsnorm_bwd(const float* norm_w, int32_t d, float eps, co
  * table: HOST struct of device pointers as for dfssm_lm_head_fwd; 1 <= m <= 65536.
  * A target of DFSSM_IGNORE_TARGET gives nll 0 (lse is written); any other target outside [0, vocab)
  * is treated the same and sets DFSSM_DEVERR_TOKEN_ID in the workspace's error word. A non-finite sx
- * or scale makes nll and lse of the tokens it reaches NaN and leaves the other tokens alone.
+ * makes its token's lse and nll NaN and leaves the other tokens alone; a non-finite scale (Inf of either sign, NaN)
+ * makes all tokens' NaN. The nll of a token without a target is 0 all the same.
  *
  * workspace: 256-byte aligned device memory of at least dfssm_xent_workspace_bytes (backward: 0 for
  * _fwd, 1 for _bwd), zeroed once before its first use. Its first 4 bytes are a device error word
@@ -371,7 +372,8 @@ dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8_t* q, cons
  * (straight through the quantiser):
  *   dh[t] = grad[t] * ( sum_v exp(l[t, v] - lse[t]) scale[v] table[v] - scale[target] table[target] )
  * lse: the forward call's (m fp32); grad: m fp32; dh: m x d bf16 (device, 16-byte aligned). Tokens
- * without a target (see above) get a row of zeros, whatever their sx, lse and grad hold. The
+ * without a target (see above) get a row of zeros, whatever their sx, lse and grad hold; a non-finite sx or scale makes
+ * the rows of the others that it reaches (as above) NaN. The
  * probabilities are rounded to fp16 for the product with the table, the sums kept in fp32; the target's
  * factor exp(l - lse) - 1 is not rounded to fp16 (confident tokens, whose factor is near 0, keep their gradient's
  * relative precision, as far as lse's own fp32 rounding lets it). */

@@ -291,3 +291,23 @@ def test_loss_of_confident_tokens_with_large_logits(v, d):
     err = (nll.double() - want).abs()
     assert (err <= room).all(), [f"{float(r):.3g}" for r in err / want]
     assert ((lse.double() - (hit + want)).abs() <= room + 2.0 ** -24 * (hit + want).abs()).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_scale_that_is_not_finite_shows_in_every_token(bad):
+    """... whatever the sign of its row's sums; an s_x in its own token."""
+    a = inputs(14, 140, 900, 256)
+    a["scale"][300] = bad
+    nll, lse, _ = fwd(a)
+    dh, _ = bwd(a, lse)
+    b = inputs(14, 140, 900, 256)
+    b["sx"][7] = bad
+    b["tg"][7] = 5
+    b["q"][7] = b["q"][7].abs().clamp(1, 127)
+    b["table"] = -b["table"].clamp(-127, 127).abs().clamp(min=1)         # every sum of token 7 below 0
+    nll2, lse2, _ = fwd(b)
+    torch.cuda.synchronize()
+    on = a["tg"] >= 0
+    assert torch.isnan(lse).all() and torch.isnan(nll[on]).all() and (nll[~on] == 0).all()
+    assert torch.isnan(dh[on]).all() and (dh[~on] == 0).all()
+    assert torch.isnan(lse2[7]) and torch.isnan(nll2[7]) and torch.isfinite(lse2[8:]).all()
