@@ -73,7 +73,10 @@ constexpr int dh_threads(int nm) { return 4 * 32 + 128 * dh_stages(nm); }
 // the stages; barriers; the accumulators' staging rows, 2 KB for each of up to 16 warps
 constexpr int kDhSmem = 192 * 1024 + 256 + 16 * 2048 + 1024;
 
-constexpr int kTokBlock = 2048;          // tokens whose gradient is worked on at a time
+// Most tokens whose gradient is worked on at a time: with them the piece of g that stays in the L2 is 20,480 rows of the
+// table wide, and a product of that many tokens is bound by the tensor cores' side, not by the table
+constexpr int kTokBlock = 2048;
+constexpr int kTokTile = 256;            // the blocks' sizes are multiples of it
 constexpr size_t kGradBytes = 80u << 20; // about the fp16 piece that stays in the 126 MB L2
 
 struct LogitsArgs {
@@ -827,33 +830,48 @@ static_assert(kBNFew >= kBM && kBNFew % 8 == 0, "the 128 rows that a product rea
 
 int tile_rows(int m) { return m <= kBM ? kBNFew : kBN; }
 
-// How a gradient call is cut: token blocks, vocabulary pieces, the product's units over the CTAs.
+// How a gradient call is cut: the tokens into blocks of nearly equal numbers of 256-token tiles, each with a product of its own
+// size (blocks of 2,048 and a last one that ran the same product for what was left: 2,049 tokens 1,055 us, now 657, 3,000
+// 1,048, now 870); the vocabulary into pieces; a block's product into units over the CTAs.
 struct DhPlan {
-    int tok_block;      // tokens per block
+    int blocks;
+    int tok_block;      // tokens of the first block, the largest
     int pieces;
     int piece;          // table rows per piece (a multiple of the logits' tile and of 64)
     int nm;             // 128-token accumulators per CTA
-    DhSplit sp;
-    int slots;          // partial sums a tile can have
 };
 
-DhPlan dh_plan(int m, int vocab, int d) {
+// tokens in front of block i
+int block_begin(int m, int blocks, int i) {
+    const int tiles = (m + kTokTile - 1) / kTokTile;
+    const int64_t t = (int64_t)kTokTile * (tiles / blocks * i + (i < tiles % blocks ? i : tiles % blocks));
+    return t < m ? (int)t : m;
+}
+
+DhPlan dh_plan(int m, int vocab) {
     DhPlan p;
-    p.tok_block = m < kTokBlock ? m : kTokBlock;
+    p.blocks = (m + kTokBlock - 1) / kTokBlock;
+    p.tok_block = block_begin(m, p.blocks, 1);
     const int bn = tile_rows(p.tok_block), all = (vocab + bn - 1) / bn;
     const int most = (int)(kGradBytes / ((size_t)p.tok_block * 2 * bn));       // tiles of the largest piece
     p.pieces = (all + most - 1) / most;
     p.piece = (all + p.pieces - 1) / p.pieces * bn;
     p.nm = p.tok_block > kBM ? 2 : 1;
-    p.sp.n_ct = (d + kBN - 1) / kBN;
-    p.sp.ns = p.piece / 64;
-    // at most 8 x 32 tiles of at most 2^18 units
-    const uint32_t units = (uint32_t)((p.tok_block + p.nm * kBM - 1) / (p.nm * kBM)) * p.sp.n_ct * p.sp.ns;
-    p.sp.ctas = units / 8 < 1 ? 1 : units / 8 < (uint32_t)kSms ? (int)(units / 8) : kSms;        // 8 units at least
-    p.sp.share = units / p.sp.ctas;
-    p.sp.more = units % p.sp.ctas;
-    p.slots = (int)((p.sp.ns + p.sp.share - 1) / p.sp.share) + 1;
     return p;
+}
+
+// The units of a block of mb tokens over the CTAs, and the partial sums that a tile can have
+DhSplit dh_split(const DhPlan& p, int mb, int d, int* slots) {
+    DhSplit sp;
+    sp.n_ct = (d + kBN - 1) / kBN;
+    sp.ns = p.piece / 64;
+    // at most 8 x 32 tiles of at most 2^18 units
+    const uint32_t units = (uint32_t)((mb + p.nm * kBM - 1) / (p.nm * kBM)) * sp.n_ct * sp.ns;
+    sp.ctas = units / 8 < 1 ? 1 : units / 8 < (uint32_t)kSms ? (int)(units / 8) : kSms;        // 8 units at least
+    sp.share = units / sp.ctas;
+    sp.more = units % sp.ctas;
+    *slots = (int)((sp.ns + sp.share - 1) / sp.share) + 1;
+    return sp;
 }
 
 struct XentWs {
@@ -866,7 +884,7 @@ XentWs xent_ws(int m, int vocab, int d, bool backward) {
         w.part = o;
         o = up256(o + (size_t)2 * ((vocab + tile_rows(m) - 1) / tile_rows(m)) * m * sizeof(float2));
     } else {
-        const DhPlan p = dh_plan(m, vocab, d);
+        const DhPlan p = dh_plan(m, vocab);
         w.smax = o;
         o += 256;
         w.hit = o;
@@ -874,7 +892,14 @@ XentWs xent_ws(int m, int vocab, int d, bool backward) {
         w.g = o;
         o = up256(o + (size_t)p.tok_block * p.piece * sizeof(__half));
         w.dh = o;
-        o = up256(o + (size_t)p.pieces * p.slots * p.tok_block * d * sizeof(float));
+        size_t rows = 0;                                  // a smaller block's tiles can have more slots
+        for (int i = 0; i < p.blocks; ++i) {
+            const int mb = block_begin(m, p.blocks, i + 1) - block_begin(m, p.blocks, i);
+            int slots;
+            dh_split(p, mb, d, &slots);
+            rows = rows > (size_t)slots * mb ? rows : (size_t)slots * mb;
+        }
+        o = up256(o + p.pieces * rows * d * sizeof(float));
     }
     w.total = o;
     return w;
@@ -1011,15 +1036,17 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
     float* hit = reinterpret_cast<float*>(ws + w.hit);
     __half* g = reinterpret_cast<__half*>(ws + w.g);
     float* part = reinterpret_cast<float*>(ws + w.dh);
-    const DhPlan p = dh_plan(m, vocab, d);
+    const DhPlan p = dh_plan(m, vocab);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap me;
     const int bn = tile_rows(p.tok_block);
     if (!encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, bn)) return DFSSM_ERR_CUDA;
     xent_smax_kernel<<<1, 1024, 0, s>>>(table->scale, vocab, smax);
     cudaError_t e = cudaGetLastError();
-    for (int t0 = 0; t0 < m && e == cudaSuccess; t0 += p.tok_block) {
-        const int mb = m - t0 < p.tok_block ? m - t0 : p.tok_block;
+    for (int i = 0; i < p.blocks && e == cudaSuccess; ++i) {
+        const int t0 = block_begin(m, p.blocks, i), mb = block_begin(m, p.blocks, i + 1) - t0;
+        int slots;
+        const DhSplit sp = dh_split(p, mb, d, &slots);
         CUtensorMap mq, mg;
         if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q + (int64_t)t0 * d, d, mb, d, stage_tokens(mb)) ||
             !encode_rows(&mg, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, g, p.piece, mb, p.piece, kBM))
@@ -1046,13 +1073,13 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
             a.err = err;
             const int tiles = n_tt * ((a.v_end - v0 + bn - 1) / bn);
             e = launch_after(xent_logits_kernel<kGrad>, tiles < sms ? tiles : sms, kLgThreads, kLgSmem, s, mq, me, a);
-            const DhArgs b{table->table, d, mb, v0, a.v_end - v0, p.sp, part + (size_t)(v0 / p.piece) * p.slots * mb * d, err};
+            const DhArgs b{table->table, d, mb, v0, a.v_end - v0, sp, part + (size_t)(v0 / p.piece) * slots * mb * d, err};
             if (e == cudaSuccess)
-                e = launch_after(p.nm == 1 ? xent_dh_kernel<1> : xent_dh_kernel<2>, p.sp.ctas, dh_threads(p.nm), kDhSmem, s, mg, b);
+                e = launch_after(p.nm == 1 ? xent_dh_kernel<1> : xent_dh_kernel<2>, sp.ctas, dh_threads(p.nm), kDhSmem, s, mg, b);
         }
         const int64_t n = (int64_t)mb * (d >> 2);
         if (e == cudaSuccess)
-            e = launch_after(xent_dh_out_kernel, (int)((n + 255) / 256), 256, 0, s, part, p.sp, p.pieces, p.slots, p.nm * kBM, table->table,
+            e = launch_after(xent_dh_out_kernel, (int)((n + 255) / 256), 256, 0, s, part, sp, p.pieces, slots, p.nm * kBM, table->table,
                              table->scale, vocab, d, targets + t0, grad + t0, mb, smax, hit,
                              static_cast<uint16_t*>(dh) + (int64_t)t0 * d, err);
     }

@@ -311,3 +311,14 @@ def test_a_scale_that_is_not_finite_shows_in_every_token(bad):
     assert torch.isnan(lse).all() and torch.isnan(nll[on]).all() and (nll[~on] == 0).all()
     assert torch.isnan(dh[on]).all() and (dh[~on] == 0).all()
     assert torch.isnan(lse2[7]) and torch.isnan(nll2[7]) and torch.isfinite(lse2[8:]).all()
+
+
+@pytest.mark.parametrize("m,v,d", [(2049, 300, 272), (2300, 33000, 64), (4100, 1000, 16), (4096, 21000, 32)])
+def test_token_blocks_of_unequal_size_and_vocabulary_pieces(m, v, d):
+    """More tokens than one block holds, the last block short, with one and with two pieces of the vocabulary."""
+    a = inputs(m + v, m, v, d)
+    nll, lse, _ = fwd(a)
+    dh, ws = bwd(a, lse)
+    torch.cuda.synchronize()
+    check(a, nll, lse, dh)
+    assert dfssm.dfssm_ssm_read_error(ws.data_ptr(), stream()) == (dfssm.DFSSM_OK, 0)
