@@ -49,10 +49,6 @@ namespace {
 
 constexpr int kBM = 128;                 // tokens per tile (TMEM lanes)
 constexpr int kBN = 256;                 // table rows (logits) or channels (gradient) per tile
-// With one token tile the table is streamed once and a call has few tiles: 192 rows give 262 tiles for 50,288 rows,
-// two for nearly each of 148 CTAs, where 256 rows give 197, two for a third of them, and 128 rows 393, three for two
-// thirds (1 token: 20.2 us; with 256 rows 21.8, with 128 rows 21.1).
-constexpr int kBNFew = 192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -73,8 +69,8 @@ constexpr int dh_threads(int nm) { return 4 * 32 + 128 * dh_stages(nm); }
 // the stages; barriers; the accumulators' staging rows, 2 KB for each of up to 16 warps
 constexpr int kDhSmem = 192 * 1024 + 256 + 16 * 2048 + 1024;
 
-// Most tokens whose gradient is worked on at a time: with them the piece of g that stays in the L2 is 20,480 rows of the
-// table wide, and a product of that many tokens is bound by the tensor cores' side, not by the table
+// Most tokens whose gradient is worked on at a time (8,192 tokens x 50,288 x 2048, the best of 30 calls: 2,294 us, with 1,024
+// 2,403, with 4,096 2,333; the workspace grows with it)
 constexpr int kTokBlock = 2048;
 constexpr int kTokTile = 256;            // the blocks' sizes are multiples of it
 constexpr size_t kGradBytes = 80u << 20; // about the fp16 piece that stays in the 126 MB L2
@@ -83,7 +79,7 @@ struct LogitsArgs {
     const float* scale;
     const float* sx;
     int vocab, d, m;
-    int bn;                              // table rows per tile: kBN or kBNFew
+    int bn;                              // table rows per tile: kBN, or one of kBNFew
     int a_bytes, stages;                 // of a stage: the tokens' rows; how many stages
     int v0, v_end;                       // table rows of this call
     float2* part;                        // kLse: [2 * v tiles][m]
@@ -826,9 +822,19 @@ int stage_count(int a_bytes, int bn) {
     const int n = kLgRing / (a_bytes + bn * 128);
     return n < kLgStages ? n : kLgStages;
 }
-static_assert(kBNFew >= kBM && kBNFew % 8 == 0, "the 128 rows that a product reads as tokens lie in the stage");
+constexpr int kBNFew[2] = {128, 192};
+static_assert(kBNFew[0] >= kBM, "the 128 rows that a product reads as tokens lie in the stage");
 
-int tile_rows(int m) { return m <= kBM ? kBNFew : kBN; }
+// Table rows per tile. With one token tile the table is streamed once and a call has few tiles: the size that leaves the
+// longest CTA the fewest rows, 128 where that is the same (its last epilogue is the shorter one; 256 never leaves
+// fewer). Calls back to back over tables of 2048 channels, 1 token, with 128 / 192 / 256 rows, us: 8,000 rows 10.1 / 10.7 /
+// 12.2, 32,000 16.9 / 19.8 / 17.0, 37,888 18.4 / 21.0 / 19.9, 50,288 23.0 / 22.7 / 25.4, 65,536 27.6 / 28.3 / 28.7, 128,256
+// 47.1 / 48.2 / 48.4.
+int tile_rows(int m, int vocab) {
+    if (m > kBM) return kBN;
+    auto longest = [&](int bn) { return ((vocab + bn - 1) / bn + kSms - 1) / kSms * bn; };
+    return longest(kBNFew[1]) < longest(kBNFew[0]) ? kBNFew[1] : kBNFew[0];
+}
 
 // How a gradient call is cut: the tokens into blocks of nearly equal numbers of 256-token tiles, each with a product of its own
 // size (blocks of 2,048 and a last one that ran the same product for what was left: 2,049 tokens 1,055 us, now 657, 3,000
@@ -852,7 +858,7 @@ DhPlan dh_plan(int m, int vocab) {
     DhPlan p;
     p.blocks = (m + kTokBlock - 1) / kTokBlock;
     p.tok_block = block_begin(m, p.blocks, 1);
-    const int bn = tile_rows(p.tok_block), all = (vocab + bn - 1) / bn;
+    const int bn = tile_rows(p.tok_block, vocab), all = (vocab + bn - 1) / bn;
     const int most = (int)(kGradBytes / ((size_t)p.tok_block * 2 * bn));       // tiles of the largest piece
     p.pieces = (all + most - 1) / most;
     p.piece = (all + p.pieces - 1) / p.pieces * bn;
@@ -882,7 +888,7 @@ XentWs xent_ws(int m, int vocab, int d, bool backward) {
     size_t o = 256;                                       // error word
     if (!backward) {
         w.part = o;
-        o = up256(o + (size_t)2 * ((vocab + tile_rows(m) - 1) / tile_rows(m)) * m * sizeof(float2));
+        o = up256(o + (size_t)2 * ((vocab + tile_rows(m, vocab) - 1) / tile_rows(m, vocab)) * m * sizeof(float2));
     } else {
         const DhPlan p = dh_plan(m, vocab);
         w.smax = o;
@@ -986,7 +992,7 @@ extern "C" dfssm_status dfssm_xent_fwd(const dfssm_int8_table* table, const int8
     uint32_t* err = reinterpret_cast<uint32_t*>(ws);
     float2* part = reinterpret_cast<float2*>(ws + w.part);
     CUtensorMap mq, me;
-    const int bn = tile_rows(m);
+    const int bn = tile_rows(m, vocab);
     if (!encode_rows(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q, d, m, d, stage_tokens(m)) ||
         !encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, bn))
         return DFSSM_ERR_CUDA;
@@ -1039,7 +1045,7 @@ extern "C" dfssm_status dfssm_xent_bwd(const dfssm_int8_table* table, const int8
     const DhPlan p = dh_plan(m, vocab);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap me;
-    const int bn = tile_rows(p.tok_block);
+    const int bn = tile_rows(p.tok_block, vocab);
     if (!encode_rows(&me, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, table->table, d, vocab, d, bn)) return DFSSM_ERR_CUDA;
     xent_smax_kernel<<<1, 1024, 0, s>>>(table->scale, vocab, smax);
     cudaError_t e = cudaGetLastError();

@@ -322,3 +322,14 @@ def test_token_blocks_of_unequal_size_and_vocabulary_pieces(m, v, d):
     torch.cuda.synchronize()
     check(a, nll, lse, dh)
     assert dfssm.dfssm_ssm_read_error(ws.data_ptr(), stream()) == (dfssm.DFSSM_OK, 0)
+
+
+@pytest.mark.parametrize("m", [1, 100])
+@pytest.mark.parametrize("v", [18944, 18945, 28120, 38000, 80000])
+def test_tile_sizes_of_few_tokens(m, v):
+    """Vocabularies on both sides of the rule that picks the tiles' rows, one of them exactly one tile per SM."""
+    a = inputs(m + v, m, v, 48)
+    nll, lse, _ = fwd(a)
+    dh, _ = bwd(a, lse)
+    torch.cuda.synchronize()
+    check(a, nll, lse, dh)
