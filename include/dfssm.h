@@ -357,9 +357,11 @@ dfssm_status dfssm_add_rmsnorm_bwd(const float* norm_w, int32_t d, float eps, co
  * makes all tokens' NaN. The nll of a token without a target is 0 all the same.
  *
  * workspace: 256-byte aligned device memory of at least dfssm_xent_workspace_bytes (backward: 0 for
- * _fwd, 1 for _bwd), zeroed once before its first use. Its first 4 bytes are a device error word
- * (DFSSM_DEVERR_TOKEN_ID, DFSSM_DEVERR_TIMEOUT), read and cleared by dfssm_ssm_read_error; nothing else
- * is kept between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call
+ * _fwd, 1 for _bwd), zeroed once before its first use. Backward it holds, for at most 2,048 tokens at a time,
+ * up to 80 MB of fp16 probabilities and, for each such piece of the vocabulary, four to six fp32 partial sums of the
+ * tokens x d: it grows with vocab x d (2,048 tokens: 0.27 GB at 50,288 x 2048, 1.4 GB at 256,000 x 4096).
+ * Its first 4 bytes are a device error word (DFSSM_DEVERR_TOKEN_ID, DFSSM_DEVERR_TIMEOUT), read and cleared by
+ * dfssm_ssm_read_error; nothing else is kept between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call
  * on a device sets kernel attributes (make it before any stream capture). Results repeat bit for bit. */
 #define DFSSM_IGNORE_TARGET (-100)
 dfssm_status dfssm_xent_workspace_bytes(const dfssm_int8_table* table, int32_t m, int32_t backward,
@@ -404,7 +406,8 @@ typedef struct {
  *   dt_bias, a_log, d_skip  nheads fp32;
  *   init_state  nseq x nheads x headdim x d_state fp32 (the layout of dfssm_ssm_layer.ssm_state), or NULL: zeros;
  *   cu_seqlens  nseq + 1 int32: sequence i has the token rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (any
- *               length, 0 included); rows of no sequence are neither read nor written. */
+ *               length, 0 included); rows of no sequence are not written, and what they hold
+ *               reaches no result (rows behind a sequence's end may be read, up to its last chunk's). */
 typedef struct {
     const void* x;
     int64_t x_stride;
@@ -436,8 +439,8 @@ dfssm_status dfssm_ssm_scan_workspace_bytes(const dfssm_scan_dims* dims, int32_t
  * y overlaps no input.
  * workspace: 256-byte aligned, at least dfssm_ssm_scan_workspace_bytes, zeroed once before its first use.
  * Its first 4 bytes are a device error word (DFSSM_DEVERR_SEQLENS: a sequence whose offsets are negative,
- * descending or beyond total is skipped), read and cleared by dfssm_ssm_read_error; nothing else is kept
- * between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call on a device
+ * descending or beyond total is skipped; DFSSM_DEVERR_TIMEOUT: an in-kernel wait of a forward call gave up), read
+ * and cleared by dfssm_ssm_read_error; nothing else is kept between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call on a device
  * sets kernel attributes (make it before any stream capture). Results repeat bit for bit. */
 dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
                                 int32_t nseq, void* y, int64_t y_stride, float* final_state, void* workspace,
@@ -464,7 +467,8 @@ typedef struct {
 
 /* The gradient of sum(dy y) + sum(dfinal_state final_state) with respect to every input. dy: bf16 as y;
  * dfinal_state: as final_state, or NULL (zeros). Nothing of the forward call is needed; the states are
- * computed again and kept in the workspace (64 KB per 64 tokens and head). No gradient overlaps an input or dy.
+ * computed again and kept in the workspace (64 KB per 64 tokens and head: 64 heads, 64 KB per token, so that the
+ * device's memory ends a call's tokens long before 2^22). No gradient overlaps an input or dy.
  * Errors and limits as for dfssm_ssm_scan_fwd (with backward = 1). */
 dfssm_status dfssm_ssm_scan_bwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
                                 int32_t nseq, const void* dy, int64_t dy_stride, const float* dfinal_state,
