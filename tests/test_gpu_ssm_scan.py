@@ -431,3 +431,32 @@ def test_repeatable_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     check_fwd(b, y3, fin3)
     check_bwd(b, r3)
+
+
+@pytest.mark.parametrize("dt0,spread", [((1.0, 30.0), 3.0), ((0.3, 3.0), 1.0), ((1e-6, 1e-5), 0.1)])
+def test_fast_and_slow_decays_of_long_calls(dt0, spread):
+    """The same in chunks of 128 tokens, whose decays off the diagonal are products of two (a chunk of twice the tokens has
+    at most twice the exponent c of two of 64, at 2^-21 of it, within the 2^-20 c of the bound)."""
+    a = inputs(17, [700, 0, 131, 300], 4, 2, True, 3, dt0, spread)
+    y, fin, _ = run_fwd(a)
+    torch.cuda.synchronize()
+    check_fwd(a, y, fin)
+
+
+@pytest.mark.parametrize("lens", [[40, 3, 0, 65], [300, 1, 0, 200], [1700, 30]])
+def test_rows_of_no_sequence_reach_no_result(lens):
+    """NaN in front of the first sequence and behind the last, in every input: the results are the same bits as beside
+    other rows, and the rows are not written."""
+    a = inputs(18, lens, 2, 1, True, 150)
+    a["cu"] += 70                                        # 70 rows in front, 80 behind
+    used = torch.zeros(a["total"], dtype=torch.bool, device="cuda")
+    used[70:70 + sum(lens)] = True
+    b = {**a, **{k: a[k].clone() for k in ("row", "z", "dy")}}
+    for k in ("row", "z", "dy"):
+        b[k][~used] = float("nan")
+    (y, fin, _), (y2, fin2, _) = run_fwd(a), run_fwd(b)
+    (r, _), (r2, _) = run_bwd(a), run_bwd(b)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(fin, fin2) and (y2[~used] == 77).all()
+    for k in r:
+        assert torch.equal(r[k], r2[k]) and torch.isfinite(r2[k]).all(), k
