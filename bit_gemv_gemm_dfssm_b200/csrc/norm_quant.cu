@@ -20,8 +20,9 @@
 // rows; one partial row per CTA goes to the workspace and a second kernel adds the partials.
 // Every order of summation is fixed by m and d.
 //
-// Measured, 16,384 x 2048 with a bf16 delta: forward 66 us, 6.6 TB/s; gradient with dw 79 + 7 us, 6.0 TB/s. One token:
-// the launch, 2.4 us in a graph, 5 us with the gradient's two.
+// Measured, 16,384 x 2048 with a bf16 delta: forward 72 us with the L2 flushed before it, 6.1 TB/s (66 back to back from a
+// graph, where the next call overwrites what is still in the L2); gradient with dw 88 us, 5.3 TB/s (84). One token: the
+// launch, 2.4 us in a graph, 5 us with the gradient's two.
 #include <cmath>
 #include <cstdint>
 
@@ -34,7 +35,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 8192;
-constexpr int kBwdCtasPerSm = 3;                   // what the registers of the usual widths allow
+// CTAs of the gradient per SM: what the registers allow up to 256 and for 1,025 to 2,048 channels (80 to 89 of them). Where a
+// thread holds more pieces of a row (124 to 254 registers) one or two CTAs fit, and the grid goes in two or three turns.
+constexpr int kBwdCtasPerSm = 3;
 constexpr int kBwdMaxCtas = 148 * kBwdCtasPerSm;   // partial rows of dw in the workspace
 
 __device__ __forceinline__ void load8(const float* p, float v[8]) {

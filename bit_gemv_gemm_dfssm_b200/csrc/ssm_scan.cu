@@ -800,9 +800,12 @@ __global__ void __launch_bounds__(256, 2) scan_state_kernel(const Args a, const 
 
 // Forward calls whose sequences have at most kDirectMean tokens on average take the warp-MMA kernel in one launch, where
 // even one sequence holding all the tokens is not long (kDirectTokens), or not long beside the work there is. Measured,
-// sequences x tokens, 64 heads, one launch against tensor cores behind table and tiles (us): 1 x 1 5.5 / 17,
-// 1 x 128 14 / 18, 1 x 256 25 / 20, 1 x 512 47 / 27, 2 x 256 26 / 21, 4 x 128 20.5 / 27, 4 x 256 37 / 32, 16 x 64 41 / 81,
-// 128 x 8 193 / 512.
+// sequences x tokens, 64 heads from states, calls back to back from a graph, one launch against tensor cores behind table
+// and tiles (us): 1 x 1 5.5 / 16, 1 x 128 14 / 17, 1 x 256 25 / 20, 1 x 512 46 / 27, 2 x 256 25 / 20, 4 x 128 21 / 27, 4 x 256
+// 36 / 32, 9 x 112 39 / 45, 16 x 64 41 / 73, 128 x 8 193 / 485, 128 x 31 244 / 526. The lengths are on the device, so the
+// rule sees their mean: a long sequence beside short ones pays for what the usual calls of that mean gain, 1,000 tokens beside 8
+// single ones 91 / 55, 700 beside 7 of 40 67 / 50, 500 beside 3 single ones 47 / 33 (3,900 beside 127 single ones: 398 / 574, in
+// the last place 551 / 582).
 constexpr int kDirectMean = 128;
 constexpr int kDirectTokens = 1024;
 

@@ -26,7 +26,7 @@
 // 10% faster). Partial dB and dC of the splits and partial parameter sums per chunk are added in order by two
 // small kernels.
 //
-// Measured (4 x 2,048 tokens, 64 heads): 394 to 406 us of the call's 650, the states' kernel 240 to 250. Neither the tensor pipe nor
+// Measured (4 x 2,048 tokens, 64 heads): 394 to 406 us of the call's 651 (back to back from a graph), the states' kernel 240 to 250. Neither the tensor pipe nor
 // shared memory is near its limit (36 and 52 %): a head's chain of products, exchanges and sums between two
 // barriers bounds it, with one CTA per SM (228 KB); left out one at a time, Z and M cost 55 us, dC and dB 80, dx 45,
 // the loads 28. The states alone are 1.1 GB of traffic, 166 us of the HBM's rate.

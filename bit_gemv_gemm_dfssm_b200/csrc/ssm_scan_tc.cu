@@ -19,7 +19,7 @@
 // They meet in mbarriers only, so that the products of one chunk run beside the conversions of the next. Every
 // wait is bounded.
 //
-// Measured (8 sequences, 16,384 tokens, 64 heads): the call 260 us, 4.5 us per chunk and SM, where the products take 20 % of the
+// Measured (8 sequences, 16,384 tokens, 64 heads): the call 269 us back to back from a graph, 4.5 us per chunk and SM, where the products take 20 % of the
 // tensor pipe and 250 MB 12 % of the HBM's rate: the chain G -> M -> Ya -> y and S -> D -> S of one chunk, each step
 // a hand-over between roles, bounds it. Chunks of 64 tokens on warp MMAs took 440 us; one role's loops unrolled
 // further, or twice the warps per role, were slower (instruction fetches; 290 to 320 us).

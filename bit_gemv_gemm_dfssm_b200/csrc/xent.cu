@@ -29,10 +29,11 @@
 // from 1 - p = 2^-12 on (dh then off by its own size at p = 0.9999). exp(l - lse) - 1 is taken from the exact sum
 // in 64 bits, one number per token. Every order is fixed.
 //
-// Measured, 50,288 x 2048. 2,048 tokens: logits 122 to 137 us, 82 to 84 % of the tensor pipe (256 columns of kind::i8 take about
-// 200 cycles per 32 bytes of K); gradient 563 us in three pieces of 56 + 130, 54 % of the tensor pipe in the second, whose
-// bytes-to-fp16 conversion and shared-memory traffic bound it. 1 token: logits 23 us, 4.5 TB/s of the table, the join
-// 6 beside it; 16 tokens: gradient 62 us, the table twice, 23 + 45.
+// Measured, 50,288 x 2048, 20 calls back to back from a graph at 1,965 MHz (some seconds of the 2,048-token calls meet the
+// power cap: 161 us at 1,485 MHz, 665 at 1,650). 2,048 tokens: loss 138 us, of it the logits 122, 82 to 84 % of the tensor
+// pipe (256 columns of kind::i8 take about 200 cycles per 32 bytes of K); gradient 563 us in three pieces of 56 + 130 and 33 at
+// the end, 67 and 54 % of the tensor pipe, the second's bytes-to-fp16 conversion and shared-memory traffic bound it. 1 token:
+// 23 us on a cold table (4.5 TB/s), the join 5 beside it; 16 tokens: gradient 64 us, the table twice, 23 + 45.
 #include <cuda_fp16.h>
 
 #include <cmath>

@@ -361,8 +361,9 @@ dfssm_status dfssm_add_rmsnorm_bwd(const float* norm_w, int32_t d, float eps, co
  * up to 80 MB of fp16 probabilities and, for each such piece of the vocabulary, four to six fp32 partial sums of the
  * tokens x d: it grows with vocab x d (2,048 tokens: 0.27 GB at 50,288 x 2048, 1.4 GB at 256,000 x 4096).
  * Its first 4 bytes are a device error word (DFSSM_DEVERR_TOKEN_ID, DFSSM_DEVERR_TIMEOUT), read and cleared by
- * dfssm_ssm_read_error; nothing else is kept between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call
- * on a device sets kernel attributes (make it before any stream capture). Results repeat bit for bit. */
+ * dfssm_ssm_read_error; nothing else is kept between calls. Calls sharing a workspace must be ordered. Allocates
+ * nothing; the first call on a device sets kernel attributes (make it before any stream capture). Results repeat bit
+ * for bit. */
 #define DFSSM_IGNORE_TARGET (-100)
 dfssm_status dfssm_xent_workspace_bytes(const dfssm_int8_table* table, int32_t m, int32_t backward,
                                         size_t* bytes);
@@ -434,14 +435,17 @@ dfssm_status dfssm_ssm_scan_workspace_bytes(const dfssm_scan_dims* dims, int32_t
  * 2^22, 1 <= nseq <= 65536, (total/128 + nseq) ngroups below 2^23. States are kept in fp32; a sequence is
  * worked on in chunks of 64 or 128 tokens. An Inf or NaN in x, b, c, dt or the initial state makes what it reaches Inf
  * or NaN, and can do so to every channel of its head (of its group, from b and c) in its chunk, in front of it
- * too, and behind it, but not in another sequence. Inside a chunk b and c are rounded to steps of 2^-28 of
- * their group's largest magnitude (exact down to 2^-17 of it), the states' new part to 2^-38 of the largest addend.
- * y overlaps no input.
+ * too, and behind it, but not in another sequence; a dt_raw of -Inf, or of the type's lowest value, is a token that leaves
+ * the state as it is. exp(a_log) dt summed over 128 tokens has to be finite in fp32, in units of log 2. Inside a chunk b
+ * and c are rounded to steps of 2^-28 of their group's largest magnitude (exact down to 2^-17 of it), x to 2^-38 of its
+ * head's, the states' new part to 2^-38 of the largest addend; for y the products C B^T dt and the state are rounded to
+ * fp16 (2^-12 of the value). y overlaps no input.
  * workspace: 256-byte aligned, at least dfssm_ssm_scan_workspace_bytes, zeroed once before its first use.
  * Its first 4 bytes are a device error word (DFSSM_DEVERR_SEQLENS: a sequence whose offsets are negative,
  * descending or beyond total is skipped; DFSSM_DEVERR_TIMEOUT: an in-kernel wait of a forward call gave up), read
- * and cleared by dfssm_ssm_read_error; nothing else is kept between calls. Calls sharing a workspace must be ordered. Allocates nothing; the first call on a device
- * sets kernel attributes (make it before any stream capture). Results repeat bit for bit. */
+ * and cleared by dfssm_ssm_read_error; nothing else is kept between calls. Calls sharing a workspace must be ordered.
+ * Allocates nothing; the first call on a device sets kernel attributes (make it before any stream capture). Results
+ * repeat bit for bit. */
 dfssm_status dfssm_ssm_scan_fwd(const dfssm_scan_dims* dims, const dfssm_scan_inputs* in, int32_t total,
                                 int32_t nseq, void* y, int64_t y_stride, float* final_state, void* workspace,
                                 size_t workspace_bytes, void* stream);

@@ -460,3 +460,17 @@ def test_rows_of_no_sequence_reach_no_result(lens):
     assert torch.equal(y, y2) and torch.equal(fin, fin2) and (y2[~used] == 77).all()
     for k in r:
         assert torch.equal(r[k], r2[k]) and torch.isfinite(r2[k]).all(), k
+
+
+@pytest.mark.parametrize("lens", [[1, 70, 33], [600, 20]])
+def test_tokens_masked_by_the_lowest_step(lens):
+    """dt_raw of -Inf and of the type's lowest value: dt is 0, the state passes, the gradient of dt_raw is 0."""
+    a = inputs(19, lens, 2, 1, True)
+    n = a["total"]
+    a["z"][torch.arange(0, n, 3, device="cuda")] = float("-inf")
+    a["z"][torch.arange(1, n, 7, device="cuda")] = torch.finfo(BF).min
+    y, fin, _ = run_fwd(a)
+    r, _ = run_bwd(a)
+    torch.cuda.synchronize()
+    check_fwd(a, y, fin)
+    check_bwd(a, r)
